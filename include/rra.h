@@ -340,6 +340,63 @@ RRA_API int rra_prefill_step(const void* q, const void* k_new, const void* v_new
                              int T, int Hq, int Hkv, int D, double rope_base, int rope_style, float scale,
                              int32_t* err_flag, void* stream);
 
+/* --- Attention of a batch whose sequences share a long prefix ---
+ *
+ * Sequences that begin with the same tokens (one system prompt, one document, the samples of one
+ * prompt) can map them to the same blocks of a paged cache ([Opt-2026] §四 PagedKVCache). The
+ * decode and verify calls then read those blocks once per sequence; these calls read them once for
+ * the whole batch. The softmax over a row's tokens is that over the prefix and that over the
+ * sequence's own tokens, joined by their maxima and sums ([KVC-GQA-RoPE] §4.2, blockwise softmax):
+ *   out[b, j, h] = softmax(q_rot[b, j, h] . K_b[0 : n]^T * scale) . V_b[0 : n],  n = L_b - gamma + 1 + j
+ * with K_b the prefix's tokens [0, prefix_len) followed by the sequence's own [prefix_len, L_b).
+ *
+ *   q_rot, out      bf16 [B, gamma, Hq, D], gamma 1..16 new tokens per sequence (1: a decode step)
+ *   k_pool, v_pool  bf16 [num_blocks, block_size, Hkv, D], block_size a power of two >= 8
+ *   prefix_blocks   int32 [prefix_len / block_size]: the prefix's blocks in order (a row of a block
+ *                   table will do; may be NULL when prefix_len is 0)
+ *   prefix_len      a multiple of block_size, at most max_blocks_per_seq * block_size. Every prefix
+ *                   token has to be written.
+ *   block_table     int32 [B, max_blocks_per_seq] as in the other calls. Entries before prefix_len /
+ *                   block_size are not read.
+ *   seq_lens        int32 [B]: L_b, the prefix and the gamma new tokens included. Query token j attends
+ *                   the first L_b - gamma + 1 + j tokens; where that is not positive the row is zero
+ *                   (L_b = 0 for a padding row). L_b may lie inside the prefix.
+ *   num_splits      splits of the sequences' own tokens, prefix_splits chunks of the prefix; 0 = chosen
+ *                   by the library. With prefix_splits 0 and a prefix too short to pay for its
+ *                   own pass, one kernel reads prefix and own tokens together (prefix chunks 0).
+ *   workspace       of rra_shared_prefix_plan's bytes, zero-filled before its first use. Calls of any
+ *                   shapes may take turns on one (its counters have the same place for all of them);
+ *                   calls sharing it must not overlap on the GPU.
+ * Other arguments, error bits and statuses as in rra_verify_attn; RRA_EUNSUPPORTED where prefix_len
+ * is not a multiple of block_size, RRA_ERANGE above 448 partials per row (own splits + prefix chunks)
+ * or 262144 groups of up to 16 rows (sequences x KV heads x head slices).
+ */
+RRA_API int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_pool,
+                                   const int32_t* prefix_blocks, int prefix_len, const int32_t* block_table,
+                                   int max_blocks_per_seq, const int32_t* seq_lens, int block_size, int num_blocks,
+                                   void* out, int B, int gamma, int Hq, int Hkv, int D, float scale, int num_splits,
+                                   int prefix_splits, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                                   void* stream);
+
+/* The whole step: RoPE and append of the gamma new tokens at positions[b] .. positions[b] + gamma - 1
+ * (rra_rope_append_verify), then the attention with L_b = positions[b] + gamma. positions[b] must be at
+ * least prefix_len: tokens below it would land in the shared blocks. They are not written, set
+ * RRA_ERR_POSITION and leave that sequence's output unwritten, as positions past the cache do. q_out
+ * receives q_rot and must not overlap q. */
+RRA_API int rra_shared_prefix_step(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                                   void* q_out, void* k_pool, void* v_pool, const int32_t* prefix_blocks,
+                                   int prefix_len, const int32_t* block_table, int max_blocks_per_seq, int block_size,
+                                   int num_blocks, void* out, int B, int gamma, int Hq, int Hkv, int D,
+                                   double rope_base, int rope_style, float scale, int num_splits, int prefix_splits,
+                                   void* workspace, size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/* The effective own splits and prefix chunks of these calls (any of the three pointers may be NULL)
+ * and their workspace bytes; a negative rra_status on bad arguments. Queries the current device's
+ * SM count. */
+RRA_API int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq,
+                                   int block_size, int num_splits, int prefix_splits, int* own_splits,
+                                   int* prefix_chunks, size_t* workspace_bytes);
+
 /* Bytes of a K+V cache: 2 * n_layers * n_kv_heads * head_dim * seq_len * batch * dtype_bytes
  * ([Opt-2026] §四 memory formula; [KVC-GQA-RoPE] §5.3). Host only; returns 0 when an
  * argument is negative or the product overflows 64 bits. */

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   const int pos = a.positions[b] + j_new;
   const bool paged = a.block_table != nullptr;
   const long long cap = paged ? (static_cast<long long>(a.max_blocks_per_seq) << a.log2_bs) : a.max_len;
-  if (pos < 0 || pos >= cap) {
+  if (pos < a.min_pos || pos >= cap) {
     if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, RRA_ERR_POSITION);
     return;
   }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_rows_kernel(const Ro
   const int pos = a.positions[b] + j_new;
   const bool paged = a.block_table != nullptr;
   const long long cap = paged ? (static_cast<long long>(a.max_blocks_per_seq) << a.log2_bs) : a.max_len;
-  if (pos < 0 || pos >= cap) {
+  if (pos < a.min_pos || pos >= cap) {
     if (threadIdx.x == 0) flag_error(a.err, RRA_ERR_POSITION);
     return;
   }

@@ -269,6 +269,77 @@ int check_prefill_limits(int T, int Hq, int Hkv, int64_t capacity) {
   return RRA_OK;
 }
 
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Shared-prefix attention: the plan of the sequences' own tokens (the verify kernel's) and the
+// chunks of the prefix.
+struct SharedPlan {
+  Plan own;
+  int prefix_splits = 0;  // 0: no separate pass, the own-token kernel reads the prefix too
+  int prefix_chunk = 0;
+};
+
+// Most partials (prefix chunks + own splits) one merge takes: two weights per partial of its 16 rows
+// in the merging CTA's 64 KB ring.
+constexpr int kSharedMaxPartials = 448;
+
+int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq, int block_size,
+                     int num_splits, int prefix_splits, SharedPlan* p) {
+  if (!pow2(block_size)) return block_size <= 0 ? RRA_EINVAL : RRA_EUNSUPPORTED;
+  if (max_blocks_per_seq < 1 || prefix_len < 0 || prefix_splits < 0) return RRA_EINVAL;
+  const int64_t capacity = int64_t(max_blocks_per_seq) * block_size;
+  if (prefix_len > capacity) return RRA_EINVAL;
+  if (prefix_len % block_size != 0) return RRA_EUNSUPPORTED;
+  int st = make_plan_verify(B, gamma, Hq, Hkv, D, capacity, block_size, num_splits, &p->own);
+  if (st != RRA_OK) return st;
+  const int64_t rows = int64_t(B) * gamma * (Hq / Hkv);
+  const bool pass = prefix_len > 0 && rows > 0 && (prefix_splits > 0 || (B > 1 && prefix_len >= 256));
+  if (pass) {
+    const int tile = 8192 / D;
+    const int64_t tiles = (prefix_len + tile - 1) / tile;
+    const int64_t row_tiles = (rows + rra::kSharedPrefixRows - 1) / rra::kSharedPrefixRows;
+    const int64_t max_chunk = std::max<int64_t>(1, int64_t(rra::kSharedPrefixTableEntries) * block_size / tile);
+    if (Hkv > 65535) return RRA_ERANGE;
+    const int64_t resident = 2 * int64_t(std::max(1, sm_count()));
+    int64_t best = 0, best_cost = INT64_MAX;
+    // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
+    const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
+    const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, 40);
+    for (int64_t s = lo; s <= hi; ++s) {
+      const int64_t chunk = std::min((tiles + s - 1) / s, max_chunk), n = (tiles + chunk - 1) / chunk;
+      const int64_t waves = (Hkv * row_tiles * n + resident - 1) / resident;
+      const int64_t cost = waves * (chunk + 6);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = chunk;
+      }
+    }
+    p->prefix_chunk = static_cast<int>(best * tile);
+    p->prefix_splits = static_cast<int>((tiles + best - 1) / best);
+    st = plan_splits(B, Hkv, Hq / Hkv, capacity - prefix_len, block_size, num_splits, &p->own);
+    if (st != RRA_OK) return st;
+  }
+  return p->prefix_splits + p->own.splits > kSharedMaxPartials ? RRA_ERANGE : RRA_OK;
+}
+
+// Workspace of shared-prefix attention: arrival counters, one per 16 rows, in a first part of the same
+// size for every shape (so that calls of different shapes, captured or not, may take turns on one
+// workspace), then partials o [R, S, D] and (max, sum) [R, S, 2] floats (S = prefix chunks + own
+// splits), 256-byte aligned.
+constexpr size_t kSharedCounterBytes = size_t(1) << 20;
+struct SharedWs {
+  size_t o, ml, total;
+};
+SharedWs shared_ws(int64_t rows, int D, const SharedPlan& p) {
+  const size_t S = size_t(p.prefix_splits) + p.own.splits;
+  SharedWs w{};
+  if (S <= 1 || rows <= 0) return w;
+  w.o = kSharedCounterBytes;
+  w.ml = w.o + align256(rows * S * D * sizeof(float));
+  w.total = w.ml + rows * S * 2 * sizeof(float);
+  return w;
+}
+
 // KV groups per prefill scheduling band: as many as have their prompt's K and V (T x D x 2 x
 // 2 bytes each, bf16) within 64 MB, half of the L2, and divide Hkv; at least one.
 int prefill_kv_band(int T, int Hkv, int D) {
@@ -286,8 +357,6 @@ int64_t verify_rows(int B, int gamma, int Hq, int Hkv) {
 // Workspace layout, each part 256-byte aligned (R = B*Hq, G = merge_groups(splits)):
 // partials o [R, splits, D] and (max, sum) [R, splits, 2] floats, level-2 partials o [R, G, D]
 // and (max, sum) [R, G, 2] floats, counters [R] and group counters [R, G] int32.
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 struct WsLayout {
   size_t o, ml, o2, ml2, cnt, gcnt, total;
 };
@@ -789,10 +858,11 @@ int rra_rope_append(const void* q, const void* k_new, const void* v_new, const i
                                 stream);
 }
 
-int rra_rope_append_verify(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
+// min_pos: tokens at positions below it are refused (the tokens of a shared prefix).
+static int rope_append_launch(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
                            void* k_cache, void* v_cache, const int32_t* block_table, int max_blocks_per_seq,
                            int block_size, int num_blocks, int max_len, int B, int gamma, int Hq, int Hkv, int D,
-                           double rope_base, int rope_style, rra_dtype dt, int32_t* err_flag, void* stream) {
+                           double rope_base, int rope_style, rra_dtype dt, int min_pos, int32_t* err_flag, void* stream) {
   int st = check_shapes(B, Hq, Hkv, D, dt);
   if (st != RRA_OK) return st;
   if (gamma < 1) return RRA_EINVAL;
@@ -829,11 +899,21 @@ int rra_rope_append_verify(const void* q, const void* k_new, const void* v_new, 
   a.Hkv = Hkv;
   a.D = D;
   a.gamma = gamma;
+  a.min_pos = min_pos;
   rra::fill_rope_phi(a.rope_phi, D, rope_base);
   a.rope_style = rope_style;
   a.err = err_flag;
   const cudaError_t e = rra::launch_rope_append(a, dt, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RRA_OK : cuda_fail(e, "rope_append launch");
+}
+
+int rra_rope_append_verify(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
+                           void* k_cache, void* v_cache, const int32_t* block_table, int max_blocks_per_seq,
+                           int block_size, int num_blocks, int max_len, int B, int gamma, int Hq, int Hkv, int D,
+                           double rope_base, int rope_style, rra_dtype dt, int32_t* err_flag, void* stream) {
+  return rope_append_launch(q, k_new, v_new, positions, q_out, k_cache, v_cache, block_table, max_blocks_per_seq,
+                            block_size, num_blocks, max_len, B, gamma, Hq, Hkv, D, rope_base, rope_style, dt, 0,
+                            err_flag, stream);
 }
 
 int rra_decode_attn_contig(const void* q_rot, const void* k_cache, const void* v_cache, const int32_t* seq_lens,
@@ -1204,6 +1284,115 @@ int rra_prefill_step(const void* q, const void* k_new, const void* v_new, const 
   if (st != RRA_OK) return st;
   return rra_prefill_attn(q_out, k_cache, v_cache, block_table, max_blocks_per_seq, positions, block_size, num_blocks,
                           max_len, out, B, T, Hq, Hkv, D, scale, err_flag, stream);
+}
+
+// Checks and launch shared by the shared-prefix entry points; positions or seq_lens is given.
+static int shared_prefix_launch(const void* q_rot, const void* k_pool, const void* v_pool, const int32_t* prefix_blocks,
+                                int prefix_len, const int32_t* block_table, int max_blocks_per_seq,
+                                const int32_t* seq_lens, const int32_t* positions, int block_size, int num_blocks,
+                                void* out, int B, int gamma, int Hq, int Hkv, int D, float scale, int num_splits,
+                                int prefix_splits, void* workspace, size_t ws_bytes, int32_t* err_flag, void* stream,
+                                bool check_only) {
+  SharedPlan p;
+  int st = make_plan_shared(B, gamma, Hq, Hkv, D, prefix_len, max_blocks_per_seq, block_size, num_splits, prefix_splits,
+                            &p);
+  if (st != RRA_OK) return st;
+  if (num_blocks < 1 || !std::isfinite(scale)) return RRA_EINVAL;
+  if (B == 0) return RRA_OK;
+  if (!q_rot || !k_pool || !v_pool || !block_table || (!seq_lens && !positions) || !out) return RRA_EINVAL;
+  if (prefix_len > 0 && !prefix_blocks) return RRA_EINVAL;
+  if (!aligned16(q_rot) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return RRA_EINVAL;
+  const int64_t rows = verify_rows(B, gamma, Hq, Hkv);
+  if (rows > int64_t(16 * kSharedCounterBytes / sizeof(int))) return RRA_ERANGE;
+  const SharedWs w = shared_ws(rows, D, p);
+  if (w.total > 0 && (workspace == nullptr || ws_bytes < w.total || !aligned16(workspace))) return RRA_EWORKSPACE;
+  if (check_only) return RRA_OK;
+  CUtensorMap km, vm;
+  const int box_rows = block_size < p.own.tile ? block_size : p.own.tile;
+  st = encode_pool_map(&km, k_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
+  if (st == RRA_OK) st = encode_pool_map(&vm, v_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
+  if (st != RRA_OK) return st;
+  rra::DecodeArgs a{};
+  a.q = q_rot;
+  a.k = k_pool;
+  a.v = v_pool;
+  a.seq_lens = seq_lens;
+  a.positions = positions;
+  a.block_table = block_table;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.log2_bs = ilog2(block_size);
+  a.num_blocks = num_blocks;
+  a.out = out;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  a.counters = reinterpret_cast<int*>(base);
+  a.ws_o = reinterpret_cast<float*>(base + w.o);
+  a.ws_ml = reinterpret_cast<float*>(base + w.ml);
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.gamma = gamma;
+  a.hpc = p.own.hpc;
+  a.capacity = max_blocks_per_seq * block_size;
+  a.num_splits = p.prefix_splits + p.own.splits;
+  a.chunk = p.own.chunk;
+  a.prefix_blocks = prefix_blocks;
+  a.prefix_len = prefix_len;
+  a.prefix_splits = p.prefix_splits;
+  a.prefix_chunk = p.prefix_chunk;
+  a.first_token = p.prefix_splits > 0 ? prefix_len : 0;
+  const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
+  a.scale_log2 = s * 1.4426950408889634f;
+  a.err = err_flag;
+  return finish_decode(rra::launch_shared_prefix(a, km, vm, static_cast<cudaStream_t>(stream)));
+}
+
+int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq,
+                           int block_size, int num_splits, int prefix_splits, int* own_splits, int* prefix_chunks,
+                           size_t* workspace_bytes) {
+  SharedPlan p;
+  const int st = make_plan_shared(B, gamma, Hq, Hkv, D, prefix_len, max_blocks_per_seq, block_size, num_splits,
+                                  prefix_splits, &p);
+  if (st != RRA_OK) return st;
+  const int64_t rows = verify_rows(B, gamma, Hq, Hkv);
+  if (rows > int64_t(16 * kSharedCounterBytes / sizeof(int))) return RRA_ERANGE;
+  if (own_splits != nullptr) *own_splits = p.own.splits;
+  if (prefix_chunks != nullptr) *prefix_chunks = p.prefix_splits;
+  if (workspace_bytes != nullptr) *workspace_bytes = shared_ws(rows, D, p).total;
+  return RRA_OK;
+}
+
+int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_pool, const int32_t* prefix_blocks,
+                           int prefix_len, const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                           int block_size, int num_blocks, void* out, int B, int gamma, int Hq, int Hkv, int D,
+                           float scale, int num_splits, int prefix_splits, void* workspace, size_t ws_bytes,
+                           int32_t* err_flag, void* stream) {
+  return shared_prefix_launch(q_rot, k_pool, v_pool, prefix_blocks, prefix_len, block_table, max_blocks_per_seq,
+                              seq_lens, nullptr, block_size, num_blocks, out, B, gamma, Hq, Hkv, D, scale, num_splits,
+                              prefix_splits, workspace, ws_bytes, err_flag, stream, false);
+}
+
+int rra_shared_prefix_step(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
+                           void* k_pool, void* v_pool, const int32_t* prefix_blocks, int prefix_len,
+                           const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks, void* out,
+                           int B, int gamma, int Hq, int Hkv, int D, double rope_base, int rope_style, float scale,
+                           int num_splits, int prefix_splits, void* workspace, size_t ws_bytes, int32_t* err_flag,
+                           void* stream) {
+  // every check of both parts first, so that nothing is enqueued when one would refuse
+  int st = shared_prefix_launch(q_out, k_pool, v_pool, prefix_blocks, prefix_len, block_table, max_blocks_per_seq,
+                                nullptr, positions, block_size, num_blocks, out, B, gamma, Hq, Hkv, D, scale,
+                                num_splits, prefix_splits, workspace, ws_bytes, err_flag, stream, true);
+  if (st != RRA_OK) return st;
+  st = check_step_args(q, k_new, v_new, positions, q_out, k_pool, v_pool, out, B * gamma, Hq, D, rope_base, rope_style,
+                       scale, RRA_BF16);
+  if (st != RRA_OK || B == 0) return st;
+  st = rope_append_launch(q, k_new, v_new, positions, q_out, k_pool, v_pool, block_table, max_blocks_per_seq,
+                          block_size, num_blocks, 0, B, gamma, Hq, Hkv, D, rope_base, rope_style, RRA_BF16, prefix_len,
+                          err_flag, stream);
+  if (st != RRA_OK) return st;
+  return shared_prefix_launch(q_out, k_pool, v_pool, prefix_blocks, prefix_len, block_table, max_blocks_per_seq,
+                              nullptr, positions, block_size, num_blocks, out, B, gamma, Hq, Hkv, D, scale, num_splits,
+                              prefix_splits, workspace, ws_bytes, err_flag, stream, false);
 }
 
 }  // extern "C"

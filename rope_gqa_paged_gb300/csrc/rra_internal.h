@@ -29,6 +29,7 @@ struct RopeArgs {
   int rope_style;
   int32_t* err;
   int gamma;                    // new tokens per sequence (0 or 1: one); q/k_new/v_new/q_out [B*gamma, H, D]
+  int min_pos;                  // bf16 / fp32 caches: positions below it are refused (the tokens of a shared prefix)
   // INT8 caches only: k_cache / v_cache hold int8 codes, quantised with these per-KV-head
   // scales; with window > 0 the bf16 values also go to ring slot pos % window.
   const float* k_scale;
@@ -89,6 +90,15 @@ struct DecodeArgs {
   // Speculative verify (verify.cuh): gamma new tokens per sequence at positions[b] ..
   // positions[b] + gamma - 1; q and out are [B, gamma, Hq, D].
   int gamma;
+  // Shared prefix (shared_prefix.cuh, verify.cuh): the first prefix_len tokens of every sequence are
+  // in prefix_blocks. With prefix_splits > 0 their attention is computed for all rows at once, in
+  // chunks of prefix_chunk tokens whose partials fill slots [0, prefix_splits) of num_splits; the
+  // sequences' own tokens start at first_token (prefix_len, or 0 when prefix_splits is 0).
+  const int32_t* prefix_blocks;
+  int prefix_len;
+  int prefix_splits;
+  int prefix_chunk;
+  int first_token;
   // Prefill: CTAs run band by band, a band being kv_band KV groups (0: all of them) whose keys
   // and values fit in L2 together, longest query blocks first within a band.
   int kv_band;
@@ -185,6 +195,12 @@ cudaError_t launch_decode_verify(const DecodeArgs& a, const CUtensorMap& k_map, 
                                  bool fused, cudaStream_t stream);
 // Largest gamma of the one-launch verify step.
 constexpr int kVerifyFusedMaxGammaHost = 8;
+// Shared-prefix attention (a.seq_lens or a.positions, the prefix fields, a.gamma, a.hpc set): query rows
+// of one prefix CTA, and the most prefix blocks of one chunk.
+constexpr int kSharedPrefixRows = 128;
+constexpr int kSharedPrefixTableEntries = 2048;
+cudaError_t launch_shared_prefix(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                 cudaStream_t stream);
 // Prefill: causal attention of the T = a.gamma prompt tokens of each sequence (a.positions: the
 // first one's position); 64 query rows (a.hpc heads x 64 / a.hpc tokens) per CTA.
 cudaError_t launch_prefill(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, bool paged,

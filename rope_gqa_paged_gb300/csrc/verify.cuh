@@ -215,6 +215,36 @@ struct VerifyRows {
   }
 };
 
+// Shared prefix: the partial row of new token j, head i of KV head g's group, of sequence b (the
+// inverse of VerifyRows).
+struct SharedRows {
+  int Hkv, n_rep, hpc, gamma;
+  __device__ size_t operator()(int b, int g, int i, int j) const {
+    const int slice = i / hpc;
+    return ((static_cast<size_t>(b) * Hkv + g) * (n_rep / hpc) + slice) * kVerifyRows + (i - slice * hpc) * gamma + j;
+  }
+};
+
+// Shared prefix: waits for the prefix's partials, then merges them with the n_work partials of the
+// sequence's own chunks (slots [0, prefix_splits + n_work) of its rows) into the output; zero rows
+// where there is none. Called by all nthreads consumer threads of one CTA of the rows.
+template <int D>
+__device__ __forceinline__ void merge_shared(const DecodeArgs& a, size_t row0, int rows, int n_work, uint8_t* ring,
+                                             int ring_bytes, VerifyRows out_row, int nthreads) {
+  const int tid = threadIdx.x, count = a.prefix_splits + n_work;
+  if (count == 0) {
+    for (int i = tid; i < rows * D; i += nthreads)
+      static_cast<__nv_bfloat16*>(a.out)[out_row(row0 + i / D) * D + i % D] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  pdl_wait();
+  float* scratch = reinterpret_cast<float*>(ring);
+  if (!merge_partials_bulk<__nv_bfloat16, D>(a, a.ws_o, a.ws_ml, a.num_splits, 0, count, rows, row0, nullptr, nullptr,
+                                             0, 0, scratch, ring_bytes, tid, nthreads, out_row))
+    merge_partials<__nv_bfloat16, D, VerifyRows, false>(a, a.ws_o, a.ws_ml, a.num_splits, 0, count, rows, row0, nullptr,
+                                                        nullptr, 0, 0, scratch, tid, nthreads, out_row);
+}
+
 // FUSED: the whole verify step in this launch. a.q holds the unrotated q of the gamma new tokens
 // (gamma <= kVerifyFusedMaxGamma); the consumer warps take sin/cos of the gamma positions once per
 // CTA (rope_cos_sin, as the decode step), rotate their query rows in registers, and split-0
@@ -222,7 +252,14 @@ struct VerifyRows {
 // v_new into the cache, one warp per token, and its producer waits for those writes (an mbarrier
 // with one arrival per token) before the TMA of the first tile that holds a new token. Head-slice
 // CTAs of that chunk write identical bytes.
-template <int D, bool PAGED, bool FUSED = false>
+//
+// SHARED: the sequences' own tokens of shared-prefix attention, [first_token, L_b). The kernel
+// before it (shared_prefix.cuh) may still be computing the prefix's partials: this one reads only
+// what that kernel's predecessors wrote (past L1; that kernel let it start after it had waited for
+// them) and waits for it before the merge, which the last split of a sequence's rows makes of the
+// prefix's partials and its own, in one level. Lengths may be given (seq_lens; query token j attends
+// the first L_b - gamma + 1 + j tokens, none if that is not positive: a zero row).
+template <int D, bool PAGED, bool FUSED = false, bool SHARED = false>
 __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     decode_verify_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
@@ -244,20 +281,41 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
   const VerifyRows out_row{a.Hq, a.Hkv, n_rep, slices, hpc, gamma};
 
   pdl_launch_dependents();
-  pdl_wait();  // the kernel before this one (the append, or the previous step) has finished
+  if (!SHARED || a.prefix_splits == 0) pdl_wait();  // the kernel before this one (the append, or the previous step) has finished
+  const int start = (SHARED ? a.first_token : 0) + split * a.chunk;
   // the chunk's block ids load alongside the position
   ChunkBlockIds<(kMmaTableEntries + C::kThreads - 1) / C::kThreads> pre_ids;
-  if constexpr (PAGED) pre_ids.load(a, b, (split * a.chunk) >> a.log2_bs, threadIdx.x, C::kThreads);
+  if constexpr (SHARED) pre_ids.load_shared(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
+  else if constexpr (PAGED) pre_ids.load(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
 
-  const int p0 = a.positions[b];
-  int L = p0 + gamma;
-  if (p0 < 0 || L > a.capacity) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
-    return;
+  int p0, L;
+  if (SHARED && a.positions == nullptr) {
+    L = __ldcg(a.seq_lens + b);
+    if (L < 0 || L > a.capacity) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_SEQ_LEN);
+      L = min(max(L, 0), a.capacity);
+    }
+    p0 = L - gamma;  // token j attends [0, p0 + j], which may be empty
+  } else {
+    p0 = SHARED ? __ldcg(a.positions + b) : a.positions[b];
+    L = p0 + gamma;
+    if (p0 < (SHARED ? a.prefix_len : 0) || L > a.capacity) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
+      if (SHARED) pdl_wait();  // this kernel does not end before the one before it
+      return;
+    }
   }
-  const int start = split * a.chunk;
-  const int n_work = (L + a.chunk - 1) / a.chunk;
-  if (start >= L) return;
+  const int n_work = SHARED ? max(L - a.first_token + a.chunk - 1, 0) / a.chunk : (L + a.chunk - 1) / a.chunk;
+  if constexpr (SHARED) {
+    if (split >= max(n_work, 1)) return;
+    if (n_work == 0) {  // no token of its own: the prefix's partials alone (zero rows without any)
+      if (threadIdx.x < C::kConsumerWarps * 32)
+        merge_shared<D>(a, vbase, rows, 0, smem, C::kRingBytes, out_row, C::kConsumerWarps * 32);
+      return;
+    }
+  } else {
+    if (start >= L) return;
+  }
   const int end = min(L, start + a.chunk);
   const int n_tiles = (end - start + C::kTile - 1) / C::kTile;
   // fused step: new tokens app_lo .. app_hi - 1 lie in this chunk and are appended here
@@ -296,6 +354,7 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
     }
+    if constexpr (SHARED) asm volatile("fence.proxy.async.global;" ::: "memory");  // the append's writes, for the copies
     int issued = 0;
     for (int it = 0; it < n_tiles; ++it) {
       const int s = it % C::kStages;
@@ -361,8 +420,13 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
         static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<size_t>(b) * gamma + j) * a.Hq + h0 + hh) * D);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      qa[kk][i] = r < rows ? q[kk * 8 + t] : 0u;
-      qa[kk][2 + i] = r < rows ? q[kk * 8 + 4 + t] : 0u;
+      if constexpr (SHARED) {
+        qa[kk][i] = r < rows ? __ldcg(q + kk * 8 + t) : 0u;
+        qa[kk][2 + i] = r < rows ? __ldcg(q + kk * 8 + 4 + t) : 0u;
+      } else {
+        qa[kk][i] = r < rows ? q[kk * 8 + t] : 0u;
+        qa[kk][2 + i] = r < rows ? q[kk * 8 + 4 + t] : 0u;
+      }
     }
   }
   if constexpr (FUSED) {
@@ -510,10 +574,10 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
 #pragma unroll
     for (int w = 0; w < C::kConsumerWarps; ++w)
       osum = fmaf(red_w[w * kVerifyRows + r], red_o[(w * kVerifyRows + r) * kRS + d], osum);
-    if (n_work == 1) {
+    if (n_work == 1 && (!SHARED || a.prefix_splits == 0)) {
       static_cast<__nv_bfloat16*>(a.out)[out_row(vbase + r) * D + d] = __float2bfloat16_rn(lsum > 0.f ? osum / lsum : 0.f);
     } else {
-      const size_t ps = (vbase + r) * a.num_splits + split;
+      const size_t ps = (vbase + r) * a.num_splits + (SHARED ? a.prefix_splits : 0) + split;
       a.ws_o[ps * D + d] = osum;
       if (d == 0) {
         a.ws_ml[2 * ps] = Mx;
@@ -521,7 +585,12 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
       }
     }
   }
-  if (n_work > 1) {
+  if constexpr (SHARED) {
+    __shared__ int s_last;
+    if (n_work + a.prefix_splits > 1 &&
+        arrive_last(a.counters + vbase / kVerifyRows, n_work, &s_last, a.err, threadIdx.x, kConsumers))
+      merge_shared<D>(a, vbase, rows, n_work, smem, C::kRingBytes, out_row, kConsumers);
+  } else if (n_work > 1) {
     __shared__ int s_last;
     finish_split_rows<__nv_bfloat16, D, VerifyRows, false>(a, vbase, rows, split, n_work,
                                                            reinterpret_cast<float*>(smem), &s_last, threadIdx.x,
@@ -529,16 +598,17 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
   }
 }
 
-template <int D, bool PAGED, bool FUSED>
+template <int D, bool PAGED, bool FUSED, bool SHARED = false>
 cudaError_t launch_decode_verify_t(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                                    cudaStream_t st) {
   using C = MmaCfg<D>;
   constexpr int kSmem = verify_smem_bytes<D>(FUSED);
   static int done[64] = {0};
-  auto kern = decode_verify_kernel<D, PAGED, FUSED>;
+  auto kern = decode_verify_kernel<D, PAGED, FUSED, SHARED>;
   cudaError_t e = ensure_smem(kern, kSmem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.num_splits * ((a.Hq / a.Hkv) / a.hpc), a.Hkv, a.B);
+  const int splits = SHARED ? a.num_splits - a.prefix_splits : a.num_splits;
+  const dim3 grid(splits * ((a.Hq / a.Hkv) / a.hpc), a.Hkv, a.B);
   return launch_pdl(kern, grid, dim3(C::kThreads), kSmem, st, km, vm, a);
 }
 

@@ -71,6 +71,13 @@ _SIGNATURES = {
                                   _c_int, _c_int, _c_int, _c_f32, _vp, _vp]),
     "rra_prefill_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp,
                                   _c_int, _c_int, _c_int, _c_int, _c_int, _c_f64, _c_int, _c_f32, _vp, _vp]),
+    "rra_shared_prefix_attn": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp, _c_int,
+                                        _c_int, _c_int, _c_int, _c_int, _c_f32, _c_int, _c_int, _vp, _c_size, _vp,
+                                        _vp]),
+    "rra_shared_prefix_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                        _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f64, _c_int, _c_f32, _c_int,
+                                        _c_int, _vp, _c_size, _vp, _vp]),
+    "rra_shared_prefix_plan": (_c_int, [_c_int] * 10 + [_vp, _vp, _vp]),
 }
 
 
@@ -125,13 +132,18 @@ def _ptr(t: Optional[torch.Tensor]):
 _device_of_thread = threading.local()
 
 
-def _stream(stream, t: torch.Tensor) -> Optional[int]:
-    """The stream handle for a call on tensor ``t``'s device (selecting that device in the
-    library when the call runs on the default stream, which carries no device)."""
+def use_device_of(t: torch.Tensor) -> None:
+    """Selects tensor ``t``'s device in the library for this thread."""
     dev = t.device.index if t.device.index is not None else torch.cuda.current_device()
     if getattr(_device_of_thread, "dev", None) != dev:
         _check("rra_use_device", lib().rra_use_device(dev))
         _device_of_thread.dev = dev
+
+
+def _stream(stream, t: torch.Tensor) -> Optional[int]:
+    """The stream handle for a call on tensor ``t``'s device (selecting that device in the
+    library when the call runs on the default stream, which carries no device)."""
+    use_device_of(t)
     if stream is None:
         return torch.cuda.current_stream(t.device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -408,6 +420,77 @@ def rra_verify_step(q, k_new, v_new, positions, q_out, k_cache, v_cache, out, bl
                                D, float(rope_base), int(rope_style), float(scale), int(num_splits), _ptr(workspace),
                                ws_bytes, _ptr(err_flag), _stream(stream, q))
     _check("rra_verify_step", st)
+
+
+# --------------------------------------------------------------------------- shared prefix
+def _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len: int, block_table, lens, out):
+    """(B, gamma, Hq, D) of the new tokens' queries; [B, Hq, D] is one new token per sequence. The C
+    calls take no element types, so they are checked here, with the shapes."""
+    if q.dim() == 4:
+        B, gamma, Hq, D = q.shape
+    elif q.dim() == 3:
+        (B, Hq, D), gamma = q.shape, 1
+    else:
+        raise ValueError("q: [B, gamma, Hq, D] or [B, Hq, D]")
+    if not (q.dtype == k_pool.dtype == v_pool.dtype == out.dtype == torch.bfloat16):
+        raise TypeError("shared-prefix attention takes bf16 queries, caches and outputs")
+    if block_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise TypeError("block_table, seq_lens and positions are int32")
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or k_pool.shape[3] != D or out.shape != q.shape:
+        raise ValueError("k_pool and v_pool: [num_blocks, block_size, Hkv, D]; out: the shape of q")
+    if block_table.dim() != 2 or block_table.shape[0] != B or lens.numel() != B:
+        raise ValueError("block_table: [B, max_blocks_per_seq]; one length or position per sequence")
+    if prefix_len > 0 and (prefix_blocks is None or prefix_blocks.dtype != torch.int32 or
+                           prefix_blocks.numel() * k_pool.shape[1] < prefix_len):
+        raise ValueError("prefix_blocks: int32, a block for every block_size tokens of the prefix")
+    return B, gamma, Hq, D
+
+
+def rra_shared_prefix_plan(B: int, gamma: int, Hq: int, Hkv: int, D: int, prefix_len: int, max_blocks_per_seq: int,
+                           block_size: int, num_splits: int = 0, prefix_splits: int = 0) -> tuple:
+    """(splits of the sequences' own tokens, prefix chunks, workspace bytes) of the shared-prefix calls."""
+    own, chunks, ws = ctypes.c_int(), ctypes.c_int(), ctypes.c_size_t()
+    _check("rra_shared_prefix_plan",
+           lib().rra_shared_prefix_plan(B, gamma, Hq, Hkv, D, prefix_len, max_blocks_per_seq, block_size, num_splits,
+                                        prefix_splits, ctypes.byref(own), ctypes.byref(chunks), ctypes.byref(ws)))
+    return own.value, chunks.value, ws.value
+
+
+def rra_shared_prefix_attn(q_rot, k_pool, v_pool, prefix_blocks, prefix_len: int, block_table, seq_lens, out,
+                           scale: float = 0.0, num_splits: int = 0, prefix_splits: int = 0, workspace=None,
+                           err_flag=None, stream=None) -> None:
+    """out[b, j] = attention of q_rot[b, j] over the first seq_lens[b] - gamma + 1 + j tokens, of which the
+    first prefix_len are in prefix_blocks for every sequence (read once for the batch)."""
+    B, gamma, Hq, D = _shared_layout(q_rot, k_pool, v_pool, prefix_blocks, prefix_len, block_table, seq_lens, out)
+    num_blocks, block_size, Hkv = k_pool.shape[:3]
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib().rra_shared_prefix_attn(_ptr(q_rot), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_blocks), int(prefix_len),
+                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens), block_size, num_blocks,
+                                      _ptr(out), B, gamma, Hq, Hkv, D, float(scale), int(num_splits),
+                                      int(prefix_splits), _ptr(workspace), ws_bytes, _ptr(err_flag),
+                                      _stream(stream, q_rot))
+    _check("rra_shared_prefix_attn", st)
+
+
+def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, prefix_blocks, prefix_len: int,
+                           block_table, out, rope_base: float = 10000.0, rope_style: int = 0, scale: float = 0.0,
+                           num_splits: int = 0, prefix_splits: int = 0, workspace=None, err_flag=None,
+                           stream=None) -> None:
+    """RoPE + append of the gamma new tokens at positions[b] (at least prefix_len), then their attention."""
+    B, gamma, Hq, D = _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len, block_table, positions, out)
+    num_blocks, block_size, Hkv = k_pool.shape[:3]
+    if not (k_new.dtype == v_new.dtype == q_out.dtype == torch.bfloat16):
+        raise TypeError("shared-prefix attention takes bf16 new tokens")
+    if k_new.numel() != B * gamma * Hkv * D or v_new.shape != k_new.shape or q_out.shape != q.shape:
+        raise ValueError("k_new and v_new: [B, gamma, Hkv, D]; q_out: the shape of q")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = lib().rra_shared_prefix_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q_out), _ptr(k_pool),
+                                      _ptr(v_pool), _ptr(prefix_blocks), int(prefix_len), _ptr(block_table),
+                                      block_table.shape[1], block_size, num_blocks, _ptr(out), B, gamma, Hq, Hkv, D,
+                                      float(rope_base), int(rope_style), float(scale), int(num_splits),
+                                      int(prefix_splits), _ptr(workspace), ws_bytes, _ptr(err_flag),
+                                      _stream(stream, q))
+    _check("rra_shared_prefix_step", st)
 
 
 # --------------------------------------------------------------------------- prefill

@@ -226,6 +226,58 @@ class VerifyStep(DecodeStep):
         return self.attend(positions, stream)
 
 
+class SharedPrefixStep(VerifyStep):
+    """The step of a batch whose sequences share their first ``prefix_len`` tokens: gamma new tokens
+    per sequence (1: decode) over a bf16 paged pool, the prefix read once for the whole batch.
+
+    ``prefix_blocks`` (int32) lists the prefix's blocks in order; ``block_table`` rows hold the
+    sequences' own blocks from column prefix_len / block_size on (what stands before is not read).
+    q / k_new / v_new are [B, gamma, H, D] and ``positions[b]`` is the first new token's position.
+    ``seq_lens`` given to a call replaces positions + gamma as the attended lengths (two calls: append,
+    then attention); a length of 0 marks a padding row.
+    """
+
+    def __init__(self, batch: int, gamma: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 k_pool: torch.Tensor, v_pool: torch.Tensor, prefix_blocks: Optional[torch.Tensor], prefix_len: int,
+                 block_table: torch.Tensor, num_splits: int = 0, prefix_splits: int = 0, rope_base: float = 10000.0,
+                 rope_style: int = 0, scale: float = 0.0):
+        self.B, self.gamma, self.Hq, self.Hkv, self.D = batch, gamma, n_q_heads, n_kv_heads, head_dim
+        self.k_cache, self.v_cache, self.block_table = k_pool, v_pool, block_table
+        self.prefix_blocks, self.prefix_len = prefix_blocks, prefix_len
+        self.rope_base, self.rope_style, self.scale = rope_base, rope_style, scale
+        self.dtype, dev = k_pool.dtype, k_pool.device
+        self.num_splits, self.prefix_splits = num_splits, prefix_splits
+        rra.use_device_of(k_pool)  # the plan depends on the device's SM count
+        self.splits, self.prefix_chunks, ws = rra.rra_shared_prefix_plan(
+            batch, gamma, n_q_heads, n_kv_heads, head_dim, prefix_len, block_table.shape[1], k_pool.shape[1],
+            num_splits, prefix_splits)
+        self.workspace = torch.zeros(ws, dtype=torch.uint8, device=dev) if ws else None  # zeroed once
+        self.q_rot = torch.empty(batch, gamma, n_q_heads, head_dim, dtype=self.dtype, device=dev)
+        self.out = torch.empty(batch, gamma, n_q_heads, head_dim, dtype=self.dtype, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.graph = None
+
+    def attend(self, seq_lens, stream=None) -> torch.Tensor:
+        """Attention of the already-appended gamma tokens over ``seq_lens`` tokens (they included)."""
+        rra.rra_shared_prefix_attn(self.q_rot, self.k_cache, self.v_cache, self.prefix_blocks, self.prefix_len,
+                                   self.block_table, seq_lens, self.out, self.scale, self.num_splits,
+                                   self.prefix_splits, self.workspace, self.err, stream)
+        return self.out
+
+    def fused(self, q, k_new, v_new, positions, stream=None) -> torch.Tensor:
+        rra.rra_shared_prefix_step(q, k_new, v_new, positions, self.q_rot, self.k_cache, self.v_cache,
+                                   self.prefix_blocks, self.prefix_len, self.block_table, self.out, self.rope_base,
+                                   self.rope_style, self.scale, self.num_splits, self.prefix_splits, self.workspace,
+                                   self.err, stream)
+        return self.out
+
+    def __call__(self, q, k_new, v_new, positions, seq_lens=None, stream=None) -> torch.Tensor:
+        if seq_lens is None:
+            return self.fused(q, k_new, v_new, positions, stream)
+        self.rope_append(q, k_new, v_new, positions, stream)
+        return self.attend(seq_lens, stream)
+
+
 class PrefillStep(VerifyStep):
     """Prefill of T prompt tokens per sequence (positions[b]: the first one's position, 0 for a
     fresh prompt): RoPE + append, then causal attention. No split-K workspace."""
