@@ -66,7 +66,9 @@ enum {
   RRA_ERR_BLOCK_ID = 2,   /* a block-table entry outside [0, num_blocks): block 0 was used instead */
   RRA_ERR_SEQ_LEN = 4,    /* seq_lens[b] < 0 or > capacity: clamped into [0, capacity] */
   RRA_ERR_TIMEOUT = 8,    /* an in-kernel pipeline wait gave up (~1 s): results are invalid */
-  RRA_ERR_WORKSPACE = 16  /* the workspace's split counters were not zero: results are invalid */
+  RRA_ERR_WORKSPACE = 16, /* the workspace's split counters were not zero: results are invalid */
+  RRA_ERR_TOKEN = 32,     /* a drafted token outside [0, V): it counts as rejected */
+  RRA_ERR_PROBS = 64      /* a row of probabilities without any: token V - 1 was drawn */
 };
 
 /* Steps 1-2: RoPE on q and k_new at positions[b], then append rotated k and raw v.
@@ -396,6 +398,37 @@ RRA_API int rra_shared_prefix_step(const void* q, const void* k_new, const void*
 RRA_API int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq,
                                    int block_size, int num_splits, int prefix_splits, int* own_splits,
                                    int* prefix_chunks, size_t* workspace_bytes);
+
+/* --- Acceptance of drafted tokens (what follows the verify step's forward pass) ---
+ *
+ * [Opt-2026] §五 (speculative decoding: the target checks the draft model's tokens). For sequence b,
+ * with p_j = target_probs[b, j] the target's distribution at drafted token j (p_gamma: after the last
+ * one) and q_j = draft_probs[b, j] the drafter's: token x_j = draft_tokens[b, j] is kept while
+ *   u_accept[b, j] * q_j(x_j) < p_j(x_j),        j = 0, 1, ..., len_b - 1.
+ * With n tokens kept, one more is drawn: from max(p_n - q_n, 0) normalised if a token was rejected
+ * (from p_n where that is zero everywhere), from p_n if all were kept, as the lowest index v whose
+ * inclusive sum exceeds u_sample[b] times the total. The tokens so emitted follow p ("min(1, p / q)").
+ * The comparison is exact, the sums are of whole numbers of 2^-60, so results do not depend on
+ * how the work is split.
+ *
+ *   target_probs  dt [B, gamma + 1, V], draft_probs dt [B, gamma, V]: V consecutive values per row, rows
+ *                 `stride_t` and sequences `stride_b` elements apart (>= 0, any alignment of the element
+ *                 type). Values in [0, 1] (others count as the nearer end, NaN as 0), rows that sum to
+ *                 about 1 (below 16). draft_probs NULL: a drafter without probabilities, q_j(x_j) = 1.
+ *   draft_tokens  int32 [B, gamma]; draft_lens int32 [B], 0..gamma tokens of sequence b (NULL: gamma;
+ *                 outside: RRA_ERR_SEQ_LEN and clamped)
+ *   u_accept, u_sample  float32 [B, gamma] and [B], uniform random numbers in [0, 1)
+ *   tokens_out    int32 [B, gamma + 1]: the n kept tokens, the drawn one, then -1
+ *   n_accepted    int32 [B]: n
+ *   positions, positions_out  int32 [B]: with positions_out (may equal positions), positions[b] + n + 1,
+ *                 the first new token's position of the next verify step. Both may be NULL.
+ * gamma is 1..32, B at most 65535, V at most 2^30. dt is bf16 or fp32. */
+RRA_API int rra_accept_draft(const void* target_probs, int64_t target_stride_b, int64_t target_stride_t,
+                             const void* draft_probs, int64_t draft_stride_b, int64_t draft_stride_t,
+                             const int32_t* draft_tokens, const int32_t* draft_lens, const float* u_accept,
+                             const float* u_sample, const int32_t* positions, int32_t* tokens_out,
+                             int32_t* n_accepted, int32_t* positions_out, int B, int gamma, int V, rra_dtype dt,
+                             int32_t* err_flag, void* stream);
 
 /* Bytes of a K+V cache: 2 * n_layers * n_kv_heads * head_dim * seq_len * batch * dtype_bytes
  * ([Opt-2026] §四 memory formula; [KVC-GQA-RoPE] §5.3). Host only; returns 0 when an

@@ -18,6 +18,7 @@ from . import _build
 
 RRA_F32, RRA_BF16 = 0, 1
 RRA_ERR_POSITION, RRA_ERR_BLOCK_ID, RRA_ERR_SEQ_LEN, RRA_ERR_TIMEOUT, RRA_ERR_WORKSPACE = 1, 2, 4, 8, 16
+RRA_ERR_TOKEN, RRA_ERR_PROBS = 32, 64
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -77,6 +78,8 @@ _SIGNATURES = {
     "rra_shared_prefix_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
                                         _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f64, _c_int, _c_f32, _c_int,
                                         _c_int, _vp, _c_size, _vp, _vp]),
+    "rra_accept_draft": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "rra_shared_prefix_plan": (_c_int, [_c_int] * 10 + [_vp, _vp, _vp]),
 }
 
@@ -491,6 +494,55 @@ def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, pr
                                       int(prefix_splits), _ptr(workspace), ws_bytes, _ptr(err_flag),
                                       _stream(stream, q))
     _check("rra_shared_prefix_step", st)
+
+
+# --------------------------------------------------------------------------- draft acceptance
+def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs=None, draft_lens=None,
+                     positions=None, tokens_out=None, n_accepted=None, positions_out=None, err_flag=None,
+                     stream=None) -> tuple:
+    """(tokens [B, gamma + 1], kept [B]), and with ``positions`` the next positions [B]: the drafted tokens the
+    target keeps, the one drawn after them, then -1.
+
+    target_probs [B, gamma + 1, V] and draft_probs [B, gamma, V] (or None: a drafter without
+    probabilities) are bf16 or fp32 with a unit last stride; u_accept [B, gamma] and u_sample [B] are
+    uniform random numbers in [0, 1). Outputs are made where they are not given; positions_out may be
+    positions.
+    """
+    B, gamma = draft_tokens.shape
+    V, dt = target_probs.shape[-1], _dtype_code(target_probs)
+    if target_probs.shape != (B, gamma + 1, V):
+        raise ValueError("target_probs: [B, gamma + 1, V]")
+    sq = (0, 0)
+    if draft_probs is not None:
+        if draft_probs.shape != (B, gamma, V) or draft_probs.dtype != target_probs.dtype:
+            raise ValueError("draft_probs: [B, gamma, V], of target_probs' type")
+        sq = draft_probs.stride()
+    sp = target_probs.stride()
+    for t, s in ((target_probs, sp), (draft_probs, sq)):
+        if t is not None and not (t.is_cuda and (s[2] == 1 or V == 1)):
+            raise ValueError("probabilities: CUDA tensors with a unit last stride")
+    dev, i32 = target_probs.device, torch.int32
+    if u_accept.dtype != torch.float32 or u_sample.dtype != torch.float32:
+        raise TypeError("u_accept and u_sample are float32")
+    if u_accept.shape != (B, gamma) or u_sample.numel() != B:
+        raise ValueError("u_accept: [B, gamma]; u_sample: [B]")
+    if tokens_out is None:
+        tokens_out = torch.empty(B, gamma + 1, dtype=i32, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty(B, dtype=i32, device=dev)
+    if positions_out is None and positions is not None:
+        positions_out = torch.empty(B, dtype=i32, device=dev)
+    for t, n in ((draft_tokens, B * gamma), (draft_lens, B), (positions, B), (tokens_out, B * (gamma + 1)),
+                 (n_accepted, B), (positions_out, B)):
+        if t is not None and (t.dtype != i32 or t.numel() != n):
+            raise ValueError("tokens, lengths, positions and counts are int32 tensors of [B, ...] values")
+    st = lib().rra_accept_draft(target_probs.data_ptr(), sp[0], sp[1],
+                                draft_probs.data_ptr() if draft_probs is not None else None, sq[0], sq[1],
+                                _ptr(draft_tokens), _ptr(draft_lens), _ptr(u_accept), _ptr(u_sample), _ptr(positions),
+                                _ptr(tokens_out), _ptr(n_accepted), _ptr(positions_out), B, gamma, V, dt,
+                                _ptr(err_flag), _stream(stream, target_probs))
+    _check("rra_accept_draft", st)
+    return (tokens_out, n_accepted) if positions_out is None else (tokens_out, n_accepted, positions_out)
 
 
 # --------------------------------------------------------------------------- prefill
