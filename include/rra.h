@@ -408,13 +408,13 @@ RRA_API int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int
  * With n tokens kept, one more is drawn: from max(p_n - q_n, 0) normalised if a token was rejected
  * (from p_n where that is zero everywhere), from p_n if all were kept, as the lowest index v whose
  * inclusive sum exceeds u_sample[b] times the total. The tokens so emitted follow p ("min(1, p / q)").
- * The comparison is exact, the sums are of whole numbers of 2^-60, so results do not depend on
- * how the work is split.
+ * The comparison is exact, the sums are of whole numbers of 2^-60 (bf16: 2^-45), so results do not
+ * depend on how the work is split.
  *
  *   target_probs  dt [B, gamma + 1, V], draft_probs dt [B, gamma, V]: V consecutive values per row, rows
  *                 `stride_t` and sequences `stride_b` elements apart (>= 0, any alignment of the element
  *                 type). Values in [0, 1] (others count as the nearer end, NaN as 0), rows that sum to
- *                 about 1 (below 16). draft_probs NULL: a drafter without probabilities, q_j(x_j) = 1.
+ *                 about 1 (below 8). draft_probs NULL: a drafter without probabilities, q_j(x_j) = 1.
  *   draft_tokens  int32 [B, gamma]; draft_lens int32 [B], 0..gamma tokens of sequence b (NULL: gamma;
  *                 outside: RRA_ERR_SEQ_LEN and clamped)
  *   u_accept, u_sample  float32 [B, gamma] and [B], uniform random numbers in [0, 1)

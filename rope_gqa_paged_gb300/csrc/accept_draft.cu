@@ -7,19 +7,30 @@
 // §五 names the method). The draw inverts the cumulative distribution: the lowest index v with
 // r_0 + ... + r_v > u (r_0 + ... + r_(V-1)).
 //
-// Exactness: u q and p are compared as float64 products (24 x 24 bits fit 53). The r_v are summed as
-// 64-bit integers in units of 2^-60, each probability cut to a whole number of units: integer
-// sums do not depend on their order, so any split of the vocabulary over lanes, warps and CTAs
-// gives the same token, and a float64 cumulative sum does unless u falls within ~V 2^-53 of a border.
+// Exactness: u q and p are compared as float64 products (24 x 24 bits fit 53). With every
+// probability a whole number of units (2^-60 for float32; 2^-45 for bf16, whose 8 bits it holds
+// exactly from 2^-38 up), r = p - min(p, q) is one too, and the sums are 64-bit integers. They do not
+// depend on their order, so any split of the vocabulary over lanes, warps and CTAs gives the same
+// token, and a float64 cumulative sum does unless u falls within rounding of a border.
+// The integers come from float32 additions: x + 2 rounds x to a multiple of 2^-22 and holds that
+// multiple in its low bits, so adding up the bit patterns adds up the integers; x minus the rounded
+// part is exact and goes through the same step with the next smaller constant (unit 2^-45, then
+// 2^-60). (The 64-bit conversion instruction runs at a small fraction of that: 64 rows of 128000
+// float32 values 54 us against 36 us with 64-bit shifts, and less again with the additions.)
 //
 // Bound: HBM (one row of p, and one of q where a token was rejected) for large batches, latency for
-// small ones. One cluster of CTAs takes a sequence: each CTA decides n for itself (two
-// dependent loads), sums its part of the vocabulary (a contiguous run per warp, lanes on
-// consecutive values, so rows of any alignment and stride load in whole lines), and the CTAs exchange
-// their sums through distributed shared memory: one launch, no workspace, no atomics. The warp whose
-// run holds the border reads it again (from L1 or L2) and scans it.
+// small ones. One cluster of CTAs takes a sequence: each CTA decides n for itself (two dependent
+// loads), sums its part of the vocabulary, and the CTAs exchange their sums through distributed
+// shared memory: one launch, no workspace, no atomics. The CTA whose part holds the border looks for
+// it again (in L1 or L2): its warps split the run that holds it until 256 values are left, which one
+// warp scans. (One warp scanning its whole run, 32 values a step: 33 us against ## us.) As many CTAs per sequence (up to 16) as keep the whole grid
+// resident at once.
+// Rows of any alignment load in aligned 16-byte vectors of p; where q's rows lie at another offset its
+// two vectors are shifted together. Only vectors wholly inside the row are read so.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "rra_device.cuh"
 #include "rra_internal.h"
@@ -27,11 +38,18 @@
 namespace rra {
 namespace {
 
-constexpr int kThreads = 512;
+#ifndef AD_T
+#define AD_T 256
+#define AD_S 4
+#define AD_B 2
+#endif
+constexpr int kThreads = AD_T;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = AD_S;   // 64 registers
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGamma = 32;   // one lane of a warp per drafted token
-constexpr int kBatch = 8;       // groups of 32 values whose loads a warp has in flight together
+constexpr int kBatch = AD_B;       // vectors of p (and q) a lane has in flight together
+constexpr int kScan = 8;        // values per lane of the last warp's scan
 
 struct AcceptArgs {
   const void* p;                // [B, gamma + 1, V] with these strides (elements)
@@ -50,12 +68,67 @@ struct AcceptArgs {
   int32_t* err;
 };
 
-// A probability as a whole number of 2^-60 units (NaN: 0; outside [0, 1]: the nearer end).
-__device__ __forceinline__ uint64_t units(float x) {
-  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
+// Rounding constants: kM[l] + x, |x| at most half the previous unit (at most 1 for the first), stays in
+// one binade, whose unit is 2^-22, 2^-45, 2^-60.
+__device__ constexpr float kM0 = 2.f, kM1 = 0x1.8p-22f, kM2 = 0x1.8p-37f;
+
+// Two float32 additions in one instruction: x.lo + y.lo and x.hi + y.hi.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ uint64_t neg2(uint64_t x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ uint32_t both(uint64_t x) { return static_cast<uint32_t>(x) + static_cast<uint32_t>(x >> 32); }
+
+// Sums of probabilities in units, as sums of bit patterns of the rounded values. At most 256 values go
+// into one (the second part of a value is up to 2^22 units of 2^-45, the first up to 2^22 of 2^-22).
+template <int LEVELS>
+struct UnitSum {
+  uint32_t a0 = 0, a1 = 0, a2 = 0;
+  __device__ __forceinline__ void add(float x, float y) {
+    const uint64_t xy = pack2(x, y);
+    const uint64_t t0 = add2(xy, pack2(kM0, kM0));
+    a0 += both(t0);
+    const uint64_t l0 = add2(xy, neg2(add2(t0, pack2(-kM0, -kM0))));
+    const uint64_t t1 = add2(l0, pack2(kM1, kM1));
+    a1 += both(t1);
+    if constexpr (LEVELS == 3) {
+      const uint64_t l1 = add2(l0, neg2(add2(t1, pack2(-kM1, -kM1))));
+      a2 += both(add2(l1, pack2(kM2, kM2)));
+    }
+  }
+  // the sum of the `count` values added, in units of 2^-60
+  __device__ __forceinline__ int64_t value(uint32_t count) const {
+    const auto part = [&](uint32_t a, float m) {
+      return static_cast<int64_t>(static_cast<int32_t>(a - count * __float_as_uint(m)));
+    };
+    int64_t s = (part(a0, kM0) << 38) + (part(a1, kM1) << 15);
+    if constexpr (LEVELS == 3) s += part(a2, kM2);
+    return s;
+  }
+};
+
+template <typename T>
+constexpr int kLevels = sizeof(T) == 4 ? 3 : 2;
+
+template <typename T>
+__device__ __forceinline__ int64_t units(float x) {
+  UnitSum<kLevels<T>> s;
+  s.add(x, 0.f);
+  return s.value(2);
 }
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+// NaN: 0; outside [0, 1]: the nearer end.
+template <typename T>
+__device__ __forceinline__ float load_prob(const T* p) {
+  return __saturatef(Elem<T>::load(p));
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
   return x;
@@ -68,32 +141,110 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint64_t ld_cluster(const uint64_t* local, uint32_t rank) {
+__device__ __forceinline__ int64_t ld_cluster(const int64_t* local, uint32_t rank) {
   uint32_t addr;
-  uint64_t v;
+  int64_t v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
   return v;
 }
 
-// The rest of one sequence's distribution at the decisive row: r_v and p_v in units.
+// 16 bytes of p at element offset v of a row, as probabilities; values outside [0, V) are 0.
+template <typename T, int E>
+__device__ __forceinline__ void unpack_probs(const uint4& w, float (&x)[E]) {
+  Elem<T>::unpack(w, x);
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = __saturatef(x[e]);
+}
+
+// The sum of p - min(p, q) over the elements of the vectors n0 + lane, n0 + lane + 32, ... below n1 (vector
+// n holds the elements n E - head .. n E - head + E - 1 of the row, 16-byte aligned in p); q may be
+// nullptr (the sum of p). One lane's part, in units of 2^-60.
 template <typename T>
-struct Rest {
-  const T* p;
-  const T* q;      // nullptr: nothing is taken off, but from `skip`
-  int skip;        // token whose p counts as taken off entirely (no draft probabilities), or -1
-  __device__ __forceinline__ uint64_t rest(float pv, float qv, int v) const {
-    const uint64_t a = units(pv), b = units(qv);
-    return v == skip || a <= b ? 0 : a - b;
+__device__ __forceinline__ int64_t sum_rest(const T* p, const T* q, int V, int n0, int n1, int lane) {
+  constexpr int E = Elem<T>::kPerChunk;
+  constexpr uint32_t kSize = sizeof(T);
+  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / kSize);
+  // q's vectors: those of p lie `off` elements into them
+  const int off = static_cast<int>(((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) / kSize);
+  int64_t sum = 0;
+  constexpr int kVectors = 256 / E;  // between two flushes of the 32-bit sums
+  static_assert(kVectors % kBatch == 0, "whole batches");
+  int n = n0 + lane;
+  while (n < n1) {
+    UnitSum<kLevels<T>> sp, sm;
+    uint32_t count = 0;
+    for (const int stop = min(n1, n + 32 * kVectors); n < stop; n += 32 * kBatch, count += kBatch * E) {
+      uint4 pw[kBatch], qw[kBatch], qx[kBatch];
+      int kind[kBatch];  // 0: nothing here, 1: whole vectors, 2: value by value
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int m = n + 32 * k, v = m * E - head;
+        const bool whole = v >= 0 && v + E <= V && (q == nullptr || off == 0 || (v >= off && v - off + 2 * E <= V));
+        kind[k] = m >= n1 ? 0 : whole ? 1 : 2;
+        pw[k] = qw[k] = qx[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (kind[k] == 1) {
+          pw[k] = *reinterpret_cast<const uint4*>(p + v);
+          if (q != nullptr) {
+            const uint4* a = reinterpret_cast<const uint4*>(q + (v - off));
+            qw[k] = a[0];
+            if (off != 0) qx[k] = a[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        float x[E], y[E];
+        if (kind[k] == 2) {
+          const int v = (n + 32 * k) * E - head;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const bool in = v + e >= 0 && v + e < V;
+            x[e] = in ? load_prob(p + v + e) : 0.f;
+            y[e] = in && q != nullptr ? load_prob(q + v + e) : 0.f;
+          }
+        } else {
+          unpack_probs<T, E>(pw[k], x);
+          if (q != nullptr && off != 0) {  // the vector that starts `off` elements into (qw, qx)
+            uint32_t w[8] = {qw[k].x, qw[k].y, qw[k].z, qw[k].w, qx[k].x, qx[k].y, qx[k].z, qx[k].w};
+            const uint32_t bytes = off * kSize;
+            if (bytes & 8) {
+#pragma unroll
+              for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+            }
+            if (bytes & 4) {
+#pragma unroll
+              for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+            }
+            if (kSize == 2 && (bytes & 2)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            }
+            qw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          unpack_probs<T, E>(qw[k], y);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) sp.add(x[e], x[e + 1]);
+        if (q != nullptr) {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) sm.add(fminf(x[e], y[e]), fminf(x[e + 1], y[e + 1]));
+        }
+      }
+    }
+    sum += sp.value(count);
+    if (q != nullptr) sum -= sm.value(count);
   }
-};
+  return sum;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) accept_draft_kernel(const AcceptArgs a) {
-  __shared__ uint64_t warp_sums[2][kWarps];
-  __shared__ uint64_t cta_sums[2];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(const AcceptArgs a) {
+  constexpr int E = Elem<T>::kPerChunk;
+  __shared__ int64_t warp_sums[2][kWarps];
+  __shared__ int64_t cta_sum[2];
   const int b = blockIdx.y, C = gridDim.x;
-  const uint32_t rank = cluster_rank();
+  const int rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gamma = a.gamma, V = a.V;
 
@@ -103,17 +254,21 @@ __global__ void __launch_bounds__(kThreads) accept_draft_kernel(const AcceptArgs
 
   // ---- how many tokens are kept (every warp finds it for itself: lane j has token j)
   int len = a.lens != nullptr ? a.lens[b] : gamma;
+  const float u_last = a.u_sample[b];
+  int x = -1;
+  float u = 0.f;
+  if (lane < gamma) {
+    x = a.tokens[static_cast<size_t>(b) * gamma + lane];
+    u = a.u_accept[static_cast<size_t>(b) * gamma + lane];
+  }
   if (len < 0 || len > gamma) {
     if (scribe && lane == 0) flag_error(a.err, RRA_ERR_SEQ_LEN);
     len = min(max(len, 0), gamma);
   }
   const T* prow = static_cast<const T*>(a.p) + b * a.p_sb;
   const T* qrow = static_cast<const T*>(a.q) + b * a.q_sb;
-  int x = -1;
   bool keep = false;
   if (lane < len) {
-    x = a.tokens[static_cast<size_t>(b) * gamma + lane];
-    const float u = a.u_accept[static_cast<size_t>(b) * gamma + lane];
     if (x < 0 || x >= V) {
       if (scribe) flag_error(a.err, RRA_ERR_TOKEN);
     } else {
@@ -125,8 +280,10 @@ __global__ void __launch_bounds__(kThreads) accept_draft_kernel(const AcceptArgs
   const uint32_t dropped = ~__ballot_sync(0xffffffffu, keep);
   const int n = min(dropped != 0 ? __ffs(dropped) - 1 : 32, len);
   const int at = __shfl_sync(0xffffffffu, x, n & 31);  // the rejected token (n < len)
-  const Rest<T> rest{prow + n * a.p_st, n < len && a.q != nullptr ? qrow + n * a.q_st : nullptr,
-                     n < len && a.q == nullptr ? at : -1};
+  const T* p = prow + n * a.p_st;
+  const T* q = n < len && a.q != nullptr ? qrow + n * a.q_st : nullptr;
+  // without the drafter's probabilities the rejected token alone is taken out of p
+  int skip = n < len && a.q == nullptr && at >= 0 && at < V ? at : -1;
   if (scribe) {
     for (int j = lane; j <= gamma; j += 32) {
       if (j != n) a.tokens_out[static_cast<size_t>(b) * (gamma + 1) + j] = j < n ? x : -1;
@@ -137,89 +294,105 @@ __global__ void __launch_bounds__(kThreads) accept_draft_kernel(const AcceptArgs
     }
   }
 
-  // ---- sums of r and p over this warp's run of the vocabulary
-  const int groups = (V + 31) / 32;                             // of 32 values
-  const int per_warp = (groups + C * kWarps - 1) / (C * kWarps);
-  const int g0 = min((static_cast<int>(rank) * kWarps + warp) * per_warp, groups);
-  const int g1 = min(g0 + per_warp, groups);
-  uint64_t sr = 0, sp = 0;
-  for (int g = g0; g < g1; g += kBatch) {
-    float pv[kBatch], qv[kBatch];
+  // ---- sums of r over this warp's run of the vocabulary, the CTA's and the sequence's
+  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  const int vecs = (V + head + E - 1) / E;
+  const int per_warp = (vecs + C * kWarps - 1) / (C * kWarps);
+  // this warp's sum over the vectors [n0, n1), to every lane; `sums` gets it for the CTA
+  auto run_sum = [&](int n0, int n1, int64_t* sums) {
+    int64_t s = warp_sum(sum_rest<T>(p, q, V, n0, n1, lane));
+    if (skip >= 0 && skip >= n0 * E - head && skip < n1 * E - head) s -= units<T>(load_prob(p + skip));
+    if (lane == 0) sums[warp] = s;
+  };
+  int64_t total, before;
+  // a second time, over p itself, where nothing is left (p <= q everywhere, by rounding)
+  for (int pass = 0;; ++pass) {
+    const int n0 = min((rank * kWarps + warp) * per_warp, vecs);
+    run_sum(n0, min(n0 + per_warp, vecs), warp_sums[0]);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int64_t s = 0;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int v = (g + k) * 32 + lane;
-      const bool in = g + k < g1 && v < V;
-      pv[k] = in ? Elem<T>::load(rest.p + v) : 0.f;
-      qv[k] = in && rest.q != nullptr ? Elem<T>::load(rest.q + v) : 0.f;
+      for (int w = 0; w < kWarps; ++w) s += warp_sums[0][w];
+      cta_sum[pass] = s;
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      sr += rest.rest(pv[k], qv[k], (g + k) * 32 + lane);
-      sp += units(pv[k]);
-    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    const int64_t c = lane < C ? ld_cluster(&cta_sum[pass], lane) : 0;
+    total = warp_sum(c);
+    before = warp_sum(lane < rank ? c : 0);
+    if (total > 0 || pass == 1) break;
+    q = nullptr;
+    skip = -1;
   }
-  sr = warp_sum(sr);
-  sp = warp_sum(sp);
-  if (lane == 0) {
-    warp_sums[0][warp] = sr;
-    warp_sums[1][warp] = sp;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    uint64_t s = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += warp_sums[threadIdx.x][w];
-    cta_sums[threadIdx.x] = s;
-  }
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-
-  // ---- the border u * total, and the warp whose run holds it
-  const uint64_t cr = lane < C ? ld_cluster(&cta_sums[0], lane) : 0;
-  const uint64_t cp = lane < C ? ld_cluster(&cta_sums[1], lane) : 0;
   cluster_arrive();  // this CTA has read the others' sums
-  const uint64_t total_r = warp_sum(cr), total_p = warp_sum(cp);
-  // nothing is left (p <= q everywhere, by rounding): draw from p itself
-  const int which = total_r > 0 ? 0 : 1;
-  const uint64_t total = which == 0 ? total_r : total_p;
-  const float u = fminf(fmaxf(a.u_sample[b], 0.f), 1.f - 0x1p-24f);
-  const uint64_t border = __umul64hi(total, __float2ull_rz(u * 0x1p64f));  // floor(u * total)
-  uint64_t before = warp_sum(lane < static_cast<int>(rank) ? (which == 0 ? cr : cp) : 0);
-  before += warp_sum(lane < warp ? warp_sums[which][lane & (kWarps - 1)] : 0);
-  const uint64_t mine = warp_sums[which][warp];
+
+  // ---- the border u * total, and the CTA whose part holds it
+  const float uc = fminf(fmaxf(u_last, 0.f), 1.f - 0x1p-24f);
+  const int64_t border = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(total), __float2ull_rz(uc * 0x1p64f)));
   int32_t* token_out = a.tokens_out + static_cast<size_t>(b) * (gamma + 1) + n;
-  if (total == 0) {
+  // (sums are never negative, so the first warp whose inclusive sum exceeds the border holds it)
+  int f0 = rank * kWarps * per_warp, step = per_warp, f1 = vecs;
+  bool here = false;
+  if (total <= 0) {
     if (scribe && lane == 0) {
       flag_error(a.err, RRA_ERR_PROBS);
       *token_out = V - 1;
     }
-  } else if (before <= border && border < before + mine) {
-    bool found = false;
-    for (int g = g0; g < g1 && !found; g += kBatch) {
-      uint64_t val[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int v = (g + k) * 32 + lane;
-        const bool in = g + k < g1 && v < V;
-        const float pv = in ? Elem<T>::load(rest.p + v) : 0.f;
-        const float qv = in && rest.q != nullptr ? Elem<T>::load(rest.q + v) : 0.f;
-        val[k] = which == 0 ? rest.rest(pv, qv, v) : units(pv);
+  } else {
+    for (int level = 0;; ++level) {
+      const int64_t* sums = warp_sums[level & 1];
+      int w = 0;
+      bool found = false;
+      if (before <= border) {
+        for (; w < kWarps && !found; ++w) {
+          if (border < before + sums[w]) {
+            found = true;
+            break;
+          }
+          before += sums[w];
+        }
       }
+      if (!found) break;  // (in another CTA)
+      f0 += w * step;
+      f1 = min(f0 + step, f1);
+      here = true;
+      if ((f1 - f0) * E <= 32 * kScan) break;
+      step = (f1 - f0 + kWarps - 1) / kWarps;
+      const int n0 = min(f0 + warp * step, f1);
+      run_sum(n0, min(n0 + step, f1), warp_sums[(level & 1) ^ 1]);
+      __syncthreads();
+    }
+    if (here && warp == 0) {  // at most 256 values: each lane takes kScan consecutive ones
+      const int v0 = max(f0 * E - head, 0) + lane * kScan, v1 = min(f1 * E - head, V);
+      int64_t val[kScan], c = 0;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        uint64_t c = val[k];  // inclusive sum over the lanes
+      for (int k = 0; k < kScan; ++k) {
+        const int v = v0 + k;
+        const float pv = v < v1 ? load_prob(p + v) : 0.f;
+        const float qv = v < v1 && q != nullptr ? load_prob(q + v) : 0.f;
+        val[k] = v == skip ? 0 : units<T>(pv) - units<T>(fminf(pv, qv));
+        c += val[k];
+      }
+      const int64_t own = c;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xffffffffu, c, d);
-          if (lane >= d) c += y;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
+        if (lane >= d) c += y;
+      }
+      const uint32_t over = __ballot_sync(0xffffffffu, before + c > border);
+      if (over != 0 && lane == __ffs(over) - 1) {
+        int64_t sum = before + c - own;
+        int at_k = kScan - 1;
+#pragma unroll
+        for (int k = kScan - 1; k >= 0; --k) {  // from the back: the lowest k that exceeds stays
+          int64_t incl = sum;
+#pragma unroll
+          for (int i = 0; i <= k; ++i) incl += val[i];
+          if (incl > border) at_k = k;
         }
-        const uint32_t over = __ballot_sync(0xffffffffu, before + c > border);
-        if (!found && over != 0) {
-          found = true;
-          if (lane == 0) *token_out = (g + k) * 32 + __ffs(over) - 1;
-        }
-        before += __shfl_sync(0xffffffffu, c, 31);
+        *token_out = v0 + at_k;
       }
     }
   }
@@ -292,7 +465,10 @@ extern "C" int rra_accept_draft(const void* target_probs, int64_t target_stride_
   a.gamma = gamma;
   a.V = V;
   a.err = err_flag;
-  const int clusters = rra::kMaxCluster;
+  // CTAs per sequence: the most (up to 16, a power of two) with which all CTAs are resident at once
+  int clusters = rra::kMaxCluster;
+  while (clusters > 1 && int64_t(clusters) * B > int64_t(rra::kCtasPerSm) * std::max(1, rra::current_sm_count()))
+    clusters /= 2;
   const cudaError_t e = dt == RRA_BF16
                             ? rra::launch_accept<__nv_bfloat16>(a, B, clusters, static_cast<cudaStream_t>(stream))
                             : rra::launch_accept<float>(a, B, clusters, static_cast<cudaStream_t>(stream));

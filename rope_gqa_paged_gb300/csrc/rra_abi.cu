@@ -599,6 +599,7 @@ void set_q8_args(rra::DecodeArgs* a, const Q8Layout& l, const void* k_codes, con
 
 namespace rra {
 void record_cuda_error(cudaError_t e, const char* where) { cuda_fail(e, where); }
+int current_sm_count() { return sm_count(); }
 }  // namespace rra
 
 static int decode_qk_num_splits(int B, int Hq, int Hkv, int D, int64_t max_tokens, int block_size, int num_splits,

@@ -146,6 +146,8 @@ void fill_rope_phi(uint32_t (*phi)[3], int D, double base);
 
 // Stores the text rra_last_cuda_error() returns on this thread.
 void record_cuda_error(cudaError_t e, const char* where);
+// SMs of the current device (0 without one).
+int current_sm_count();
 
 cudaError_t launch_rope_append(const RopeArgs& a, rra_dtype dt, cudaStream_t stream);
 // RoPE + append into an INT8 cache (bf16 q / k_new / v_new; a.k_scale etc. set).
