@@ -16,15 +16,14 @@
 // multiple in its low bits, so adding up the bit patterns adds up the integers; x minus the rounded
 // part is exact and goes through the same step with the next smaller constant (unit 2^-45, then
 // 2^-60). (The 64-bit conversion instruction runs at a small fraction of that: 64 rows of 128000
-// float32 values 54 us against 36 us with 64-bit shifts, and less again with the additions.)
+// float32 values 54 us with it, 36 us with 64-bit shifts, 33 us with these additions.)
 //
 // Bound: HBM (one row of p, and one of q where a token was rejected) for large batches, latency for
 // small ones. One cluster of CTAs takes a sequence: each CTA decides n for itself (two dependent
 // loads), sums its part of the vocabulary, and the CTAs exchange their sums through distributed
 // shared memory: one launch, no workspace, no atomics. The CTA whose part holds the border looks for
 // it again (in L1 or L2): its warps split the run that holds it until 256 values are left, which one
-// warp scans. (One warp scanning its whole run, 32 values a step: 33 us against ## us.) As many CTAs per sequence (up to 16) as keep the whole grid
-// resident at once.
+// warp scans. (One warp scanning its whole run, 32 values a step: 64 rows of 128000 values in 33 us, 23 us so.)
 // Rows of any alignment load in aligned 16-byte vectors of p; where q's rows lie at another offset its
 // two vectors are shifted together. Only vectors wholly inside the row are read so.
 #include <cuda_bf16.h>
@@ -38,17 +37,11 @@
 namespace rra {
 namespace {
 
-#ifndef AD_T
-#define AD_T 256
-#define AD_S 4
-#define AD_B 2
-#endif
-constexpr int kThreads = AD_T;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = AD_S;   // 64 registers
+constexpr int kCtasPerSm = 4;   // 64 registers
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGamma = 32;   // one lane of a warp per drafted token
-constexpr int kBatch = AD_B;       // vectors of p (and q) a lane has in flight together
 constexpr int kScan = 8;        // values per lane of the last warp's scan
 
 struct AcceptArgs {
@@ -157,83 +150,115 @@ __device__ __forceinline__ void unpack_probs(const uint4& w, float (&x)[E]) {
   for (int e = 0; e < E; ++e) x[e] = __saturatef(x[e]);
 }
 
-// The sum of p - min(p, q) over the elements of the vectors n0 + lane, n0 + lane + 32, ... below n1 (vector
-// n holds the elements n E - head .. n E - head + E - 1 of the row, 16-byte aligned in p); q may be
-// nullptr (the sum of p). One lane's part, in units of 2^-60.
+// The 16 bytes that start `bytes` (a multiple of the element size) into the 32 of (a, b).
 template <typename T>
-__device__ __forceinline__ int64_t sum_rest(const T* p, const T* q, int V, int n0, int n1, int lane) {
+__device__ __forceinline__ uint4 shift_vectors(const uint4& a, const uint4& b, uint32_t bytes) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (bytes & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (bytes & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (sizeof(T) == 2 && (bytes & 2)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// How q's row lies: there is none, at the offset of p's row within 16 bytes, at another one.
+enum class Rows { kOne, kAligned, kShifted };
+
+// One lane's part of the sum of p - min(p, q) over the vectors [n0, n1), all of them wholly inside the
+// row (kShifted: the two vectors of q as well).
+template <typename T, Rows ROWS>
+__device__ __forceinline__ int64_t sum_vectors(const T* p, const T* q, int head, uint32_t off, int n0, int n1, int lane) {
   constexpr int E = Elem<T>::kPerChunk;
-  constexpr uint32_t kSize = sizeof(T);
-  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / kSize);
-  // q's vectors: those of p lie `off` elements into them
-  const int off = static_cast<int>(((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) / kSize);
-  int64_t sum = 0;
-  constexpr int kVectors = 256 / E;  // between two flushes of the 32-bit sums
+  constexpr int kBatch = ROWS == Rows::kShifted ? 2 : 4;  // vectors of each row in flight per lane (64 registers)
+  constexpr int kVectors = 256 / E;                       // between two flushes of the 32-bit sums
   static_assert(kVectors % kBatch == 0, "whole batches");
+  const uint4* pv = reinterpret_cast<const uint4*>(p - head);
+  const uint4* qv = reinterpret_cast<const uint4*>(q - head - static_cast<int>(off));
+  int64_t sum = 0;
   int n = n0 + lane;
   while (n < n1) {
     UnitSum<kLevels<T>> sp, sm;
     uint32_t count = 0;
-    for (const int stop = min(n1, n + 32 * kVectors); n < stop; n += 32 * kBatch, count += kBatch * E) {
-      uint4 pw[kBatch], qw[kBatch], qx[kBatch];
-      int kind[kBatch];  // 0: nothing here, 1: whole vectors, 2: value by value
+    auto add = [&](const uint4& a, const uint4& b) {
+      float x[E];
+      unpack_probs<T, E>(a, x);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) sp.add(x[e], x[e + 1]);
+      if constexpr (ROWS != Rows::kOne) {
+        float y[E];
+        unpack_probs<T, E>(b, y);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) sm.add(fminf(x[e], y[e]), fminf(x[e + 1], y[e + 1]));
+      }
+    };
+    const int stop = min(n1, n + 32 * kVectors);
+    for (; n + 32 * (kBatch - 1) < stop; n += 32 * kBatch, count += kBatch * E) {
+      uint4 a[kBatch], b[kBatch], c[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int m = n + 32 * k, v = m * E - head;
-        const bool whole = v >= 0 && v + E <= V && (q == nullptr || off == 0 || (v >= off && v - off + 2 * E <= V));
-        kind[k] = m >= n1 ? 0 : whole ? 1 : 2;
-        pw[k] = qw[k] = qx[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (kind[k] == 1) {
-          pw[k] = *reinterpret_cast<const uint4*>(p + v);
-          if (q != nullptr) {
-            const uint4* a = reinterpret_cast<const uint4*>(q + (v - off));
-            qw[k] = a[0];
-            if (off != 0) qx[k] = a[1];
-          }
-        }
+        a[k] = pv[n + 32 * k];
+        if constexpr (ROWS != Rows::kOne) b[k] = qv[n + 32 * k];
+        if constexpr (ROWS == Rows::kShifted) c[k] = qv[n + 32 * k + 1];
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        float x[E], y[E];
-        if (kind[k] == 2) {
-          const int v = (n + 32 * k) * E - head;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const bool in = v + e >= 0 && v + e < V;
-            x[e] = in ? load_prob(p + v + e) : 0.f;
-            y[e] = in && q != nullptr ? load_prob(q + v + e) : 0.f;
-          }
-        } else {
-          unpack_probs<T, E>(pw[k], x);
-          if (q != nullptr && off != 0) {  // the vector that starts `off` elements into (qw, qx)
-            uint32_t w[8] = {qw[k].x, qw[k].y, qw[k].z, qw[k].w, qx[k].x, qx[k].y, qx[k].z, qx[k].w};
-            const uint32_t bytes = off * kSize;
-            if (bytes & 8) {
-#pragma unroll
-              for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (bytes & 4) {
-#pragma unroll
-              for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-            }
-            if (kSize == 2 && (bytes & 2)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-            }
-            qw[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          unpack_probs<T, E>(qw[k], y);
-        }
-#pragma unroll
-        for (int e = 0; e < E; e += 2) sp.add(x[e], x[e + 1]);
-        if (q != nullptr) {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) sm.add(fminf(x[e], y[e]), fminf(x[e + 1], y[e + 1]));
-        }
+        if constexpr (ROWS == Rows::kShifted) b[k] = shift_vectors<T>(b[k], c[k], off * sizeof(T));
+        add(a[k], b[k]);
+      }
+    }
+    if constexpr (kBatch > 1) {
+      for (; n < stop; n += 32, count += E) {
+        const uint4 a = pv[n];
+        uint4 b;
+        if constexpr (ROWS != Rows::kOne) b = qv[n];
+        if constexpr (ROWS == Rows::kShifted) b = shift_vectors<T>(b, qv[n + 1], off * sizeof(T));
+        add(a, b);
       }
     }
     sum += sp.value(count);
-    if (q != nullptr) sum -= sm.value(count);
+    if constexpr (ROWS != Rows::kOne) sum -= sm.value(count);
+  }
+  return sum;
+}
+
+// One lane's part of the sum of p - min(p, q) over the vectors [n0, n1) of a row (vector n holds the
+// elements n E - head .. n E - head + E - 1, 16-byte aligned in p), in units of 2^-60; q may be
+// nullptr (the sum of p). The vectors that reach over the row's ends go value by value.
+template <typename T>
+__device__ __forceinline__ int64_t sum_rest(const T* p, const T* q, int V, int n0, int n1, int lane) {
+  constexpr int E = Elem<T>::kPerChunk;
+  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  // q's vectors: those of p lie `off` elements into them
+  const uint32_t off =
+      static_cast<uint32_t>(((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) / sizeof(T));
+  const bool shifted = q != nullptr && off != 0;
+  // vectors with n E - head >= 0 (>= off) and n E - head + E (- off + 2 E) <= V
+  const int lo = (head + (shifted ? static_cast<int>(off) : 0) + E - 1) / E;
+  const int hi = max((V + head - (shifted ? E - static_cast<int>(off) : 0)) / E, 0);
+  const int i0 = min(max(n0, lo), n1), i1 = max(min(n1, hi), i0);
+  int64_t sum = 0;
+  if (q == nullptr)
+    sum = sum_vectors<T, Rows::kOne>(p, q, head, 0, i0, i1, lane);
+  else if (!shifted)
+    sum = sum_vectors<T, Rows::kAligned>(p, q, head, 0, i0, i1, lane);
+  else
+    sum = sum_vectors<T, Rows::kShifted>(p, q, head, off, i0, i1, lane);
+  const int before = (i0 - n0) * E, ends = before + (n1 - i1) * E;  // values of the other vectors
+  for (int i = lane; i < ends; i += 32) {
+    const int v = (i < before ? n0 * E + i : i1 * E + i - before) - head;
+    if (v >= 0 && v < V) {
+      const float x = load_prob(p + v);
+      sum += units<T>(x);
+      if (q != nullptr) sum -= units<T>(fminf(x, load_prob(q + v)));
+    }
   }
   return sum;
 }
@@ -465,10 +490,13 @@ extern "C" int rra_accept_draft(const void* target_probs, int64_t target_stride_
   a.gamma = gamma;
   a.V = V;
   a.err = err_flag;
-  // CTAs per sequence: the most (up to 16, a power of two) with which all CTAs are resident at once
-  int clusters = rra::kMaxCluster;
-  while (clusters > 1 && int64_t(clusters) * B > int64_t(rra::kCtasPerSm) * std::max(1, rra::current_sm_count()))
-    clusters /= 2;
+  // CTAs per sequence: 16 while they leave every CTA an SM of its own (one sequence of 32000 float32
+  // values: 5.0 us, 6.5 us with 8). Otherwise the most, up to 8, with which the whole grid is resident at
+  // once (64 x 128000 float32: 19.3 us with 8, 23.8 with 4, 27.8 with 16, whose clusters wait for 16 free
+  // places of one GPC; 256 x 100003 bf16: 29.6 us with 2, 37.2 with 8 in four turns).
+  const int64_t sms = std::max(1, rra::current_sm_count());
+  int clusters = int64_t(B) * rra::kMaxCluster <= sms ? rra::kMaxCluster : 8;
+  while (clusters > 1 && int64_t(clusters) * B > rra::kCtasPerSm * sms) clusters /= 2;
   const cudaError_t e = dt == RRA_BF16
                             ? rra::launch_accept<__nv_bfloat16>(a, B, clusters, static_cast<cudaStream_t>(stream))
                             : rra::launch_accept<float>(a, B, clusters, static_cast<cudaStream_t>(stream));
