@@ -365,13 +365,12 @@ RRA_API int rra_prefill_step(const void* q, const void* k_new, const void* v_new
  *                   (L_b = 0 for a padding row). L_b may lie inside the prefix.
  *   num_splits      splits of the sequences' own tokens, prefix_splits chunks of the prefix; 0 = chosen
  *                   by the library. With prefix_splits 0 and a prefix too short to pay for its
- *                   own pass, one kernel reads prefix and own tokens together (prefix chunks 0).
- *   workspace       of rra_shared_prefix_plan's bytes, zero-filled before its first use. Calls of any
- *                   shapes may take turns on one (its counters have the same place for all of them);
- *                   calls sharing it must not overlap on the GPU.
+ *                   own pass, prefix and own tokens are read together (prefix chunks 0).
+ *   workspace       of rra_shared_prefix_plan's bytes (may be NULL when that is 0). It needs no filling and
+ *                   keeps nothing between calls: calls of any shapes may take turns on one; calls
+ *                   sharing it must not overlap on the GPU.
  * Other arguments, error bits and statuses as in rra_verify_attn; RRA_EUNSUPPORTED where prefix_len
- * is not a multiple of block_size, RRA_ERANGE above 448 partials per row (own splits + prefix chunks)
- * or 262144 groups of up to 16 rows (sequences x KV heads x head slices).
+ * is not a multiple of block_size.
  */
 RRA_API int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_pool,
                                    const int32_t* prefix_blocks, int prefix_len, const int32_t* block_table,

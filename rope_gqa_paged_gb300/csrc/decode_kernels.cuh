@@ -196,6 +196,12 @@ struct ChunkBlockIds {
   }
 };
 
+// Shared prefix: the kernel before this one may still run when this one ends its own work; one CTA
+// waits for it, so that this grid does not complete before it.
+__device__ __forceinline__ void shared_wait_first(const DecodeArgs& a) {
+  if (a.prefix_splits > 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
+}
+
 // Counts this CTA's arrival at `cnt` (all `nthreads` consumer threads call it after their
 // last write). True in the CTA whose arrival brings the count to `target`; that CTA also puts
 // the counter back to zero, ready for the next call. No CTA ever waits for another.

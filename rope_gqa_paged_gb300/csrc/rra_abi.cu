@@ -271,17 +271,13 @@ int check_prefill_limits(int T, int Hq, int Hkv, int64_t capacity) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Shared-prefix attention: the plan of the sequences' own tokens (the verify kernel's) and the
+// Shared-prefix attention: the plan of the sequences' own tokens (the decode or verify kernel's) and the
 // chunks of the prefix.
 struct SharedPlan {
   Plan own;
   int prefix_splits = 0;  // 0: no separate pass, the own-token kernel reads the prefix too
   int prefix_chunk = 0;
 };
-
-// Most partials (prefix chunks + own splits) one merge takes: two weights per partial of its 16 rows
-// in the merging CTA's 64 KB ring.
-constexpr int kSharedMaxPartials = 448;
 
 int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq, int block_size,
                      int num_splits, int prefix_splits, SharedPlan* p) {
@@ -292,22 +288,29 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   if (prefix_len % block_size != 0) return RRA_EUNSUPPORTED;
   int st = make_plan_verify(B, gamma, Hq, Hkv, D, capacity, block_size, num_splits, &p->own);
   if (st != RRA_OK) return st;
-  const int64_t rows = int64_t(B) * gamma * (Hq / Hkv);
+  const int n_rep = Hq / Hkv;
+  if (gamma == 1) {  // the decode kernel: up to 8 heads per CTA, or 16 (two CTAs per SM)
+    p->own.hpc = decode_mma_hpc(n_rep);
+    if (p->own.hpc > 8) p->own.ctas_per_sm = 2;
+    if (static_cast<int64_t>(Hkv) * (n_rep / p->own.hpc) > 65535) return RRA_ERANGE;
+  }
+  const int64_t rows = int64_t(B) * gamma * n_rep;
   const bool pass = prefix_len > 0 && rows > 0 && (prefix_splits > 0 || (B > 1 && prefix_len >= 256));
   if (pass) {
-    const int tile = 8192 / D;
+    const int tile = rra::kSharedPrefixTile;
     const int64_t tiles = (prefix_len + tile - 1) / tile;
-    const int64_t row_tiles = (rows + rra::kSharedPrefixRows - 1) / rra::kSharedPrefixRows;
+    const int64_t per_cta = rows > rra::kSharedPrefixRows ? 2 * rra::kSharedPrefixRows : rra::kSharedPrefixRows;
+    const int64_t units = Hkv * ((rows + per_cta - 1) / per_cta);
     const int64_t max_chunk = std::max<int64_t>(1, int64_t(rra::kSharedPrefixTableEntries) * block_size / tile);
     if (Hkv > 65535) return RRA_ERANGE;
-    const int64_t resident = 2 * int64_t(std::max(1, sm_count()));
+    const int64_t resident = (rows > rra::kSharedPrefixRows ? 1 : 2) * int64_t(std::max(1, sm_count()));
     int64_t best = 0, best_cost = INT64_MAX;
     // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
     const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
     const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, 40);
     for (int64_t s = lo; s <= hi; ++s) {
       const int64_t chunk = std::min((tiles + s - 1) / s, max_chunk), n = (tiles + chunk - 1) / chunk;
-      const int64_t waves = (Hkv * row_tiles * n + resident - 1) / resident;
+      const int64_t waves = (units * n + resident - 1) / resident;
       const int64_t cost = waves * (chunk + 6);
       if (cost < best_cost) {
         best_cost = cost;
@@ -316,26 +319,21 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     }
     p->prefix_chunk = static_cast<int>(best * tile);
     p->prefix_splits = static_cast<int>((tiles + best - 1) / best);
-    st = plan_splits(B, Hkv, Hq / Hkv, capacity - prefix_len, block_size, num_splits, &p->own);
-    if (st != RRA_OK) return st;
+    if (p->prefix_splits > 65535) return RRA_ERANGE;
   }
-  return p->prefix_splits + p->own.splits > kSharedMaxPartials ? RRA_ERANGE : RRA_OK;
+  return plan_splits(B, Hkv, n_rep, capacity - (pass ? prefix_len : 0), block_size, num_splits, &p->own);
 }
 
-// Workspace of shared-prefix attention: arrival counters, one per 16 rows, in a first part of the same
-// size for every shape (so that calls of different shapes, captured or not, may take turns on one
-// workspace), then partials o [R, S, D] and (max, sum) [R, S, 2] floats (S = prefix chunks + own
-// splits), 256-byte aligned.
-constexpr size_t kSharedCounterBytes = size_t(1) << 20;
+// Workspace of shared-prefix attention: partials o [R, S, D] and (max, sum) [R, S, 2] floats, R = B gamma Hq
+// output rows, S = prefix chunks + own splits; none for S = 1. Nothing in it outlives a call.
 struct SharedWs {
-  size_t o, ml, total;
+  size_t ml, total;
 };
 SharedWs shared_ws(int64_t rows, int D, const SharedPlan& p) {
   const size_t S = size_t(p.prefix_splits) + p.own.splits;
   SharedWs w{};
   if (S <= 1 || rows <= 0) return w;
-  w.o = kSharedCounterBytes;
-  w.ml = w.o + align256(rows * S * D * sizeof(float));
+  w.ml = align256(rows * S * D * sizeof(float));
   w.total = w.ml + rows * S * 2 * sizeof(float);
   return w;
 }
@@ -447,6 +445,29 @@ int encode_pool_map(CUtensorMap* map, const void* pool, int num_blocks, int bloc
   const cuuint64_t strides[3] = {D * es, cuuint64_t(Hkv) * D * es, cuuint64_t(block_size) * Hkv * D * es};
   const cuuint32_t box[4] = {cuuint32_t(mma ? 64 : D), 1u, cuuint32_t(box_rows), 1u};
   return encode_map(map, pool, 4, dims, strides, box, dt, mma);
+}
+
+// The pools for the shared-prefix kernel: 5-D {64 dims, 8 rows, halves, groups of 8 rows of the whole pool, Hkv},
+// the box box_rows rows of one head (128-byte swizzle: every group of 8 rows and half is one 1 KB atom).
+int encode_group_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size, int Hkv, int D, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
+    return RRA_ECUDA;
+  }
+  const cuuint64_t row = cuuint64_t(Hkv) * D * 2;  // bytes of a token
+  const cuuint64_t dims[5] = {64u, 8u, cuuint64_t(D / 64), cuuint64_t(num_blocks) * (block_size / 8), cuuint64_t(Hkv)};
+  const cuuint64_t strides[4] = {row, 128u, 8 * row, cuuint64_t(D) * 2};
+  const cuuint32_t box[5] = {64u, 8u, cuuint32_t(D / 64), cuuint32_t(box_rows / 8), 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(pool), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
+    return RRA_ECUDA;
+  }
+  return RRA_OK;
 }
 
 // Contiguous cache [B, Hkv, max_len, D] as 3-D {D, max_len, B*Hkv}, boxes of 64 dims x tile rows.
@@ -1303,15 +1324,20 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   if (!q_rot || !k_pool || !v_pool || !block_table || (!seq_lens && !positions) || !out) return RRA_EINVAL;
   if (prefix_len > 0 && !prefix_blocks) return RRA_EINVAL;
   if (!aligned16(q_rot) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return RRA_EINVAL;
-  const int64_t rows = verify_rows(B, gamma, Hq, Hkv);
-  if (rows > int64_t(16 * kSharedCounterBytes / sizeof(int))) return RRA_ERANGE;
+  const int64_t rows = int64_t(B) * gamma * Hq;
+  if (rows > INT32_MAX) return RRA_ERANGE;
   const SharedWs w = shared_ws(rows, D, p);
   if (w.total > 0 && (workspace == nullptr || ws_bytes < w.total || !aligned16(workspace))) return RRA_EWORKSPACE;
   if (check_only) return RRA_OK;
-  CUtensorMap km, vm;
+  CUtensorMap km, vm, kg{}, vg{};
   const int box_rows = block_size < p.own.tile ? block_size : p.own.tile;
   st = encode_pool_map(&km, k_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
   if (st == RRA_OK) st = encode_pool_map(&vm, v_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
+  if (st == RRA_OK && p.prefix_splits > 0) {
+    const int group_rows = std::min(block_size, rra::kSharedPrefixTile);
+    st = encode_group_map(&kg, k_pool, num_blocks, block_size, Hkv, D, group_rows);
+    if (st == RRA_OK) st = encode_group_map(&vg, v_pool, num_blocks, block_size, Hkv, D, group_rows);
+  }
   if (st != RRA_OK) return st;
   rra::DecodeArgs a{};
   a.q = q_rot;
@@ -1325,8 +1351,7 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   a.num_blocks = num_blocks;
   a.out = out;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  a.counters = reinterpret_cast<int*>(base);
-  a.ws_o = reinterpret_cast<float*>(base + w.o);
+  a.ws_o = reinterpret_cast<float*>(base);
   a.ws_ml = reinterpret_cast<float*>(base + w.ml);
   a.B = B;
   a.Hq = Hq;
@@ -1345,7 +1370,7 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
   a.scale_log2 = s * 1.4426950408889634f;
   a.err = err_flag;
-  return finish_decode(rra::launch_shared_prefix(a, km, vm, static_cast<cudaStream_t>(stream)));
+  return finish_decode(rra::launch_shared_prefix(a, km, vm, kg, vg, static_cast<cudaStream_t>(stream)));
 }
 
 int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq,
@@ -1355,8 +1380,8 @@ int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_
   const int st = make_plan_shared(B, gamma, Hq, Hkv, D, prefix_len, max_blocks_per_seq, block_size, num_splits,
                                   prefix_splits, &p);
   if (st != RRA_OK) return st;
-  const int64_t rows = verify_rows(B, gamma, Hq, Hkv);
-  if (rows > int64_t(16 * kSharedCounterBytes / sizeof(int))) return RRA_ERANGE;
+  const int64_t rows = int64_t(B) * gamma * Hq;
+  if (rows > INT32_MAX) return RRA_ERANGE;
   if (own_splits != nullptr) *own_splits = p.own.splits;
   if (prefix_chunks != nullptr) *prefix_chunks = p.prefix_splits;
   if (workspace_bytes != nullptr) *workspace_bytes = shared_ws(rows, D, p).total;

@@ -1,25 +1,36 @@
 // Attention of a whole batch over a prefix that all its sequences share, on the fifth-generation
-// tensor cores: the prefix part of rra_shared_prefix_attn.
+// tensor cores, and the merge of its partials with those of the sequences' own tokens: the parts of
+// rra_shared_prefix_attn that are not the decode and verify kernels.
 //
 // Softmax over the tokens [0, n) splits at the prefix length P by log-sum-exp: with m_i, l_i, o_i
 // the maximum, the sum and the unnormalised output over part i, out = sum 2^(m_i - M) o_i / sum
 // 2^(m_i - M) l_i. The part [0, P) has the same K and V for every sequence, so for one KV head it is
 // the attention of B x gamma x n_rep query rows over P keys: a pair of matrix products whose K and V
-// are read once for all the rows. The part [P, n) is decode_verify_kernel<SHARED> (verify.cuh),
-// which also merges the partials.
+// are read once for all the rows. The part [P, n) is decode_mma_kernel<SHARED> (one new token) or
+// decode_verify_kernel<SHARED> (more). Every part leaves (o, m, l) in a slot of the row; one warp per
+// row merges the slots (shared_merge_kernel).
 //
-// One CTA takes 128 of those rows (M of every MMA) and a chunk of the prefix. Q, S, P and O live in
-// Tensor Memory, so shared memory holds nothing but a ring of K and V tiles of 16 KB (64 keys at
-// head dim 128, 128 keys at 64; TMA, 128-byte swizzle, 64-dim halves) and two CTAs fit an SM. For
-// key tile j:
-//   S = Q K_j^T     D / 16 MMAs (M 128, N kTile, K 16), Q the A operand from Tensor Memory
-//   softmax         warps 0-3, one row per thread: the S row into registers, running max (moved only
-//                   when it grows by more than 2^8), P as bf16 pairs over the S columns
-//   O += P V_j      kTile / 16 MMAs, P the A operand from Tensor Memory, V an MN-major operand
-// One lane of warp 5 issues S_0, PV_0, S_1, PV_1, ...; the MMAs run in issue order, so S_(j+1) may
-// overwrite P_j, and s_full(j + 1) also says that PV_j is complete and O may be rescaled. While one
-// CTA of an SM is in its softmax the other's MMAs run. P is rounded to bf16 (2^-8 of each weight,
-// below what the bf16 output keeps); maxima, sums and O stay in float32.
+// A prefix CTA takes one or two tiles of 128 of those rows (M of the MMAs) and a chunk of the prefix, in
+// key tiles of 64. K and V tiles (16 KB at head dim 128) arrive by TMA through boxes of {64 dims, 8
+// rows, D / 64 halves, block rows / 8}: a block of 16 tokens is one 4 KB copy and every 8-row group of
+// the tile lies at the same stride whatever the block size, as the MMA descriptors want it. (One CTA's
+// copies move small boxes slowly: two copies of 2 KB per block instead cost ## us against ## us.)
+// For row tile k and key tile j (item i):
+//   S = Q_k K_j^T     D / 16 MMAs (M 128, N 64, K 16) into Tensor Memory
+//   softmax           warpgroup k, one row per thread: the S row into registers, running max (moved only
+//                     when it grows by more than 2^8), P as bf16 pairs over the S columns
+//   O_k += P V_j      4 MMAs (M 128, N D, K 16), P the A operand from Tensor Memory, V MN-major
+// P is rounded to bf16 (half a step, 2^-8 of each weight, below what the bf16 output keeps); maxima,
+// sums and O stay in float32.
+//
+// Two shapes of CTA:
+// * NQ = 1 (up to 128 rows per KV head): Q in Tensor Memory, 256 of its columns, two CTAs per SM: while
+//   one is in its softmax the other's MMAs run, and two CTAs' copies together keep up with HBM,
+//   which bounds this case (the prefix is read once).
+// * NQ = 2 (more rows): one CTA per SM, K and V serve 256 rows, Q in shared memory, four S buffers:
+//   S of the next two items of a tile is ready before its softmax asks for it, so the two
+//   softmax warpgroups (the special-function units) run without pause. Bound: those units, 64 x 128 ex2
+//   per item at 16 a clock (512 clocks), against 640 clocks of MMAs with Q from shared memory.
 //
 // Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain); the MMA lane waits for
 // its last commit and the producer for its last copies before Tensor Memory is released.
@@ -27,39 +38,55 @@
 
 #include "decode_mma.cuh"
 #include "tcgen05.cuh"
-#include "verify.cuh"
 
 namespace rra {
 namespace spx {
 
-constexpr int kRows = kSharedPrefixRows;        // M of every MMA
-constexpr int kRing = 6;                        // K / V tile slots (K_0, V_0, K_1, V_1, ...)
-constexpr uint32_t kTmemCols = 256;             // two CTAs per SM share its 512 columns
+constexpr int kRows = kSharedPrefixRows;        // rows of a tile: M of every MMA
+constexpr int kTile = kSharedPrefixTile;        // keys per tile
 constexpr float kRescaleLog2 = 8.f;             // move the running max only when it grows by more
-constexpr int kSoftmaxThreads = 128;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = kSoftmaxThreads + 64;
 
-template <int D>
+template <int D, int NQ>
 struct Cfg {
-  static constexpr int kTile = 8192 / D;                   // keys per tile
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalfBytes = kTile * 128;
-  static constexpr int kTileBytes = kHalves * kHalfBytes;  // 16 KB
-  static constexpr uint32_t kColO = 0;                     // O: D columns
-  static constexpr uint32_t kColS = D;                     // S: kTile columns; P over its first half
-  static constexpr uint32_t kColQ = D + kTile;             // Q as bf16 pairs: D / 2 columns
-  static constexpr int kOffBar = kRing * kTileBytes;
-  // q_ready, ring_full[kRing], ring_empty[kRing], s_full, p_full, mma_done
-  static constexpr int kNumBars = 1 + 2 * kRing + 3;
+  static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
+  static constexpr int kTileBytes = kTile / 8 * kGroupBytes;
+  static constexpr int kQHalfBytes = kRows * 128;          // NQ 2: Q tiles, K-major, 64-dim halves
+  static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
+  static constexpr int kBufs = NQ == 2 ? 4 : 1;            // S buffers
+  static constexpr int kAhead = NQ == 2 ? 2 : 1;           // key tiles whose S goes out before the first P.V
+  static constexpr int kKSlots = NQ == 2 ? 5 : 3, kVSlots = NQ == 2 ? 4 : 3;
+  // Tensor Memory columns
+  static constexpr uint32_t kColO = 0;                     // O_k: D columns each
+  static constexpr uint32_t kColS = NQ * D;                // S buffers of kTile columns, P over their first half
+  static constexpr uint32_t kColQ = kColS + kBufs * kTile; // NQ 1: Q as bf16 pairs, D / 2 columns
+  static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
+  // shared memory
+  static constexpr int kOffK = kQBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kTileBytes;
+  static constexpr int kOffBar = kOffV + kVSlots * kTileBytes;
+  // q_ready, k_full, k_empty, v_full, v_empty, s_full[kBufs], p_full[kBufs], o_done[NQ], mma_done
+  static constexpr int kNumBars = 1 + 2 * kKSlots + 2 * kVSlots + 2 * kBufs + NQ + 1;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffTable = kOffTmemSlot + 16;
   static constexpr int kSmemBytes = 1024 + kOffTable + kSharedPrefixTableEntries * 4;
+  static constexpr int kSoftmaxThreads = 128 * NQ;
+  static constexpr int kThreads = kSoftmaxThreads + 64;    // + producer warp + MMA warp
+  static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
   static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kRows, kTile, false);  // Q (K-major) . K^T (K-major)
   static constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kRows, D, true);      // P (K-major) . V (MN-major)
-  static_assert(kColQ + D / 2 <= kTmemCols, "Tensor Memory columns");
-  static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert((NQ == 2 ? kColQ : kColQ + D / 2) <= kTmemCols, "Tensor Memory columns");
+  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the SM");
 };
+
+__device__ __forceinline__ void tma_g2s_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -94,45 +121,50 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&s)[N]) 
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+// L_b of sequence b, cut to the cache; the caller flags what is out of range.
+__device__ __forceinline__ int attended_length(const DecodeArgs& a, int b) {
+  const int L = a.positions != nullptr ? __ldcg(a.positions + b) + a.gamma : __ldcg(a.seq_lens + b);
+  return min(max(L, 0), a.capacity);
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
-  using C = Cfg<D>;
-  constexpr int kTile = C::kTile;
+  using C = Cfg<D, NQ>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
   const int g = blockIdx.z, split = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducerWarp = 4 * NQ, kMmaWarp = 4 * NQ + 1;
   const int start = split * a.prefix_chunk;
   const int end = min(a.prefix_len, start + a.prefix_chunk);
   const int n_tiles = (end - start + kTile - 1) / kTile;
   const int last_valid = end - start - (n_tiles - 1) * kTile;  // keys of the last tile
 
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* q_ready = bars;
-  uint64_t* ring_full = bars + 1;
-  uint64_t* ring_empty = ring_full + kRing;
-  uint64_t* s_full = ring_empty + kRing;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* mma_done = p_full + 1;
+  uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_full = q_ready + 1;
+  uint64_t* k_empty = k_full + C::kKSlots;
+  uint64_t* v_full = k_empty + C::kKSlots;
+  uint64_t* v_empty = v_full + C::kVSlots;
+  uint64_t* s_full = v_empty + C::kVSlots;
+  uint64_t* p_full = s_full + C::kBufs;
+  uint64_t* o_done = p_full + C::kBufs;
+  uint64_t* mma_done = o_done + NQ;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::kOffTable);
 
   if (threadIdx.x == 0) {
-    mbar_init(q_ready, kSoftmaxThreads);
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(&ring_full[s], 1);
-      mbar_init(&ring_empty[s], 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kSoftmaxThreads);
+    mbar_init(q_ready, C::kSoftmaxThreads);
+    for (int s = 0; s < 2 * C::kKSlots + 2 * C::kVSlots + C::kBufs; ++s) mbar_init(&k_full[s], 1);
+    for (int s = 0; s < C::kBufs; ++s) mbar_init(&p_full[s], 128);
+    for (int k = 0; k < NQ; ++k) mbar_init(&o_done[k], 1);
     mbar_init(mma_done, 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
-    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_alloc(tmem_slot, C::kTmemCols);
     tc::tmem_relinquish();
     tc::fence_before_sync();
   }
@@ -143,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int first_blk = start >> a.log2_bs;
   {
     const int n_blk = ((end - 1) >> a.log2_bs) - first_blk + 1;
-    for (int i = threadIdx.x; i < n_blk; i += kThreads) {
+    for (int i = threadIdx.x; i < n_blk; i += C::kThreads) {
       int id = a.prefix_blocks[first_blk + i];
       if (id < 0 || id >= a.num_blocks) {
         flag_error(a.err, RRA_ERR_BLOCK_ID);
@@ -155,9 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // ring position r: K of tile r / 2 (r even) or its V (r odd), in slot r % kRing
-  auto slot_of = [](int r) { return r % kRing; };
-  auto phase_of = [](int r) { return static_cast<uint32_t>((r / kRing) & 1); };
+  // item i: row tile i % NQ, key tile i / NQ, S buffer i % kBufs
+  auto ring_phase = [](int j, int slots) { return static_cast<uint32_t>((j / slots) & 1); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
@@ -165,73 +196,90 @@ __global__ void __launch_bounds__(kThreads, 2)
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
     }
-    const int bs = 1 << a.log2_bs;
+    const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
     const int box = min(bs, kTile);  // rows per TMA box, as the tensor maps were encoded
-    int issued = 0;
-    for (int r = 0; r < 2 * n_tiles; ++r) {
-      const int s = slot_of(r);
-      const int tile0 = start + (r >> 1) * kTile;
+    // tile j of K or V into its slot; false once a wait ran out
+    auto load = [&](const CUtensorMap* map, int off, uint64_t* full, uint64_t* empty, int slots, int j) -> bool {
+      const int s = j % slots, tile0 = start + j * kTile;
       const int nbox = (min(kTile, end - tile0) + box - 1) / box;
       int ok = 1;
       if (lane == 0) {
-        if (r >= kRing && !mbar_wait(&ring_empty[s], phase_of(r) ^ 1u))
+        if (j >= slots && !mbar_wait(&empty[s], ring_phase(j, slots) ^ 1u))
           ok = 0;
         else
-          mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
+          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      const CUtensorMap* map = (r & 1) ? &v_map : &k_map;
-      uint8_t* dst = smem + s * C::kTileBytes;
-      for (int c = lane; c < C::kHalves * nbox; c += 32) {  // (box, half) copies, from all lanes at once
-        const int bx = c / C::kHalves, hf = c % C::kHalves;
-        const int t = tile0 + bx * box;
-        tma_g2s_4d(dst + hf * C::kHalfBytes + bx * box * 128, map, 64 * hf, g, t & (bs - 1),
-                   tbl[(t >> a.log2_bs) - first_blk], &ring_full[s]);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      if (lane < nbox) {  // one copy per lane (at most 8)
+        const int t = tile0 + lane * box;
+        const int rows8 = (tbl[(t >> log2_bs) - first_blk] << (log2_bs - 3)) + ((t & (bs - 1)) >> 3);
+        tma_g2s_5d(smem + off + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, map, 0, 0, 0, rows8, g, &full[s]);
       }
       __syncwarp();
-      issued = r + 1;
+      return true;
+    };
+    // in the order the MMAs take them: K_0 .. K_(kAhead - 1), V_0, K_kAhead, V_1, ...
+    int nk = 0, nv = 0;
+    bool ok = true;
+    for (int t = 0; ok && t < n_tiles + C::kAhead; ++t) {
+      if (t < n_tiles && (ok = load(&k_map, C::kOffK, k_full, k_empty, C::kKSlots, t))) ++nk;
+      if (ok && t >= C::kAhead - 1 && nv < n_tiles && nv <= t - (C::kAhead - 1) &&
+          (ok = load(&v_map, C::kOffV, v_full, v_empty, C::kVSlots, nv)))
+        ++nv;
     }
     if (lane == 0) {
-      if (issued < 2 * n_tiles) flag_error(a.err, RRA_ERR_TIMEOUT);
+      if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       // no copy may still be landing when the CTA exits
-      for (int r = max(issued - kRing, 0); r < issued; ++r) mbar_wait(&ring_full[slot_of(r)], phase_of(r));
+      for (int j = max(nk - C::kKSlots, 0); j < nk; ++j) mbar_wait(&k_full[j % C::kKSlots], ring_phase(j, C::kKSlots));
+      for (int j = max(nv - C::kVSlots, 0); j < nv; ++j) mbar_wait(&v_full[j % C::kVSlots], ring_phase(j, C::kVSlots));
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
     if (lane == 0) {
-      const uint32_t ring_base = smem_addr(smem);
+      const uint32_t base = smem_addr(smem);
+      const int n_items = NQ * n_tiles;
       bool ok = mbar_wait(q_ready, 0);
       tc::fence_after_sync();
-      auto issue_s = [&](int j) -> bool {
-        const int r = 2 * j;
-        if (!mbar_wait(&ring_full[slot_of(r)], phase_of(r))) return false;
-        tc::fence_after_sync();
-        const uint32_t k_base = ring_base + slot_of(r) * C::kTileBytes;
+      auto issue_s = [&](int i) -> bool {
+        const int k = i % NQ, j = i / NQ, s = j % C::kKSlots;
+        if (k == 0) {
+          if (!mbar_wait(&k_full[s], ring_phase(j, C::kKSlots))) return false;
+          tc::fence_after_sync();
+        }
+        const uint32_t k_base = base + C::kOffK + s * C::kTileBytes;
+        const uint32_t col = tmem + C::kColS + kTile * (i % C::kBufs);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_bf16_ts(tmem + C::kColS, tmem + C::kColQ + 8 * kk,
-                          tc::sw128_desc(k_base + (kk >> 2) * C::kHalfBytes + (kk & 3) * 32, 1024, 1024), C::kIdescS,
-                          kk > 0 ? 1u : 0u);
-        tc::commit(s_full);
-        tc::commit(&ring_empty[slot_of(r)]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * 1024 + (kk & 3) * 32, 1024, C::kGroupBytes);
+          if constexpr (NQ == 2)
+            tc::mma_bf16_ss(col, tc::sw128_desc(base + (k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32,
+                                                1024, 1024),
+                            kd, C::kIdescS, kk > 0 ? 1u : 0u);
+          else
+            tc::mma_bf16_ts(col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(&s_full[i % C::kBufs]);
+        if (k == NQ - 1) tc::commit(&k_empty[s]);
         return true;
       };
-      if (ok) ok = issue_s(0);
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        const int rv = 2 * j + 1;
-        if (!mbar_wait(&ring_full[slot_of(rv)], phase_of(rv)) || !mbar_wait(p_full, j & 1)) {
+      for (int i = 0; ok && i < C::kBufs && i < n_items; ++i) ok = issue_s(i);
+      for (int i = 0; ok && i < n_items; ++i) {
+        const int k = i % NQ, j = i / NQ, s = j % C::kVSlots;
+        if ((k == 0 && !mbar_wait(&v_full[s], ring_phase(j, C::kVSlots))) || !mbar_wait(&p_full[i % C::kBufs], (i / C::kBufs) & 1)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const uint32_t v_base = ring_base + slot_of(rv) * C::kTileBytes;
+        const uint32_t v_base = base + C::kOffV + s * C::kTileBytes;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          tc::mma_bf16_ts(tmem + C::kColO, tmem + C::kColS + 8 * kk,
-                          tc::sw128_desc(v_base + kk * 2048, C::kHalfBytes, 1024), C::kIdescPV,
+          tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * (i % C::kBufs) + 8 * kk,
+                          tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV,
                           (j > 0 || kk > 0) ? 1u : 0u);
-        tc::commit(&ring_empty[slot_of(rv)]);
-        if (j + 1 < n_tiles) ok = issue_s(j + 1);
+        tc::commit(&o_done[k]);
+        if (k == NQ - 1) tc::commit(&v_empty[s]);
+        // the MMAs run in issue order: S of this buffer's next item may overwrite P
+        if (i + C::kBufs < n_items) ok = issue_s(i + C::kBufs);
       }
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       tc::commit(mma_done);  // every MMA issued above has completed once this arrives
@@ -239,67 +287,77 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else {
     // ------------------------------------------------------------------ softmax: thread = query row
+    const int k = warp >> 2;                               // row tile of this warpgroup
+    const int r = static_cast<int>(threadIdx.x) & 127;     // row = TMEM lane
     const int n_rep = a.Hq / a.Hkv;
-    const int row = blockIdx.x * kRows + static_cast<int>(threadIdx.x);
+    const int row = (blockIdx.x * NQ + k) * kRows + r;
     const bool real = row < a.B * a.gamma * n_rep;
     const bool warp_real = __any_sync(0xffffffffu, real);
     const int bt = real ? row / n_rep : 0;                 // token bt = b * gamma + j of the batch
-    const int i = real ? row - bt * n_rep : 0;             // head of the group
-    const int b = bt / a.gamma, j_new = bt - b * a.gamma;
+    const int i_head = real ? row - bt * n_rep : 0;        // head of the group
+    const size_t out_row = static_cast<size_t>(bt) * a.Hq + g * n_rep + i_head;
     // keys of the prefix that the row attends
     int lim = a.prefix_len;
     if (real) {
-      int L = a.positions != nullptr ? a.positions[b] + a.gamma : a.seq_lens[b];
-      L = min(max(L, 0), a.capacity);
-      lim = min(max(L - a.gamma + 1 + j_new, 0), a.prefix_len);
+      const int b = bt / a.gamma, j_new = bt - b * a.gamma;
+      lim = min(max(attended_length(a, b) - a.gamma + 1 + j_new, 0), a.prefix_len);
     }
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-    const uint32_t s_col = tmem + lane_base + C::kColS, o_col = tmem + lane_base + C::kColO;
-    {  // the query row into Tensor Memory: dims (2c, 2c + 1) in column kColQ + c
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                        (static_cast<size_t>(bt) * a.Hq + g * n_rep + i) * D);
-      uint32_t qw[D / 2];
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t o_col = tmem + lane_base + C::kColO + D * k;
+    {  // the query row
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + out_row * D);
+      uint4 qv[D / 8];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        qw[4 * c] = x.x;
-        qw[4 * c + 1] = x.y;
-        qw[4 * c + 2] = x.z;
-        qw[4 * c + 3] = x.w;
+      for (int c = 0; c < D / 8; ++c) qv[c] = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (NQ == 2) {  // into the Q tile (K-major, 128-byte swizzle)
+        uint8_t* dst = smem + k * C::kHalves * C::kQHalfBytes + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kQHalfBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
+        tc::fence_smem_to_async();
+      } else {  // into Tensor Memory: dims (2c, 2c + 1) in column kColQ + c
+        uint32_t qw[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          qw[4 * c] = qv[c].x;
+          qw[4 * c + 1] = qv[c].y;
+          qw[4 * c + 2] = qv[c].z;
+          qw[4 * c + 3] = qv[c].w;
+        }
+        st_cols<D / 2>(tmem + lane_base + C::kColQ, qw);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
       }
-      st_cols<D / 2>(tmem + lane_base + C::kColQ, qw);
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
       mbar_arrive(q_ready);
     }
     const float sl = a.scale_log2;
     float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      if (!warp_wait(s_full, j & 1)) {  // S_j is there, and P.V of tile j - 1 is complete
+      const int i = j * NQ + k, buf = i % C::kBufs;
+      if (!warp_wait(&s_full[buf], (i / C::kBufs) & 1)) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      if (j == n_tiles - 1 && last_valid < kTile) {
-        // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0
-        const int rv = 2 * j + 1;
-        if (!warp_wait(&ring_full[slot_of(rv)], phase_of(rv))) {
+      if (k == 0 && j == n_tiles - 1 && last_valid < kTile) {
+        // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0 (row
+        // tile 0's P.V reads this V first)
+        if (!warp_wait(&v_full[j % C::kVSlots], ring_phase(j, C::kVSlots))) {
           ok = false;
           break;
         }
-        const int r = static_cast<int>(threadIdx.x);
         if (r >= last_valid && r < kTile) {
-          uint8_t* vrow = smem + slot_of(rv) * C::kTileBytes + r * 128;
+          uint8_t* vrow = smem + C::kOffV + (j % C::kVSlots) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<uint4*>(vrow + h * C::kHalfBytes + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+            for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + h * 1024 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
         }
         tc::fence_smem_to_async();
       }
       if (warp_real) {
+        const uint32_t s_col = tmem + lane_base + C::kColS + kTile * buf;
         uint32_t sv[kTile];
         ld_cols<kTile>(s_col, sv);
         const int vis = min(lim, end) - (start + j * kTile);  // columns this row attends
@@ -334,6 +392,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         st_cols<kTile / 2>(s_col, pw);
         l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
         if (j > 0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
+          if (!warp_wait(&o_done[k], (j - 1) & 1)) {      // the P.V before this one (that of j - 2 is complete)
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -347,13 +410,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::tmem_wait_st();
       }
       tc::fence_before_sync();
-      mbar_arrive(p_full);
+      mbar_arrive(&p_full[buf]);
     }
     // ------------------------------------------------------------------ epilogue: this chunk's partial rows
-    if (ok && warp_wait(mma_done, 0)) {
+    // (the barrier may be two phases from the last one: S runs two items ahead)
+    if (ok && (n_tiles < 2 || warp_wait(&o_done[k], (n_tiles - 2) & 1)) && warp_wait(&o_done[k], (n_tiles - 1) & 1)) {
       tc::fence_after_sync();
-      const SharedRows rows{a.Hkv, n_rep, a.hpc, a.gamma};
-      const size_t ps = rows(b, g, i, j_new) * a.num_splits + split;
+      const size_t ps = out_row * a.num_splits + split;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -375,20 +438,90 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, kTmemCols);
+    tc::tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
+// One warp per output row: the prefix_splits partials of the prefix and those of the sequence's own
+// chunks that hold tokens. Rows of a sequence whose position is refused are not written.
+constexpr int kMergeWarps = 4;
+
 template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const DecodeArgs a) {
+  constexpr int E = D / 32;  // dims per lane
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(a.B) * a.gamma * a.Hq) return;
+  const int b = static_cast<int>(row / (static_cast<int64_t>(a.gamma) * a.Hq));
+  if (a.positions != nullptr) {
+    const int p0 = a.positions[b];
+    if (p0 < a.prefix_len || p0 + a.gamma > a.capacity) return;
+  }
+  const int L = attended_length(a, b);
+  const int n = a.prefix_splits + (max(L - a.first_token, 0) + a.chunk - 1) / a.chunk;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
+  const float* o = a.ws_o + row * a.num_splits * D + lane * E;
+  float M = -INFINITY, l = 0.f;  // over the partials taken so far
+  float acc[E] = {};
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const float2 x = s0 + lane < n ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
+    float m = x.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = fmaxf(m, M);
+    const float mref = m == -INFINITY ? 0.f : m;
+    const float w = ex2(x.x - mref), keep = ex2(M - mref);
+    float ls = w * x.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    l = l * keep + ls;
+    M = m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+    const int count = min(32, n - s0);
+#pragma unroll 8
+    for (int s = 0; s < count; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+      const float* p = o + static_cast<size_t>(s0 + s) * D;
+      if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+        acc[0] = fmaf(ws, v.x, acc[0]);
+        acc[1] = fmaf(ws, v.y, acc[1]);
+        acc[2] = fmaf(ws, v.z, acc[2]);
+        acc[3] = fmaf(ws, v.w, acc[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+        acc[0] = fmaf(ws, v.x, acc[0]);
+        acc[1] = fmaf(ws, v.y, acc[1]);
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int D, int NQ>
 cudaError_t launch_prefix(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  using C = Cfg<D, NQ>;
   static int done[64] = {0};
-  auto kern = shared_prefix_kernel<D>;
-  cudaError_t e = ensure_smem(kern, Cfg<D>::kSmemBytes, done);
+  auto kern = shared_prefix_kernel<D, NQ>;
+  cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   // row tiles innermost: CTAs that read the same keys run side by side and share them through L2
   const int rows = a.B * a.gamma * (a.Hq / a.Hkv);
-  const dim3 grid((rows + kRows - 1) / kRows, a.prefix_splits, a.Hkv);
-  return launch_pdl(kern, grid, dim3(kThreads), Cfg<D>::kSmemBytes, st, km, vm, a);
+  const dim3 grid((rows + NQ * kRows - 1) / (NQ * kRows), a.prefix_splits, a.Hkv);
+  return launch_pdl(kern, grid, dim3(C::kThreads), C::kSmemBytes, st, km, vm, a);
+}
+
+template <int D>
+cudaError_t launch_merge(const DecodeArgs& a, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.gamma * a.Hq;
+  const dim3 grid(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  return launch_pdl(shared_merge_kernel<D>, grid, dim3(32 * kMergeWarps), 0, st, a);
 }
 
 }  // namespace spx

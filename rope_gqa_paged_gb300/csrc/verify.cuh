@@ -215,36 +215,6 @@ struct VerifyRows {
   }
 };
 
-// Shared prefix: the partial row of new token j, head i of KV head g's group, of sequence b (the
-// inverse of VerifyRows).
-struct SharedRows {
-  int Hkv, n_rep, hpc, gamma;
-  __device__ size_t operator()(int b, int g, int i, int j) const {
-    const int slice = i / hpc;
-    return ((static_cast<size_t>(b) * Hkv + g) * (n_rep / hpc) + slice) * kVerifyRows + (i - slice * hpc) * gamma + j;
-  }
-};
-
-// Shared prefix: waits for the prefix's partials, then merges them with the n_work partials of the
-// sequence's own chunks (slots [0, prefix_splits + n_work) of its rows) into the output; zero rows
-// where there is none. Called by all nthreads consumer threads of one CTA of the rows.
-template <int D>
-__device__ __forceinline__ void merge_shared(const DecodeArgs& a, size_t row0, int rows, int n_work, uint8_t* ring,
-                                             int ring_bytes, VerifyRows out_row, int nthreads) {
-  const int tid = threadIdx.x, count = a.prefix_splits + n_work;
-  if (count == 0) {
-    for (int i = tid; i < rows * D; i += nthreads)
-      static_cast<__nv_bfloat16*>(a.out)[out_row(row0 + i / D) * D + i % D] = __float2bfloat16_rn(0.f);
-    return;
-  }
-  pdl_wait();
-  float* scratch = reinterpret_cast<float*>(ring);
-  if (!merge_partials_bulk<__nv_bfloat16, D>(a, a.ws_o, a.ws_ml, a.num_splits, 0, count, rows, row0, nullptr, nullptr,
-                                             0, 0, scratch, ring_bytes, tid, nthreads, out_row))
-    merge_partials<__nv_bfloat16, D, VerifyRows, false>(a, a.ws_o, a.ws_ml, a.num_splits, 0, count, rows, row0, nullptr,
-                                                        nullptr, 0, 0, scratch, tid, nthreads, out_row);
-}
-
 // FUSED: the whole verify step in this launch. a.q holds the unrotated q of the gamma new tokens
 // (gamma <= kVerifyFusedMaxGamma); the consumer warps take sin/cos of the gamma positions once per
 // CTA (rope_cos_sin, as the decode step), rotate their query rows in registers, and split-0
@@ -253,12 +223,14 @@ __device__ __forceinline__ void merge_shared(const DecodeArgs& a, size_t row0, i
 // with one arrival per token) before the TMA of the first tile that holds a new token. Head-slice
 // CTAs of that chunk write identical bytes.
 //
-// SHARED: the sequences' own tokens of shared-prefix attention, [first_token, L_b). The kernel
-// before it (shared_prefix.cuh) may still be computing the prefix's partials: this one reads only
-// what that kernel's predecessors wrote (past L1; that kernel let it start after it had waited for
-// them) and waits for it before the merge, which the last split of a sequence's rows makes of the
-// prefix's partials and its own, in one level. Lengths may be given (seq_lens; query token j attends
-// the first L_b - gamma + 1 + j tokens, none if that is not positive: a zero row).
+// SHARED: the sequences' own tokens of shared-prefix attention, [first_token, L_b). Every split
+// leaves its partial in slot prefix_splits + split of the output row's num_splits slots (a merge
+// kernel follows), or writes the row when there is one slot. The kernel before this one
+// (shared_prefix.cuh) may still be computing the prefix's partials: this one reads only what that
+// kernel's predecessors wrote (past L1; that kernel let it start after it had waited for them), and
+// its first CTA waits for that kernel, so that the merge finds both complete. Lengths may be given
+// (seq_lens; query token j attends the first L_b - gamma + 1 + j tokens, none if that is not
+// positive: a zero row).
 template <int D, bool PAGED, bool FUSED = false, bool SHARED = false>
 __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     decode_verify_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -301,20 +273,19 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     L = p0 + gamma;
     if (p0 < (SHARED ? a.prefix_len : 0) || L > a.capacity) {
       if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
-      if (SHARED) pdl_wait();  // this kernel does not end before the one before it
+      if (SHARED) shared_wait_first(a);
       return;
     }
   }
-  const int n_work = SHARED ? max(L - a.first_token + a.chunk - 1, 0) / a.chunk : (L + a.chunk - 1) / a.chunk;
-  if constexpr (SHARED) {
-    if (split >= max(n_work, 1)) return;
-    if (n_work == 0) {  // no token of its own: the prefix's partials alone (zero rows without any)
-      if (threadIdx.x < C::kConsumerWarps * 32)
-        merge_shared<D>(a, vbase, rows, 0, smem, C::kRingBytes, out_row, C::kConsumerWarps * 32);
-      return;
+  const int n_work = (L + a.chunk - 1) / a.chunk;
+  if (start >= L) {
+    if constexpr (SHARED) {
+      if (a.num_splits == 1)  // no merge kernel: the empty sequence's rows are zero
+        for (int i = threadIdx.x; i < rows * D; i += blockDim.x)
+          static_cast<__nv_bfloat16*>(a.out)[out_row(vbase + i / D) * D + i % D] = __float2bfloat16_rn(0.f);
+      shared_wait_first(a);
     }
-  } else {
-    if (start >= L) return;
+    return;
   }
   const int end = min(L, start + a.chunk);
   const int n_tiles = (end - start + C::kTile - 1) / C::kTile;
@@ -402,6 +373,7 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     if (lane == 0)
       for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
         mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1);
+    if constexpr (SHARED) shared_wait_first(a);
     return;
   }
 
@@ -574,10 +546,11 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
 #pragma unroll
     for (int w = 0; w < C::kConsumerWarps; ++w)
       osum = fmaf(red_w[w * kVerifyRows + r], red_o[(w * kVerifyRows + r) * kRS + d], osum);
-    if (n_work == 1 && (!SHARED || a.prefix_splits == 0)) {
+    if (SHARED ? a.num_splits == 1 : n_work == 1) {
       static_cast<__nv_bfloat16*>(a.out)[out_row(vbase + r) * D + d] = __float2bfloat16_rn(lsum > 0.f ? osum / lsum : 0.f);
     } else {
-      const size_t ps = (vbase + r) * a.num_splits + (SHARED ? a.prefix_splits : 0) + split;
+      const size_t ps = SHARED ? out_row(vbase + r) * a.num_splits + a.prefix_splits + split
+                               : (vbase + r) * a.num_splits + split;
       a.ws_o[ps * D + d] = osum;
       if (d == 0) {
         a.ws_ml[2 * ps] = Mx;
@@ -585,16 +558,13 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
       }
     }
   }
-  if constexpr (SHARED) {
-    __shared__ int s_last;
-    if (n_work + a.prefix_splits > 1 &&
-        arrive_last(a.counters + vbase / kVerifyRows, n_work, &s_last, a.err, threadIdx.x, kConsumers))
-      merge_shared<D>(a, vbase, rows, n_work, smem, C::kRingBytes, out_row, kConsumers);
-  } else if (n_work > 1) {
-    __shared__ int s_last;
-    finish_split_rows<__nv_bfloat16, D, VerifyRows, false>(a, vbase, rows, split, n_work,
-                                                           reinterpret_cast<float*>(smem), &s_last, threadIdx.x,
-                                                           kConsumers, out_row, C::kRingBytes);
+  if constexpr (!SHARED) {
+    if (n_work > 1) {
+      __shared__ int s_last;
+      finish_split_rows<__nv_bfloat16, D, VerifyRows, false>(a, vbase, rows, split, n_work,
+                                                             reinterpret_cast<float*>(smem), &s_last, threadIdx.x,
+                                                             kConsumers, out_row, C::kRingBytes);
+    }
   }
 }
 
