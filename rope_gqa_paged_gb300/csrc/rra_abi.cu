@@ -297,13 +297,13 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   const int64_t rows = int64_t(B) * gamma * n_rep;
   const bool pass = prefix_len > 0 && rows > 0 && (prefix_splits > 0 || (B > 1 && prefix_len >= 256));
   if (pass) {
-    const int tile = rra::kSharedPrefixTile;
+    const int nq = rra::shared_prefix_nq(rows), tile = rra::shared_prefix_tile(D, nq);
     const int64_t tiles = (prefix_len + tile - 1) / tile;
-    const int64_t per_cta = rows > rra::kSharedPrefixRows ? 2 * rra::kSharedPrefixRows : rra::kSharedPrefixRows;
+    const int64_t per_cta = nq * rra::kSharedPrefixRows;
     const int64_t units = Hkv * ((rows + per_cta - 1) / per_cta);
     const int64_t max_chunk = std::max<int64_t>(1, int64_t(rra::kSharedPrefixTableEntries) * block_size / tile);
     if (Hkv > 65535) return RRA_ERANGE;
-    const int64_t resident = (rows > rra::kSharedPrefixRows ? 1 : 2) * int64_t(std::max(1, sm_count()));
+    const int64_t resident = (nq == 2 ? 1 : 2) * int64_t(std::max(1, sm_count()));
     int64_t best = 0, best_cost = INT64_MAX;
     // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
     const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
@@ -1334,7 +1334,8 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   st = encode_pool_map(&km, k_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
   if (st == RRA_OK) st = encode_pool_map(&vm, v_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
   if (st == RRA_OK && p.prefix_splits > 0) {
-    const int group_rows = std::min(block_size, rra::kSharedPrefixTile);
+    const int nq = rra::shared_prefix_nq(int64_t(B) * gamma * (Hq / Hkv));
+    const int group_rows = std::min(block_size, rra::shared_prefix_tile(D, nq));
     st = encode_group_map(&kg, k_pool, num_blocks, block_size, Hkv, D, group_rows);
     if (st == RRA_OK) st = encode_group_map(&vg, v_pool, num_blocks, block_size, Hkv, D, group_rows);
   }

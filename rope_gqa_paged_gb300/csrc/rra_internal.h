@@ -198,12 +198,14 @@ cudaError_t launch_decode_verify(const DecodeArgs& a, const CUtensorMap& k_map, 
 // Largest gamma of the one-launch verify step.
 constexpr int kVerifyFusedMaxGammaHost = 8;
 // Shared-prefix attention (a.seq_lens or a.positions, the prefix fields, a.gamma, a.hpc set): query rows
-// of a prefix row tile, keys of a prefix tile, the most prefix blocks of one chunk.
+// of a prefix row tile, row tiles per CTA for that many rows per KV head, the most blocks of one chunk.
 constexpr int kSharedPrefixRows = 128;
-constexpr int kSharedPrefixTile = 64;
+// keys of a tile: 64 (128 at head dim 64) for one row tile per CTA, 128 for two (NQ)
+__host__ __device__ constexpr int shared_prefix_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
+__host__ __device__ constexpr int shared_prefix_nq(int64_t rows) { return rows > kSharedPrefixRows ? 2 : 1; }
 constexpr int kSharedPrefixTableEntries = 2048;
 // k_map / v_map: the pools as the decode kernels read them; k_groups / v_groups: as {64 dims, 8 rows,
-// D / 64 halves, groups of 8 rows, Hkv} with boxes of min(block size, 64) rows (prefix_splits > 0).
+// D / 64 halves, groups of 8 rows, Hkv} with boxes of min(block size, tile) rows (prefix_splits > 0).
 cudaError_t launch_shared_prefix(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                  const CUtensorMap& k_groups, const CUtensorMap& v_groups, cudaStream_t stream);
 // Prefill: causal attention of the T = a.gamma prompt tokens of each sequence (a.positions: the

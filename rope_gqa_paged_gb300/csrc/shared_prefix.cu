@@ -11,8 +11,8 @@ cudaError_t launch_d(const DecodeArgs& a, const CUtensorMap& k_map, const CUtens
                      const CUtensorMap& v_groups, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.prefix_splits > 0)
-    e = a.B * a.gamma * (a.Hq / a.Hkv) > kSharedPrefixRows ? spx::launch_prefix<D, 2>(a, k_groups, v_groups, st)
-                                                           : spx::launch_prefix<D, 1>(a, k_groups, v_groups, st);
+    e = shared_prefix_nq(int64_t(a.B) * a.gamma * (a.Hq / a.Hkv)) == 2 ? spx::launch_prefix<D, 2>(a, k_groups, v_groups, st)
+                                                                       : spx::launch_prefix<D, 1>(a, k_groups, v_groups, st);
   if (e != cudaSuccess) return e;
   if (a.gamma > 1)
     e = launch_decode_verify_t<D, true, false, true>(a, k_map, v_map, st);

@@ -11,26 +11,29 @@
 // row merges the slots (shared_merge_kernel).
 //
 // A prefix CTA takes one or two tiles of 128 of those rows (M of the MMAs) and a chunk of the prefix, in
-// key tiles of 64. K and V tiles (16 KB at head dim 128) arrive by TMA through boxes of {64 dims, 8
-// rows, D / 64 halves, block rows / 8}: a block of 16 tokens is one 4 KB copy and every 8-row group of
-// the tile lies at the same stride whatever the block size, as the MMA descriptors want it. (One CTA's
-// copies move small boxes slowly: two copies of 2 KB per block instead cost ## us against ## us.)
-// For row tile k and key tile j (item i):
-//   S = Q_k K_j^T     D / 16 MMAs (M 128, N 64, K 16) into Tensor Memory
+// key tiles. K and V tiles arrive by TMA through boxes of {64 dims, 8 rows, D / 64 halves, block rows /
+// 8}: a block of 16 tokens is one 4 KB copy, and every 8-row group of the tile lies at the same
+// stride whatever the block size, as the MMA descriptors want it. For row tile k and key tile j:
+//   S_k = Q_k K_j^T   D / 16 MMAs (M 128, N kTile, K 16) into Tensor Memory
 //   softmax           warpgroup k, one row per thread: the S row into registers, running max (moved only
 //                     when it grows by more than 2^8), P as bf16 pairs over the S columns
-//   O_k += P V_j      4 MMAs (M 128, N D, K 16), P the A operand from Tensor Memory, V MN-major
+//   O_k += P V_j      kTile / 16 MMAs (M 128, N D, K 16), P the A operand from Tensor Memory, V MN-major
 // P is rounded to bf16 (half a step, 2^-8 of each weight, below what the bf16 output keeps); maxima,
 // sums and O stay in float32.
 //
+// One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
+// so S may overwrite the P before it, and one commit per S says that everything before it is
+// complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back
+// to the producer. (A commit costs some 250 clocks between MMAs: with three per tile, and
+// tiles of 64 keys, 512 rows x 8 heads x 16384 keys took 230 us against ## us.)
+//
 // Two shapes of CTA:
-// * NQ = 1 (up to 128 rows per KV head): Q in Tensor Memory, 256 of its columns, two CTAs per SM: while
-//   one is in its softmax the other's MMAs run, and two CTAs' copies together keep up with HBM,
-//   which bounds this case (the prefix is read once).
-// * NQ = 2 (more rows): one CTA per SM, K and V serve 256 rows, Q in shared memory, four S buffers:
-//   S of the next two items of a tile is ready before its softmax asks for it, so the two
-//   softmax warpgroups (the special-function units) run without pause. Bound: those units, 64 x 128 ex2
-//   per item at 16 a clock (512 clocks), against 640 clocks of MMAs with Q from shared memory.
+// * NQ = 1 (up to 128 rows per KV head): key tiles of 64 (128 at head dim 64), Q in Tensor Memory, 256 of
+//   its columns, two CTAs per SM: while one is in its softmax the other's MMAs run, and two
+//   CTAs' copies together keep up with HBM, which bounds this case (the prefix is read once).
+// * NQ = 2 (more rows): key tiles of 128, one CTA per SM, K and V serve 256 rows, Q in shared memory; one
+//   row tile's MMAs run while the other is in its softmax. Bound: those two in turn, 1024 clocks of MMAs
+//   and 1024 of ex2 (16 a clock) per row tile and key tile.
 //
 // Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain); the MMA lane waits for
 // its last commit and the producer for its last copies before Tensor Memory is released.
@@ -43,30 +46,28 @@ namespace rra {
 namespace spx {
 
 constexpr int kRows = kSharedPrefixRows;        // rows of a tile: M of every MMA
-constexpr int kTile = kSharedPrefixTile;        // keys per tile
 constexpr float kRescaleLog2 = 8.f;             // move the running max only when it grows by more
 
 template <int D, int NQ>
 struct Cfg {
+  static constexpr int kTile = shared_prefix_tile(D, NQ);  // keys per tile
   static constexpr int kHalves = D / 64;
   static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
   static constexpr int kTileBytes = kTile / 8 * kGroupBytes;
   static constexpr int kQHalfBytes = kRows * 128;          // NQ 2: Q tiles, K-major, 64-dim halves
   static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
-  static constexpr int kBufs = NQ == 2 ? 4 : 1;            // S buffers
-  static constexpr int kAhead = NQ == 2 ? 2 : 1;           // key tiles whose S goes out before the first P.V
-  static constexpr int kKSlots = NQ == 2 ? 5 : 3, kVSlots = NQ == 2 ? 4 : 3;
+  static constexpr int kSlots = NQ == 2 ? (D == 64 ? 4 : 2) : 3;  // of K, and as many of V
   // Tensor Memory columns
   static constexpr uint32_t kColO = 0;                     // O_k: D columns each
-  static constexpr uint32_t kColS = NQ * D;                // S buffers of kTile columns, P over their first half
-  static constexpr uint32_t kColQ = kColS + kBufs * kTile; // NQ 1: Q as bf16 pairs, D / 2 columns
+  static constexpr uint32_t kColS = NQ * D;                // S_k: kTile columns each, P over their first half
+  static constexpr uint32_t kColQ = kColS + NQ * kTile;    // NQ 1: Q as bf16 pairs, D / 2 columns
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
   // shared memory
   static constexpr int kOffK = kQBytes;
-  static constexpr int kOffV = kOffK + kKSlots * kTileBytes;
-  static constexpr int kOffBar = kOffV + kVSlots * kTileBytes;
-  // q_ready, k_full, k_empty, v_full, v_empty, s_full[kBufs], p_full[kBufs], o_done[NQ], mma_done
-  static constexpr int kNumBars = 1 + 2 * kKSlots + 2 * kVSlots + 2 * kBufs + NQ + 1;
+  static constexpr int kOffV = kOffK + kSlots * kTileBytes;
+  static constexpr int kOffBar = kOffV + kSlots * kTileBytes;
+  // q_ready, k_full, k_empty, v_full, v_empty, s_full[NQ], p_full[NQ], mma_done
+  static constexpr int kNumBars = 1 + 4 * kSlots + 2 * NQ + 1;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffTable = kOffTmemSlot + 16;
   static constexpr int kSmemBytes = 1024 + kOffTable + kSharedPrefixTableEntries * 4;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
   using C = Cfg<D, NQ>;
+  constexpr int kTile = C::kTile, kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -145,21 +147,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
 
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* k_full = q_ready + 1;
-  uint64_t* k_empty = k_full + C::kKSlots;
-  uint64_t* v_full = k_empty + C::kKSlots;
-  uint64_t* v_empty = v_full + C::kVSlots;
-  uint64_t* s_full = v_empty + C::kVSlots;
-  uint64_t* p_full = s_full + C::kBufs;
-  uint64_t* o_done = p_full + C::kBufs;
-  uint64_t* mma_done = o_done + NQ;
+  uint64_t* k_empty = k_full + kSlots;
+  uint64_t* v_full = k_empty + kSlots;
+  uint64_t* v_empty = v_full + kSlots;
+  uint64_t* s_full = v_empty + kSlots;
+  uint64_t* p_full = s_full + NQ;
+  uint64_t* mma_done = p_full + NQ;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::kOffTable);
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, C::kSoftmaxThreads);
-    for (int s = 0; s < 2 * C::kKSlots + 2 * C::kVSlots + C::kBufs; ++s) mbar_init(&k_full[s], 1);
-    for (int s = 0; s < C::kBufs; ++s) mbar_init(&p_full[s], 128);
-    for (int k = 0; k < NQ; ++k) mbar_init(&o_done[k], 1);
+    for (int s = 0; s < 4 * kSlots + NQ; ++s) mbar_init(&k_full[s], 1);  // ... and s_full
+    for (int k = 0; k < NQ; ++k) mbar_init(&p_full[k], 128);
     mbar_init(mma_done, 1);
     fence_barrier_init();
   }
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // item i: row tile i % NQ, key tile i / NQ, S buffer i % kBufs
-  auto ring_phase = [](int j, int slots) { return static_cast<uint32_t>((j / slots) & 1); };
+  auto slot_of = [](int j) { return j % kSlots; };
+  auto phase_of = [](int j) { return static_cast<uint32_t>((j / kSlots) & 1); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
@@ -199,18 +199,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
     const int box = min(bs, kTile);  // rows per TMA box, as the tensor maps were encoded
     // tile j of K or V into its slot; false once a wait ran out
-    auto load = [&](const CUtensorMap* map, int off, uint64_t* full, uint64_t* empty, int slots, int j) -> bool {
-      const int s = j % slots, tile0 = start + j * kTile;
+    auto load = [&](const CUtensorMap* map, int off, uint64_t* full, uint64_t* empty, int j) -> bool {
+      const int s = slot_of(j), tile0 = start + j * kTile;
       const int nbox = (min(kTile, end - tile0) + box - 1) / box;
       int ok = 1;
       if (lane == 0) {
-        if (j >= slots && !mbar_wait(&empty[s], ring_phase(j, slots) ^ 1u))
+        if (j >= kSlots && !mbar_wait(&empty[s], phase_of(j) ^ 1u))
           ok = 0;
         else
           mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-      if (lane < nbox) {  // one copy per lane (at most 8)
+      if (lane < nbox) {  // one copy per lane (at most 16)
         const int t = tile0 + lane * box;
         const int rows8 = (tbl[(t >> log2_bs) - first_blk] << (log2_bs - 3)) + ((t & (bs - 1)) >> 3);
         tma_g2s_5d(smem + off + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, map, 0, 0, 0, rows8, g, &full[s]);
@@ -218,36 +218,33 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
       __syncwarp();
       return true;
     };
-    // in the order the MMAs take them: K_0 .. K_(kAhead - 1), V_0, K_kAhead, V_1, ...
     int nk = 0, nv = 0;
-    bool ok = true;
-    for (int t = 0; ok && t < n_tiles + C::kAhead; ++t) {
-      if (t < n_tiles && (ok = load(&k_map, C::kOffK, k_full, k_empty, C::kKSlots, t))) ++nk;
-      if (ok && t >= C::kAhead - 1 && nv < n_tiles && nv <= t - (C::kAhead - 1) &&
-          (ok = load(&v_map, C::kOffV, v_full, v_empty, C::kVSlots, nv)))
-        ++nv;
+    while (nv < n_tiles) {
+      if (!load(&k_map, C::kOffK, k_full, k_empty, nk)) break;
+      ++nk;
+      if (!load(&v_map, C::kOffV, v_full, v_empty, nv)) break;
+      ++nv;
     }
     if (lane == 0) {
-      if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
+      if (nv < n_tiles) flag_error(a.err, RRA_ERR_TIMEOUT);
       // no copy may still be landing when the CTA exits
-      for (int j = max(nk - C::kKSlots, 0); j < nk; ++j) mbar_wait(&k_full[j % C::kKSlots], ring_phase(j, C::kKSlots));
-      for (int j = max(nv - C::kVSlots, 0); j < nv; ++j) mbar_wait(&v_full[j % C::kVSlots], ring_phase(j, C::kVSlots));
+      for (int j = max(nk - kSlots, 0); j < nk; ++j) mbar_wait(&k_full[slot_of(j)], phase_of(j));
+      for (int j = max(nv - kSlots, 0); j < nv; ++j) mbar_wait(&v_full[slot_of(j)], phase_of(j));
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
     if (lane == 0) {
       const uint32_t base = smem_addr(smem);
-      const int n_items = NQ * n_tiles;
       bool ok = mbar_wait(q_ready, 0);
       tc::fence_after_sync();
-      auto issue_s = [&](int i) -> bool {
-        const int k = i % NQ, j = i / NQ, s = j % C::kKSlots;
+      auto issue_s = [&](int k, int j) -> bool {
+        const int s = slot_of(j);
         if (k == 0) {
-          if (!mbar_wait(&k_full[s], ring_phase(j, C::kKSlots))) return false;
+          if (!mbar_wait(&k_full[s], phase_of(j))) return false;
           tc::fence_after_sync();
         }
         const uint32_t k_base = base + C::kOffK + s * C::kTileBytes;
-        const uint32_t col = tmem + C::kColS + kTile * (i % C::kBufs);
+        const uint32_t col = tmem + C::kColS + kTile * k;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * 1024 + (kk & 3) * 32, 1024, C::kGroupBytes);
@@ -258,28 +255,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
           else
             tc::mma_bf16_ts(col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
         }
-        tc::commit(&s_full[i % C::kBufs]);
-        if (k == NQ - 1) tc::commit(&k_empty[s]);
+        tc::commit(&s_full[k]);
         return true;
       };
-      for (int i = 0; ok && i < C::kBufs && i < n_items; ++i) ok = issue_s(i);
-      for (int i = 0; ok && i < n_items; ++i) {
-        const int k = i % NQ, j = i / NQ, s = j % C::kVSlots;
-        if ((k == 0 && !mbar_wait(&v_full[s], ring_phase(j, C::kVSlots))) || !mbar_wait(&p_full[i % C::kBufs], (i / C::kBufs) & 1)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
+      for (int k = 0; ok && k < NQ; ++k) ok = issue_s(k, 0);
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int s = slot_of(j);
         const uint32_t v_base = base + C::kOffV + s * C::kTileBytes;
+        ok = mbar_wait(&v_full[s], phase_of(j));
+        for (int k = 0; ok && k < NQ; ++k) {
+          if (!mbar_wait(&p_full[k], j & 1)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * (i % C::kBufs) + 8 * kk,
-                          tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-        tc::commit(&o_done[k]);
-        if (k == NQ - 1) tc::commit(&v_empty[s]);
-        // the MMAs run in issue order: S of this buffer's next item may overwrite P
-        if (i + C::kBufs < n_items) ok = issue_s(i + C::kBufs);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + 8 * kk,
+                            tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+          if (j + 1 < n_tiles) ok = issue_s(k, j + 1);
+        }
       }
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       tc::commit(mma_done);  // every MMA issued above has completed once this arrives
@@ -334,21 +330,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      const int i = j * NQ + k, buf = i % C::kBufs;
-      if (!warp_wait(&s_full[buf], (i / C::kBufs) & 1)) {
+      if (!warp_wait(&s_full[k], j & 1)) {  // S_k is there, and every MMA issued before it is complete
         ok = false;
         break;
       }
       tc::fence_after_sync();
+      if (k == NQ - 1 && r == 0) {
+        mbar_arrive(&k_empty[slot_of(j)]);
+        if (j > 0) mbar_arrive(&v_empty[slot_of(j - 1)]);
+      }
       if (k == 0 && j == n_tiles - 1 && last_valid < kTile) {
         // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0 (row
         // tile 0's P.V reads this V first)
-        if (!warp_wait(&v_full[j % C::kVSlots], ring_phase(j, C::kVSlots))) {
+        if (!warp_wait(&v_full[slot_of(j)], phase_of(j))) {
           ok = false;
           break;
         }
         if (r >= last_valid && r < kTile) {
-          uint8_t* vrow = smem + C::kOffV + (j % C::kVSlots) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
+          uint8_t* vrow = smem + C::kOffV + slot_of(j) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         tc::fence_smem_to_async();
       }
       if (warp_real) {
-        const uint32_t s_col = tmem + lane_base + C::kColS + kTile * buf;
+        const uint32_t s_col = tmem + lane_base + C::kColS + kTile * k;
         uint32_t sv[kTile];
         ld_cols<kTile>(s_col, sv);
         const int vis = min(lim, end) - (start + j * kTile);  // columns this row attends
@@ -392,11 +391,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         st_cols<kTile / 2>(s_col, pw);
         l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
         if (j > 0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
-          if (!warp_wait(&o_done[k], (j - 1) & 1)) {      // the P.V before this one (that of j - 2 is complete)
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
@@ -410,11 +404,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         tc::tmem_wait_st();
       }
       tc::fence_before_sync();
-      mbar_arrive(&p_full[buf]);
+      mbar_arrive(&p_full[k]);
     }
     // ------------------------------------------------------------------ epilogue: this chunk's partial rows
-    // (the barrier may be two phases from the last one: S runs two items ahead)
-    if (ok && (n_tiles < 2 || warp_wait(&o_done[k], (n_tiles - 2) & 1)) && warp_wait(&o_done[k], (n_tiles - 1) & 1)) {
+    if (ok && warp_wait(mma_done, 0)) {
       tc::fence_after_sync();
       const size_t ps = out_row * a.num_splits + split;
 #pragma unroll 1
