@@ -23,9 +23,10 @@
 //
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
 // so S may overwrite the P before it, and one commit per S says that everything before it is
-// complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back
-// to the producer. (A commit costs some 250 clocks between MMAs: with three per tile, and
-// tiles of 64 keys, 512 rows x 8 heads x 16384 keys took 230 us against ## us.)
+// complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back to
+// the producer. The lane is an elected one (elect_one) and the commits few: with a lane chosen by
+// its index and three commits per tile of 64 keys, 512 rows x 8 heads x 16384 keys took 230 us
+// against ## us. (A second MMA warp, one per row tile, was slower.)
 //
 // Two shapes of CTA:
 // * NQ = 1 (up to 128 rows per KV head): key tiles of 64 (128 at head dim 64), Q in Tensor Memory, 256 of
@@ -89,6 +90,14 @@ __device__ __forceinline__ void tma_g2s_5d(void* dst, const CUtensorMap* map, in
       : "memory");
 }
 
+// One lane of a converged warp. The compiler knows that a branch on elect.sync holds one thread and keeps the
+// MMAs' operands in uniform registers there: 15 clocks an MMA, against some 80 behind a test of the lane.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
   const int g = blockIdx.z, split = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kProducerWarp = 4 * NQ, kMmaWarp = 4 * NQ + 1;
   const int start = split * a.prefix_chunk;
   const int end = min(a.prefix_len, start + a.prefix_chunk);
@@ -157,9 +166,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::kOffTable);
 
   if (threadIdx.x == 0) {
-    mbar_init(q_ready, C::kSoftmaxThreads);
-    for (int s = 0; s < 4 * kSlots + NQ; ++s) mbar_init(&k_full[s], 1);  // ... and s_full
-    for (int k = 0; k < NQ; ++k) mbar_init(&p_full[k], 128);
+    mbar_init(q_ready, 4 * NQ);  // one arrival per softmax warp
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], NQ);  // every row tile gives a slot back
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], NQ);
+    }
+    for (int k = 0; k < NQ; ++k) mbar_init(&s_full[k], 1);
+    for (int k = 0; k < NQ; ++k) mbar_init(&p_full[k], 4);
     mbar_init(mma_done, 1);
     fence_barrier_init();
   }
@@ -186,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   }
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   auto slot_of = [](int j) { return j % kSlots; };
   auto phase_of = [](int j) { return static_cast<uint32_t>((j / kSlots) & 1); };
 
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t base = smem_addr(smem);
       bool ok = mbar_wait(q_ready, 0);
       tc::fence_after_sync();
@@ -243,28 +258,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
           if (!mbar_wait(&k_full[s], phase_of(j))) return false;
           tc::fence_after_sync();
         }
-        const uint32_t k_base = base + C::kOffK + s * C::kTileBytes;
-        const uint32_t col = tmem + C::kColS + kTile * k;
+        const uint32_t k_base = base + C::kOffK + s * C::kTileBytes, s_col = tmem + C::kColS + kTile * k;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * 1024 + (kk & 3) * 32, 1024, C::kGroupBytes);
           if constexpr (NQ == 2)
-            tc::mma_bf16_ss(col, tc::sw128_desc(base + (k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32,
-                                                1024, 1024),
+            tc::mma_bf16_ss(s_col, tc::sw128_desc(base + (k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32,
+                                                  1024, 1024),
                             kd, C::kIdescS, kk > 0 ? 1u : 0u);
           else
-            tc::mma_bf16_ts(col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
+            tc::mma_bf16_ts(s_col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
         }
         tc::commit(&s_full[k]);
         return true;
       };
-      for (int k = 0; ok && k < NQ; ++k) ok = issue_s(k, 0);
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) ok = ok && issue_s(k, 0);
       for (int j = 0; ok && j < n_tiles; ++j) {
         const int s = slot_of(j);
         const uint32_t v_base = base + C::kOffV + s * C::kTileBytes;
         ok = mbar_wait(&v_full[s], phase_of(j));
-        for (int k = 0; ok && k < NQ; ++k) {
-          if (!mbar_wait(&p_full[k], j & 1)) {
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          if (!ok || !mbar_wait(&p_full[k], j & 1)) {
             ok = false;
             break;
           }
@@ -324,7 +340,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         tc::tmem_wait_st();
         tc::fence_before_sync();
       }
-      mbar_arrive(q_ready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
     }
     const float sl = a.scale_log2;
     float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
@@ -335,13 +352,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         break;
       }
       tc::fence_after_sync();
-      if (k == NQ - 1 && r == 0) {
+      if (r == 0) {
         mbar_arrive(&k_empty[slot_of(j)]);
         if (j > 0) mbar_arrive(&v_empty[slot_of(j - 1)]);
       }
-      if (k == 0 && j == n_tiles - 1 && last_valid < kTile) {
-        // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0 (row
-        // tile 0's P.V reads this V first)
+      if (j == n_tiles - 1 && last_valid < kTile) {
+        // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0 (both
+        // row tiles' threads write them, each before its own P.V)
         if (!warp_wait(&v_full[slot_of(j)], phase_of(j))) {
           ok = false;
           break;
@@ -404,7 +421,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         tc::tmem_wait_st();
       }
       tc::fence_before_sync();
-      mbar_arrive(&p_full[k]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[k]);
     }
     // ------------------------------------------------------------------ epilogue: this chunk's partial rows
     if (ok && warp_wait(mma_done, 0)) {
