@@ -428,19 +428,28 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     if (ok && warp_wait(mma_done, 0)) {
       tc::fence_after_sync();
       const size_t ps = out_row * a.num_splits + split;
+      // the row through shared memory (Q and the ring, which every MMA has read by now) and out in one
+      // copy: 16-byte stores of 32 rows at a time cost 1.7 TB/s. Rows 16 bytes apart modulo the banks.
+      constexpr int kPitch = D * 4 + 16;
+      static_assert(NQ * kRows * kPitch <= C::kOffBar, "the rows fit");
+      uint8_t* orow = smem + (k * kRows + r) * kPitch;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         tc::tmem_ld32(o_col + 32 * c, v);
         tc::tmem_wait_ld();
-        if (!real) continue;
-        float4* po = reinterpret_cast<float4*>(a.ws_o + ps * D) + 8 * c;
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          po[x] = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]), __uint_as_float(v[4 * x + 2]),
-                              __uint_as_float(v[4 * x + 3]));
+          *reinterpret_cast<uint4*>(orow + 128 * c + 16 * x) = make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
       }
+      tc::fence_smem_to_async();
+      if (real)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.ws_o + ps * D),
+                     "r"(smem_addr(orow)), "n"(D * 4)
+                     : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       if (real) *reinterpret_cast<float2*>(a.ws_ml + 2 * ps) = make_float2(m_use, l);
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // written before the CTA ends
     } else {
       flag_error(a.err, RRA_ERR_TIMEOUT);
     }

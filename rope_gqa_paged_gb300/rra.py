@@ -137,7 +137,7 @@ _device_of_thread = threading.local()
 
 def use_device_of(t: torch.Tensor) -> None:
     """Selects tensor ``t``'s device in the library for this thread."""
-    dev = t.device.index if t.device.index is not None else torch.cuda.current_device()
+    dev = t.get_device()
     if getattr(_device_of_thread, "dev", None) != dev:
         _check("rra_use_device", lib().rra_use_device(dev))
         _device_of_thread.dev = dev
@@ -147,8 +147,8 @@ def _stream(stream, t: torch.Tensor) -> Optional[int]:
     """The stream handle for a call on tensor ``t``'s device (selecting that device in the
     library when the call runs on the default stream, which carries no device)."""
     use_device_of(t)
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+    if stream is None:  # the handle alone: torch.cuda.current_stream builds a Stream object, 2 us of a call
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -426,27 +426,32 @@ def rra_verify_step(q, k_new, v_new, positions, q_out, k_cache, v_cache, out, bl
 
 
 # --------------------------------------------------------------------------- shared prefix
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
 def _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len: int, block_table, lens, out):
-    """(B, gamma, Hq, D) of the new tokens' queries; [B, Hq, D] is one new token per sequence. The C
-    calls take no element types, so they are checked here, with the shapes."""
-    if q.dim() == 4:
-        B, gamma, Hq, D = q.shape
-    elif q.dim() == 3:
-        (B, Hq, D), gamma = q.shape, 1
+    """(B, gamma, Hq, D, num_blocks, block_size, Hkv, block-table columns) of a shared-prefix call; queries
+    [B, Hq, D] are one new token per sequence. The C calls take no element types, so they are checked
+    here, with the shapes."""
+    shape, pool, table = q.shape, k_pool.shape, block_table.shape
+    if len(shape) == 4:
+        B, gamma, Hq, D = shape
+    elif len(shape) == 3:
+        (B, Hq, D), gamma = shape, 1
     else:
         raise ValueError("q: [B, gamma, Hq, D] or [B, Hq, D]")
-    if not (q.dtype == k_pool.dtype == v_pool.dtype == out.dtype == torch.bfloat16):
+    if not (q.dtype == k_pool.dtype == v_pool.dtype == out.dtype == _BF16):
         raise TypeError("shared-prefix attention takes bf16 queries, caches and outputs")
-    if block_table.dtype != torch.int32 or lens.dtype != torch.int32:
+    if not block_table.dtype == lens.dtype == _I32:
         raise TypeError("block_table, seq_lens and positions are int32")
-    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or k_pool.shape[3] != D or out.shape != q.shape:
+    if len(pool) != 4 or v_pool.shape != pool or pool[3] != D or out.shape != shape:
         raise ValueError("k_pool and v_pool: [num_blocks, block_size, Hkv, D]; out: the shape of q")
-    if block_table.dim() != 2 or block_table.shape[0] != B or lens.numel() != B:
+    if len(table) != 2 or table[0] != B or lens.numel() != B:
         raise ValueError("block_table: [B, max_blocks_per_seq]; one length or position per sequence")
-    if prefix_len > 0 and (prefix_blocks is None or prefix_blocks.dtype != torch.int32 or
-                           prefix_blocks.numel() * k_pool.shape[1] < prefix_len):
+    if prefix_len > 0 and (prefix_blocks is None or prefix_blocks.dtype != _I32 or
+                           prefix_blocks.numel() * pool[1] < prefix_len):
         raise ValueError("prefix_blocks: int32, a block for every block_size tokens of the prefix")
-    return B, gamma, Hq, D
+    return B, gamma, Hq, D, pool[0], pool[1], pool[2], table[1]
 
 
 def rra_shared_prefix_plan(B: int, gamma: int, Hq: int, Hkv: int, D: int, prefix_len: int, max_blocks_per_seq: int,
@@ -464,15 +469,15 @@ def rra_shared_prefix_attn(q_rot, k_pool, v_pool, prefix_blocks, prefix_len: int
                            err_flag=None, stream=None) -> None:
     """out[b, j] = attention of q_rot[b, j] over the first seq_lens[b] - gamma + 1 + j tokens, of which the
     first prefix_len are in prefix_blocks for every sequence (read once for the batch)."""
-    B, gamma, Hq, D = _shared_layout(q_rot, k_pool, v_pool, prefix_blocks, prefix_len, block_table, seq_lens, out)
-    num_blocks, block_size, Hkv = k_pool.shape[:3]
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = lib().rra_shared_prefix_attn(_ptr(q_rot), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_blocks), int(prefix_len),
-                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens), block_size, num_blocks,
-                                      _ptr(out), B, gamma, Hq, Hkv, D, float(scale), int(num_splits),
-                                      int(prefix_splits), _ptr(workspace), ws_bytes, _ptr(err_flag),
+    B, gamma, Hq, D, num_blocks, block_size, Hkv, cols = _shared_layout(q_rot, k_pool, v_pool, prefix_blocks,
+                                                                        prefix_len, block_table, seq_lens, out)
+    st = lib().rra_shared_prefix_attn(_ptr(q_rot), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_blocks), prefix_len,
+                                      _ptr(block_table), cols, _ptr(seq_lens), block_size, num_blocks, _ptr(out), B,
+                                      gamma, Hq, Hkv, D, scale, num_splits, prefix_splits, _ptr(workspace),
+                                      workspace.nbytes if workspace is not None else 0, _ptr(err_flag),
                                       _stream(stream, q_rot))
-    _check("rra_shared_prefix_attn", st)
+    if st != 0:
+        raise RraError("rra_shared_prefix_attn", st)
 
 
 def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, prefix_blocks, prefix_len: int,
@@ -480,23 +485,30 @@ def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, pr
                            num_splits: int = 0, prefix_splits: int = 0, workspace=None, err_flag=None,
                            stream=None) -> None:
     """RoPE + append of the gamma new tokens at positions[b] (at least prefix_len), then their attention."""
-    B, gamma, Hq, D = _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len, block_table, positions, out)
-    num_blocks, block_size, Hkv = k_pool.shape[:3]
-    if not (k_new.dtype == v_new.dtype == q_out.dtype == torch.bfloat16):
+    B, gamma, Hq, D, num_blocks, block_size, Hkv, cols = _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len,
+                                                                        block_table, positions, out)
+    if not k_new.dtype == v_new.dtype == q_out.dtype == _BF16:
         raise TypeError("shared-prefix attention takes bf16 new tokens")
     if k_new.numel() != B * gamma * Hkv * D or v_new.shape != k_new.shape or q_out.shape != q.shape:
         raise ValueError("k_new and v_new: [B, gamma, Hkv, D]; q_out: the shape of q")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = lib().rra_shared_prefix_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q_out), _ptr(k_pool),
-                                      _ptr(v_pool), _ptr(prefix_blocks), int(prefix_len), _ptr(block_table),
-                                      block_table.shape[1], block_size, num_blocks, _ptr(out), B, gamma, Hq, Hkv, D,
-                                      float(rope_base), int(rope_style), float(scale), int(num_splits),
-                                      int(prefix_splits), _ptr(workspace), ws_bytes, _ptr(err_flag),
+                                      _ptr(v_pool), _ptr(prefix_blocks), prefix_len, _ptr(block_table), cols,
+                                      block_size, num_blocks, _ptr(out), B, gamma, Hq, Hkv, D, rope_base, rope_style,
+                                      scale, num_splits, prefix_splits, _ptr(workspace),
+                                      workspace.nbytes if workspace is not None else 0, _ptr(err_flag),
                                       _stream(stream, q))
-    _check("rra_shared_prefix_step", st)
+    if st != 0:
+        raise RraError("rra_shared_prefix_step", st)
 
 
 # --------------------------------------------------------------------------- draft acceptance
+def _i32(t, shape, what: str) -> int:
+    """The pointer of a contiguous int32 tensor of this shape."""
+    if t.dtype != _I32 or t.shape != shape:
+        raise ValueError(f"{what}: an int32 tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
 def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs=None, draft_lens=None,
                      positions=None, tokens_out=None, n_accepted=None, positions_out=None, err_flag=None,
                      stream=None) -> tuple:
@@ -508,40 +520,50 @@ def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs
     uniform random numbers in [0, 1). Outputs are made where they are not given; positions_out may be
     positions.
     """
-    B, gamma = draft_tokens.shape
-    V, dt = target_probs.shape[-1], _dtype_code(target_probs)
+    ids = draft_tokens.shape
+    B, gamma = ids
+    V, dt = target_probs.shape[-1], target_probs.dtype
+    code = RRA_F32 if dt == _F32 else _dtype_code(target_probs)
     if target_probs.shape != (B, gamma + 1, V):
         raise ValueError("target_probs: [B, gamma + 1, V]")
-    sq = (0, 0)
+    pb, pt, p1 = target_probs.stride()
+    if not target_probs.is_cuda or (p1 != 1 and V > 1):
+        raise ValueError("target_probs: a CUDA tensor with a unit last stride")
+    q_ptr, qb, qt = None, 0, 0
     if draft_probs is not None:
-        if draft_probs.shape != (B, gamma, V) or draft_probs.dtype != target_probs.dtype:
+        if draft_probs.shape != (B, gamma, V) or draft_probs.dtype != dt:
             raise ValueError("draft_probs: [B, gamma, V], of target_probs' type")
-        sq = draft_probs.stride()
-    sp = target_probs.stride()
-    for t, s in ((target_probs, sp), (draft_probs, sq)):
-        if t is not None and not (t.is_cuda and (s[2] == 1 or V == 1)):
-            raise ValueError("probabilities: CUDA tensors with a unit last stride")
-    dev, i32 = target_probs.device, torch.int32
-    if u_accept.dtype != torch.float32 or u_sample.dtype != torch.float32:
+        qb, qt, q1 = draft_probs.stride()
+        if not draft_probs.is_cuda or (q1 != 1 and V > 1):
+            raise ValueError("draft_probs: a CUDA tensor with a unit last stride")
+        q_ptr = draft_probs.data_ptr()
+    if not u_accept.dtype == u_sample.dtype == _F32:
         raise TypeError("u_accept and u_sample are float32")
-    if u_accept.shape != (B, gamma) or u_sample.numel() != B:
+    if u_accept.shape != ids or u_sample.shape != (B,):
         raise ValueError("u_accept: [B, gamma]; u_sample: [B]")
+    if tokens_out is None and n_accepted is None and positions_out is None:
+        # one allocation for all (each costs as much as the launch)
+        n = B * (gamma + 1)
+        buf = torch.empty((n + (2 * B if positions is not None else B),), dtype=_I32, device=target_probs.device)
+        tokens_out, n_accepted = buf.as_strided((B, gamma + 1), (gamma + 1, 1), 0), buf.as_strided((B,), (1,), n)
+        if positions is not None:
+            positions_out = buf.as_strided((B,), (1,), n + B)
     if tokens_out is None:
-        tokens_out = torch.empty(B, gamma + 1, dtype=i32, device=dev)
+        tokens_out = draft_tokens.new_empty((B, gamma + 1))
     if n_accepted is None:
-        n_accepted = torch.empty(B, dtype=i32, device=dev)
-    if positions_out is None and positions is not None:
-        positions_out = torch.empty(B, dtype=i32, device=dev)
-    for t, n in ((draft_tokens, B * gamma), (draft_lens, B), (positions, B), (tokens_out, B * (gamma + 1)),
-                 (n_accepted, B), (positions_out, B)):
-        if t is not None and (t.dtype != i32 or t.numel() != n):
-            raise ValueError("tokens, lengths, positions and counts are int32 tensors of [B, ...] values")
-    st = lib().rra_accept_draft(target_probs.data_ptr(), sp[0], sp[1],
-                                draft_probs.data_ptr() if draft_probs is not None else None, sq[0], sq[1],
-                                _ptr(draft_tokens), _ptr(draft_lens), _ptr(u_accept), _ptr(u_sample), _ptr(positions),
-                                _ptr(tokens_out), _ptr(n_accepted), _ptr(positions_out), B, gamma, V, dt,
-                                _ptr(err_flag), _stream(stream, target_probs))
-    _check("rra_accept_draft", st)
+        n_accepted = draft_tokens.new_empty((B,))
+    if positions is not None and positions_out is None:
+        positions_out = draft_tokens.new_empty((B,))
+    row = (B,)
+    st = lib().rra_accept_draft(
+        target_probs.data_ptr(), pb, pt, q_ptr, qb, qt, _i32(draft_tokens, ids, "draft_tokens"),
+        _i32(draft_lens, row, "draft_lens") if draft_lens is not None else None, _ptr(u_accept), _ptr(u_sample),
+        _i32(positions, row, "positions") if positions is not None else None,
+        _i32(tokens_out, (B, gamma + 1), "tokens_out"), _i32(n_accepted, row, "n_accepted"),
+        _i32(positions_out, row, "positions_out") if positions_out is not None else None, B, gamma, V, code,
+        _ptr(err_flag), _stream(stream, target_probs))
+    if st != 0:
+        raise RraError("rra_accept_draft", st)
     return (tokens_out, n_accepted) if positions_out is None else (tokens_out, n_accepted, positions_out)
 
 
