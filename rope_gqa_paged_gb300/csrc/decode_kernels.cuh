@@ -168,18 +168,6 @@ struct ChunkBlockIds {
       id[k] = i < reach ? row[i] : 0;
     }
   }
-  // Shared prefix: the blocks before prefix_len come from prefix_blocks. Read past L1 (the caller
-  // may not have waited for the kernel before it).
-  __device__ __forceinline__ void load_shared(const DecodeArgs& a, int b, int first_blk, int tid, int nthreads) {
-    const int32_t* row = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
-    const int own = a.prefix_len >> a.log2_bs;
-    const int reach = min(((a.chunk + (1 << a.log2_bs) - 1) >> a.log2_bs) + 1, a.max_blocks_per_seq - first_blk);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = tid + k * nthreads;
-      id[k] = i < reach ? __ldcg((first_blk + i < own ? a.prefix_blocks : row) + first_blk + i) : 0;
-    }
-  }
   __device__ __forceinline__ void store(const DecodeArgs& a, int32_t* tbl, int n_blk, int tid, int nthreads) const {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -195,12 +183,6 @@ struct ChunkBlockIds {
     }
   }
 };
-
-// Shared prefix: the kernel before this one may still run when this one ends its own work; one CTA
-// waits for it, so that this grid does not complete before it.
-__device__ __forceinline__ void shared_wait_first(const DecodeArgs& a) {
-  if (a.prefix_splits > 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
-}
 
 // Counts this CTA's arrival at `cnt` (all `nthreads` consumer threads call it after their
 // last write). True in the CTA whose arrival brings the count to `target`; that CTA also puts

@@ -433,9 +433,7 @@ __device__ __forceinline__ void append_token_bf16(const DecodeArgs& a, const flo
   if (lane == 0 && !a.test_hold_append) mbar_arrive(appended);  // the hold: see DecodeArgs
 }
 
-// SHARED (paged, not fused): the sequences' own tokens of shared-prefix attention with one new token,
-// as decode_verify_kernel<SHARED> (verify.cuh) describes it.
-template <int D, bool PAGED, bool FUSED, int NT = 1, bool NARROW = false, bool SHARED = false>
+template <int D, bool PAGED, bool FUSED, int NT = 1, bool NARROW = false>
 __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, NT, NARROW>::kCtasPerSm)
     decode_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                       const DecodeArgs a) {
@@ -455,7 +453,7 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
   // kernel has finished, only warm L2 with this CTA's first tiles, from lengths and block ids
   // read ahead (they may still change: they only choose what to prefetch, clamped in range).
   pdl_launch_dependents();
-  if (!SHARED && threadIdx.x == C::kConsumerWarps * 32) {
+  if (threadIdx.x == C::kConsumerWarps * 32) {
     const int Ls = min(max(FUSED ? a.positions[b] + 1 : a.seq_lens[b], 0), a.capacity);
     const int s0 = split * a.chunk;
     const int e0 = min(Ls, s0 + a.chunk);
@@ -484,12 +482,10 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
       }
     }
   }
-  if (!SHARED || a.prefix_splits == 0) pdl_wait();
-  const int start = (SHARED ? a.first_token : 0) + split * a.chunk;
+  pdl_wait();
   // the chunk's block ids load alongside the sequence length
   ChunkBlockIds<(kMmaTableEntries + C::kThreads - 1) / C::kThreads> pre_ids;
-  if constexpr (SHARED) pre_ids.load_shared(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
-  else if constexpr (PAGED) pre_ids.load(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
+  if constexpr (PAGED) pre_ids.load(a, b, (split * a.chunk) >> a.log2_bs, threadIdx.x, C::kThreads);
 
   int L;
   if constexpr (FUSED) {
@@ -499,25 +495,17 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
       return;
     }
     L = pos + 1;
-  } else if (SHARED && a.positions != nullptr) {
-    const int pos = __ldcg(a.positions + b);
-    if (pos < a.prefix_len || pos >= a.capacity) {
-      if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
-      shared_wait_first(a);
-      return;
-    }
-    L = pos + 1;
   } else {
-    L = SHARED ? __ldcg(a.seq_lens + b) : a.seq_lens[b];
+    L = a.seq_lens[b];
     if (L < 0 || L > a.capacity) {
       if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_SEQ_LEN);
       L = min(max(L, 0), a.capacity);
     }
   }
+  const int start = split * a.chunk;
   const int n_work = (L + a.chunk - 1) / a.chunk;  // splits of this sequence that hold tokens
   if (start >= L) {
-    if constexpr (SHARED) shared_wait_first(a);
-    if (L == 0 && split == 0 && (!SHARED || a.num_splits == 1)) {
+    if (L == 0 && split == 0) {
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(b) * a.Hq + h0) * D;
       for (int i = threadIdx.x; i < hpc * D; i += blockDim.x) out[i] = __float2bfloat16_rn(0.f);
     }
@@ -561,7 +549,6 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
     }
-    if constexpr (SHARED) asm volatile("fence.proxy.async.global;" ::: "memory");  // the append's writes, for the copies
     int issued = 0;
     for (int it = 0; it < n_tiles; ++it) {
       const int s = it % C::kStages;
@@ -613,7 +600,6 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
     if (lane == 0)
       for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
         mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1);
-    if constexpr (SHARED) shared_wait_first(a);
     return;
   }
 
@@ -628,13 +614,8 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
                                                           (static_cast<size_t>(b) * a.Hq + h0 + 8 * n + hd) * D);
 #pragma unroll
     for (int kk = 0; kk < C::kKSteps; ++kk) {
-      if constexpr (SHARED) {
-        qb[n][kk][0] = 8 * n + hd < hpc ? __ldcg(q + kk * 8 + (lane & 3)) : 0u;
-        qb[n][kk][1] = 8 * n + hd < hpc ? __ldcg(q + kk * 8 + 4 + (lane & 3)) : 0u;
-      } else {
-        qb[n][kk][0] = 8 * n + hd < hpc ? q[kk * 8 + (lane & 3)] : 0u;
-        qb[n][kk][1] = 8 * n + hd < hpc ? q[kk * 8 + 4 + (lane & 3)] : 0u;
-      }
+      qb[n][kk][0] = 8 * n + hd < hpc ? q[kk * 8 + (lane & 3)] : 0u;
+      qb[n][kk][1] = 8 * n + hd < hpc ? q[kk * 8 + 4 + (lane & 3)] : 0u;
     }
   }
   if constexpr (FUSED) {
@@ -782,10 +763,10 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
     for (int w = 0; w < C::kConsumerWarps; ++w)
       osum = fmaf(red_w[w * C::kMaxHeads + h], red_o[(w * C::kMaxHeads + h) * kRS + d], osum);
     const size_t bh = static_cast<size_t>(b) * a.Hq + h0 + h;
-    if (SHARED ? a.num_splits == 1 : n_work == 1) {
+    if (n_work == 1) {
       static_cast<__nv_bfloat16*>(a.out)[bh * D + d] = __float2bfloat16_rn(lsum > 0.f ? osum / lsum : 0.f);
     } else {
-      const size_t ps = bh * a.num_splits + (SHARED ? a.prefix_splits : 0) + split;
+      const size_t ps = bh * a.num_splits + split;
       a.ws_o[ps * D + d] = osum;
       if (d == 0) {
         a.ws_ml[2 * ps] = M;
@@ -793,25 +774,22 @@ __global__ void __launch_bounds__(MmaCfgN<D, NT, NARROW>::kThreads, MmaCfgN<D, N
       }
     }
   }
-  if constexpr (!SHARED) {
-    if (n_work > 1) {
-      __shared__ int s_last;
-      finish_split<__nv_bfloat16, D>(a, b, h0, hpc, split, n_work, reinterpret_cast<float*>(smem), &s_last,
-                                     threadIdx.x, kConsumers, C::kRingBytes);
-    }
+  if (n_work > 1) {
+    __shared__ int s_last;
+    finish_split<__nv_bfloat16, D>(a, b, h0, hpc, split, n_work, reinterpret_cast<float*>(smem), &s_last,
+                                   threadIdx.x, kConsumers, C::kRingBytes);
   }
 }
 
-template <int D, bool PAGED, bool FUSED, int NT, bool NARROW = false, bool SHARED = false>
+template <int D, bool PAGED, bool FUSED, int NT, bool NARROW = false>
 cudaError_t launch_decode_mma_nt(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int hpc,
                                  cudaStream_t st) {
   using C = MmaCfgN<D, NT, NARROW>;
   static int done[64] = {0};
-  auto kern = decode_mma_kernel<D, PAGED, FUSED, NT, NARROW, SHARED>;
+  auto kern = decode_mma_kernel<D, PAGED, FUSED, NT, NARROW>;
   cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  const int splits = SHARED ? a.num_splits - a.prefix_splits : a.num_splits;
-  const dim3 grid(splits * ((a.Hq / a.Hkv) / hpc), a.Hkv, a.B);
+  const dim3 grid(a.num_splits * ((a.Hq / a.Hkv) / hpc), a.Hkv, a.B);
   return launch_pdl(kern, grid, dim3(C::kThreads), C::kSmemBytes, st, km, vm, a);
 }
 

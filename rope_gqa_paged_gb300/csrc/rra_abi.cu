@@ -271,30 +271,28 @@ int check_prefill_limits(int T, int Hq, int Hkv, int64_t capacity) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Shared-prefix attention: the plan of the sequences' own tokens (the decode or verify kernel's) and the
-// chunks of the prefix.
+// Shared-prefix attention: how the sequences' own tokens and the prefix are cut.
 struct SharedPlan {
-  Plan own;
+  int hpc = 1;            // query heads per own-token unit (with gamma tokens at most 16 rows)
+  int chunk = 0;          // own tokens per unit
+  int splits = 1;
   int prefix_splits = 0;  // 0: no separate pass, the own-token kernel reads the prefix too
   int prefix_chunk = 0;
 };
 
 int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq, int block_size,
                      int num_splits, int prefix_splits, SharedPlan* p) {
+  int st = check_shapes(B, Hq, Hkv, D, RRA_BF16);
+  if (st != RRA_OK) return st;
   if (!pow2(block_size)) return block_size <= 0 ? RRA_EINVAL : RRA_EUNSUPPORTED;
-  if (max_blocks_per_seq < 1 || prefix_len < 0 || prefix_splits < 0) return RRA_EINVAL;
+  if (gamma < 1 || max_blocks_per_seq < 1 || prefix_len < 0 || num_splits < 0 || prefix_splits < 0) return RRA_EINVAL;
   const int64_t capacity = int64_t(max_blocks_per_seq) * block_size;
   if (prefix_len > capacity) return RRA_EINVAL;
-  if (prefix_len % block_size != 0) return RRA_EUNSUPPORTED;
-  int st = make_plan_verify(B, gamma, Hq, Hkv, D, capacity, block_size, num_splits, &p->own);
-  if (st != RRA_OK) return st;
+  if (gamma > 16 || block_size < 8 || prefix_len % block_size != 0) return RRA_EUNSUPPORTED;
   const int n_rep = Hq / Hkv;
-  if (gamma == 1) {  // the decode kernel: up to 8 heads per CTA, or 16 (two CTAs per SM)
-    p->own.hpc = decode_mma_hpc(n_rep);
-    if (p->own.hpc > 8) p->own.ctas_per_sm = 2;
-    if (static_cast<int64_t>(Hkv) * (n_rep / p->own.hpc) > 65535) return RRA_ERANGE;
-  }
   const int64_t rows = int64_t(B) * gamma * n_rep;
+  if (capacity > (int64_t(1) << 30) || Hkv > 65535 || int64_t(B) * gamma * Hq > INT32_MAX) return RRA_ERANGE;
+  const int64_t sms = std::max(1, sm_count());
   const bool pass = prefix_len > 0 && rows > 0 && (prefix_splits > 0 || (B > 1 && prefix_len >= 256));
   if (pass) {
     const int nq = rra::shared_prefix_nq(rows), tile = rra::shared_prefix_tile(D, nq);
@@ -302,8 +300,7 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     const int64_t per_cta = nq * rra::kSharedPrefixRows;
     const int64_t units = Hkv * ((rows + per_cta - 1) / per_cta);
     const int64_t max_chunk = std::max<int64_t>(1, int64_t(rra::kSharedPrefixTableEntries) * block_size / tile);
-    if (Hkv > 65535) return RRA_ERANGE;
-    const int64_t resident = (nq == 2 ? 1 : 2) * int64_t(std::max(1, sm_count()));
+    const int64_t resident = (nq == 2 ? 1 : 2) * sms;
     int64_t best = 0, best_cost = INT64_MAX;
     // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
     const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
@@ -319,9 +316,28 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     }
     p->prefix_chunk = static_cast<int>(best * tile);
     p->prefix_splits = static_cast<int>((tiles + best - 1) / best);
-    if (p->prefix_splits > 65535) return RRA_ERANGE;
   }
-  return plan_splits(B, Hkv, n_rep, capacity - (pass ? prefix_len : 0), block_size, num_splits, &p->own);
+  // own tokens: the fewest head slices of at most 16 rows
+  const int slices = (n_rep + 16 / gamma - 1) / (16 / gamma);
+  p->hpc = (n_rep + slices - 1) / slices;
+  const int tok = rra::own_stage_tokens(D);
+  const int64_t stages = std::max<int64_t>(1, (capacity - (pass ? prefix_len : 0) + tok - 1) / tok);
+  // a chunk spans at most kOwnMaxBlocks blocks, wherever in a block it starts
+  const int64_t most = std::max<int64_t>(1, int64_t(rra::kOwnMaxBlocks - 1) * block_size / tok);
+  int64_t chunk;
+  if (num_splits > 0) {
+    chunk = (stages + num_splits - 1) / num_splits;
+  } else {
+    const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), target = 2 * 8 * sms;
+    chunk = (stages * units + target - 1) / target;
+    chunk = std::max<int64_t>(chunk, 256 / tok);
+  }
+  chunk = std::min(std::max<int64_t>(chunk, 1), most);
+  p->chunk = static_cast<int>(chunk * tok);
+  const int64_t splits = (stages + chunk - 1) / chunk;
+  if (splits > 65535 || p->prefix_splits > 65535) return RRA_ERANGE;
+  p->splits = static_cast<int>(splits);
+  return RRA_OK;
 }
 
 // Workspace of shared-prefix attention: partials o [R, S, D] and (max, sum) [R, S, 2] floats, R = B gamma Hq
@@ -330,7 +346,7 @@ struct SharedWs {
   size_t ml, total;
 };
 SharedWs shared_ws(int64_t rows, int D, const SharedPlan& p) {
-  const size_t S = size_t(p.prefix_splits) + p.own.splits;
+  const size_t S = size_t(p.prefix_splits) + p.splits;
   SharedWs w{};
   if (S <= 1 || rows <= 0) return w;
   w.ml = align256(rows * S * D * sizeof(float));
@@ -1320,24 +1336,24 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
                             &p);
   if (st != RRA_OK) return st;
   if (num_blocks < 1 || !std::isfinite(scale)) return RRA_EINVAL;
+  if (int64_t(num_blocks) * (block_size / 8) > INT32_MAX) return RRA_ERANGE;  // groups of 8 rows, a TMA coordinate
   if (B == 0) return RRA_OK;
   if (!q_rot || !k_pool || !v_pool || !block_table || (!seq_lens && !positions) || !out) return RRA_EINVAL;
   if (prefix_len > 0 && !prefix_blocks) return RRA_EINVAL;
   if (!aligned16(q_rot) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return RRA_EINVAL;
   const int64_t rows = int64_t(B) * gamma * Hq;
-  if (rows > INT32_MAX) return RRA_ERANGE;
   const SharedWs w = shared_ws(rows, D, p);
   if (w.total > 0 && (workspace == nullptr || ws_bytes < w.total || !aligned16(workspace))) return RRA_EWORKSPACE;
   if (check_only) return RRA_OK;
-  CUtensorMap km, vm, kg{}, vg{};
-  const int box_rows = block_size < p.own.tile ? block_size : p.own.tile;
-  st = encode_pool_map(&km, k_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
-  if (st == RRA_OK) st = encode_pool_map(&vm, v_pool, num_blocks, block_size, Hkv, D, box_rows, RRA_BF16, true);
+  rra::SharedMaps maps{};
+  const int own_rows = std::min(block_size, rra::own_stage_tokens(D));
+  st = encode_group_map(&maps.k_own, k_pool, num_blocks, block_size, Hkv, D, own_rows);
+  if (st == RRA_OK) st = encode_group_map(&maps.v_own, v_pool, num_blocks, block_size, Hkv, D, own_rows);
   if (st == RRA_OK && p.prefix_splits > 0) {
     const int nq = rra::shared_prefix_nq(int64_t(B) * gamma * (Hq / Hkv));
     const int group_rows = std::min(block_size, rra::shared_prefix_tile(D, nq));
-    st = encode_group_map(&kg, k_pool, num_blocks, block_size, Hkv, D, group_rows);
-    if (st == RRA_OK) st = encode_group_map(&vg, v_pool, num_blocks, block_size, Hkv, D, group_rows);
+    st = encode_group_map(&maps.k_prefix, k_pool, num_blocks, block_size, Hkv, D, group_rows);
+    if (st == RRA_OK) st = encode_group_map(&maps.v_prefix, v_pool, num_blocks, block_size, Hkv, D, group_rows);
   }
   if (st != RRA_OK) return st;
   rra::DecodeArgs a{};
@@ -1359,10 +1375,10 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   a.Hkv = Hkv;
   a.D = D;
   a.gamma = gamma;
-  a.hpc = p.own.hpc;
+  a.hpc = p.hpc;
   a.capacity = max_blocks_per_seq * block_size;
-  a.num_splits = p.prefix_splits + p.own.splits;
-  a.chunk = p.own.chunk;
+  a.num_splits = p.prefix_splits + p.splits;
+  a.chunk = p.chunk;
   a.prefix_blocks = prefix_blocks;
   a.prefix_len = prefix_len;
   a.prefix_splits = p.prefix_splits;
@@ -1371,7 +1387,7 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
   a.scale_log2 = s * 1.4426950408889634f;
   a.err = err_flag;
-  return finish_decode(rra::launch_shared_prefix(a, km, vm, kg, vg, static_cast<cudaStream_t>(stream)));
+  return finish_decode(rra::launch_shared_prefix(a, maps, static_cast<cudaStream_t>(stream)));
 }
 
 int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, int max_blocks_per_seq,
@@ -1382,8 +1398,7 @@ int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int prefix_
                                   prefix_splits, &p);
   if (st != RRA_OK) return st;
   const int64_t rows = int64_t(B) * gamma * Hq;
-  if (rows > INT32_MAX) return RRA_ERANGE;
-  if (own_splits != nullptr) *own_splits = p.own.splits;
+  if (own_splits != nullptr) *own_splits = p.splits;
   if (prefix_chunks != nullptr) *prefix_chunks = p.prefix_splits;
   if (workspace_bytes != nullptr) *workspace_bytes = shared_ws(rows, D, p).total;
   return RRA_OK;

@@ -90,7 +90,7 @@ struct DecodeArgs {
   // Speculative verify (verify.cuh): gamma new tokens per sequence at positions[b] ..
   // positions[b] + gamma - 1; q and out are [B, gamma, Hq, D].
   int gamma;
-  // Shared prefix (shared_prefix.cuh, verify.cuh): the first prefix_len tokens of every sequence are
+  // Shared prefix (shared_prefix.cuh, own_tokens.cuh): the first prefix_len tokens of every sequence are
   // in prefix_blocks. With prefix_splits > 0 their attention is computed for all rows at once, in
   // chunks of prefix_chunk tokens whose partials fill slots [0, prefix_splits) of num_splits; the
   // sequences' own tokens start at first_token (prefix_len, or 0 when prefix_splits is 0).
@@ -204,10 +204,15 @@ constexpr int kSharedPrefixRows = 128;
 __host__ __device__ constexpr int shared_prefix_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
 __host__ __device__ constexpr int shared_prefix_nq(int64_t rows) { return rows > kSharedPrefixRows ? 2 : 1; }
 constexpr int kSharedPrefixTableEntries = 2048;
-// k_map / v_map: the pools as the decode kernels read them; k_groups / v_groups: as {64 dims, 8 rows,
-// D / 64 halves, groups of 8 rows, Hkv} with boxes of min(block size, tile) rows (prefix_splits > 0).
-cudaError_t launch_shared_prefix(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                                 const CUtensorMap& k_groups, const CUtensorMap& v_groups, cudaStream_t stream);
+// tokens of an own-token stage, the most blocks of one own-token chunk
+__host__ __device__ constexpr int own_stage_tokens(int D) { return 2048 / D; }
+constexpr int kOwnMaxBlocks = 128;
+// The pools as {64 dims, 8 rows, D / 64 halves, groups of 8 rows, Hkv}: boxes of min(block size, prefix tile)
+// rows (prefix_splits > 0) and of min(block size, own stage) rows.
+struct SharedMaps {
+  CUtensorMap k_prefix, v_prefix, k_own, v_own;
+};
+cudaError_t launch_shared_prefix(const DecodeArgs& a, const SharedMaps& maps, cudaStream_t stream);
 // Prefill: causal attention of the T = a.gamma prompt tokens of each sequence (a.positions: the
 // first one's position); 64 query rows (a.hpc heads x 64 / a.hpc tokens) per CTA.
 cudaError_t launch_prefill(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, bool paged,

@@ -222,16 +222,7 @@ struct VerifyRows {
 // v_new into the cache, one warp per token, and its producer waits for those writes (an mbarrier
 // with one arrival per token) before the TMA of the first tile that holds a new token. Head-slice
 // CTAs of that chunk write identical bytes.
-//
-// SHARED: the sequences' own tokens of shared-prefix attention, [first_token, L_b). Every split
-// leaves its partial in slot prefix_splits + split of the output row's num_splits slots (a merge
-// kernel follows), or writes the row when there is one slot. The kernel before this one
-// (shared_prefix.cuh) may still be computing the prefix's partials: this one reads only what that
-// kernel's predecessors wrote (past L1; that kernel let it start after it had waited for them), and
-// its first CTA waits for that kernel, so that the merge finds both complete. Lengths may be given
-// (seq_lens; query token j attends the first L_b - gamma + 1 + j tokens, none if that is not
-// positive: a zero row).
-template <int D, bool PAGED, bool FUSED = false, bool SHARED = false>
+template <int D, bool PAGED, bool FUSED = false>
 __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     decode_verify_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
@@ -253,40 +244,20 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
   const VerifyRows out_row{a.Hq, a.Hkv, n_rep, slices, hpc, gamma};
 
   pdl_launch_dependents();
-  if (!SHARED || a.prefix_splits == 0) pdl_wait();  // the kernel before this one (the append, or the previous step) has finished
-  const int start = (SHARED ? a.first_token : 0) + split * a.chunk;
+  pdl_wait();  // the kernel before this one (the append, or the previous step) has finished
   // the chunk's block ids load alongside the position
   ChunkBlockIds<(kMmaTableEntries + C::kThreads - 1) / C::kThreads> pre_ids;
-  if constexpr (SHARED) pre_ids.load_shared(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
-  else if constexpr (PAGED) pre_ids.load(a, b, start >> a.log2_bs, threadIdx.x, C::kThreads);
+  if constexpr (PAGED) pre_ids.load(a, b, (split * a.chunk) >> a.log2_bs, threadIdx.x, C::kThreads);
 
-  int p0, L;
-  if (SHARED && a.positions == nullptr) {
-    L = __ldcg(a.seq_lens + b);
-    if (L < 0 || L > a.capacity) {
-      if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_SEQ_LEN);
-      L = min(max(L, 0), a.capacity);
-    }
-    p0 = L - gamma;  // token j attends [0, p0 + j], which may be empty
-  } else {
-    p0 = SHARED ? __ldcg(a.positions + b) : a.positions[b];
-    L = p0 + gamma;
-    if (p0 < (SHARED ? a.prefix_len : 0) || L > a.capacity) {
-      if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
-      if (SHARED) shared_wait_first(a);
-      return;
-    }
-  }
-  const int n_work = (L + a.chunk - 1) / a.chunk;
-  if (start >= L) {
-    if constexpr (SHARED) {
-      if (a.num_splits == 1)  // no merge kernel: the empty sequence's rows are zero
-        for (int i = threadIdx.x; i < rows * D; i += blockDim.x)
-          static_cast<__nv_bfloat16*>(a.out)[out_row(vbase + i / D) * D + i % D] = __float2bfloat16_rn(0.f);
-      shared_wait_first(a);
-    }
+  const int p0 = a.positions[b];
+  int L = p0 + gamma;
+  if (p0 < 0 || L > a.capacity) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) flag_error(a.err, RRA_ERR_POSITION);
     return;
   }
+  const int start = split * a.chunk;
+  const int n_work = (L + a.chunk - 1) / a.chunk;
+  if (start >= L) return;
   const int end = min(L, start + a.chunk);
   const int n_tiles = (end - start + C::kTile - 1) / C::kTile;
   // fused step: new tokens app_lo .. app_hi - 1 lie in this chunk and are appended here
@@ -325,7 +296,6 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
     }
-    if constexpr (SHARED) asm volatile("fence.proxy.async.global;" ::: "memory");  // the append's writes, for the copies
     int issued = 0;
     for (int it = 0; it < n_tiles; ++it) {
       const int s = it % C::kStages;
@@ -373,7 +343,6 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
     if (lane == 0)
       for (int it = issued > C::kStages ? issued - C::kStages : 0; it < issued; ++it)
         mbar_wait(&full[it % C::kStages], (it / C::kStages) & 1);
-    if constexpr (SHARED) shared_wait_first(a);
     return;
   }
 
@@ -392,13 +361,8 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
         static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<size_t>(b) * gamma + j) * a.Hq + h0 + hh) * D);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      if constexpr (SHARED) {
-        qa[kk][i] = r < rows ? __ldcg(q + kk * 8 + t) : 0u;
-        qa[kk][2 + i] = r < rows ? __ldcg(q + kk * 8 + 4 + t) : 0u;
-      } else {
-        qa[kk][i] = r < rows ? q[kk * 8 + t] : 0u;
-        qa[kk][2 + i] = r < rows ? q[kk * 8 + 4 + t] : 0u;
-      }
+      qa[kk][i] = r < rows ? q[kk * 8 + t] : 0u;
+      qa[kk][2 + i] = r < rows ? q[kk * 8 + 4 + t] : 0u;
     }
   }
   if constexpr (FUSED) {
@@ -546,11 +510,10 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
 #pragma unroll
     for (int w = 0; w < C::kConsumerWarps; ++w)
       osum = fmaf(red_w[w * kVerifyRows + r], red_o[(w * kVerifyRows + r) * kRS + d], osum);
-    if (SHARED ? a.num_splits == 1 : n_work == 1) {
+    if (n_work == 1) {
       static_cast<__nv_bfloat16*>(a.out)[out_row(vbase + r) * D + d] = __float2bfloat16_rn(lsum > 0.f ? osum / lsum : 0.f);
     } else {
-      const size_t ps = SHARED ? out_row(vbase + r) * a.num_splits + a.prefix_splits + split
-                               : (vbase + r) * a.num_splits + split;
+      const size_t ps = (vbase + r) * a.num_splits + split;
       a.ws_o[ps * D + d] = osum;
       if (d == 0) {
         a.ws_ml[2 * ps] = Mx;
@@ -558,27 +521,24 @@ __global__ void __launch_bounds__(MmaCfg<D>::kThreads, RRA_MMA_CTAS_PER_SM)
       }
     }
   }
-  if constexpr (!SHARED) {
-    if (n_work > 1) {
-      __shared__ int s_last;
-      finish_split_rows<__nv_bfloat16, D, VerifyRows, false>(a, vbase, rows, split, n_work,
-                                                             reinterpret_cast<float*>(smem), &s_last, threadIdx.x,
-                                                             kConsumers, out_row, C::kRingBytes);
-    }
+  if (n_work > 1) {
+    __shared__ int s_last;
+    finish_split_rows<__nv_bfloat16, D, VerifyRows, false>(a, vbase, rows, split, n_work,
+                                                           reinterpret_cast<float*>(smem), &s_last, threadIdx.x,
+                                                           kConsumers, out_row, C::kRingBytes);
   }
 }
 
-template <int D, bool PAGED, bool FUSED, bool SHARED = false>
+template <int D, bool PAGED, bool FUSED>
 cudaError_t launch_decode_verify_t(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
                                    cudaStream_t st) {
   using C = MmaCfg<D>;
   constexpr int kSmem = verify_smem_bytes<D>(FUSED);
   static int done[64] = {0};
-  auto kern = decode_verify_kernel<D, PAGED, FUSED, SHARED>;
+  auto kern = decode_verify_kernel<D, PAGED, FUSED>;
   cudaError_t e = ensure_smem(kern, kSmem, done);
   if (e != cudaSuccess) return e;
-  const int splits = SHARED ? a.num_splits - a.prefix_splits : a.num_splits;
-  const dim3 grid(splits * ((a.Hq / a.Hkv) / a.hpc), a.Hkv, a.B);
+  const dim3 grid(a.num_splits * ((a.Hq / a.Hkv) / a.hpc), a.Hkv, a.B);
   return launch_pdl(kern, grid, dim3(C::kThreads), kSmem, st, km, vm, a);
 }
 
