@@ -57,18 +57,20 @@ struct Cfg {
   static constexpr int kTileBytes = kTile / 8 * kGroupBytes;
   static constexpr int kQHalfBytes = kRows * 128;          // NQ 2: Q tiles, K-major, 64-dim halves
   static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
-  static constexpr int kSlots = NQ == 2 ? (D == 64 ? 4 : 2) : 3;  // of K, and as many of V
+#ifndef SP_RING2
+#define SP_RING2 4
+#endif
+  static constexpr int kRing = NQ == 2 ? (D == 64 ? 6 : SP_RING2) : 6;  // slots: K_0, V_0, K_1, V_1, ...
   // Tensor Memory columns
   static constexpr uint32_t kColO = 0;                     // O_k: D columns each
   static constexpr uint32_t kColS = NQ * D;                // S_k: kTile columns each, P over their first half
   static constexpr uint32_t kColQ = kColS + NQ * kTile;    // NQ 1: Q as bf16 pairs, D / 2 columns
   static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
   // shared memory
-  static constexpr int kOffK = kQBytes;
-  static constexpr int kOffV = kOffK + kSlots * kTileBytes;
-  static constexpr int kOffBar = kOffV + kSlots * kTileBytes;
-  // q_ready, k_full, k_empty, v_full, v_empty, s_full[NQ], p_full[NQ], mma_done
-  static constexpr int kNumBars = 1 + 4 * kSlots + 2 * NQ + 1;
+  static constexpr int kOffRing = kQBytes;
+  static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
+  // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ], mma_done
+  static constexpr int kNumBars = 1 + 2 * kRing + 2 * NQ + 1;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffTable = kOffTmemSlot + 16;
   static constexpr int kSmemBytes = 1024 + kOffTable + kSharedPrefixTableEntries * 4;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
   using C = Cfg<D, NQ>;
-  constexpr int kTile = C::kTile, kSlots = C::kSlots;
+  constexpr int kTile = C::kTile, kRing = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -155,11 +157,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   const int last_valid = end - start - (n_tiles - 1) * kTile;  // keys of the last tile
 
   uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* k_full = q_ready + 1;
-  uint64_t* k_empty = k_full + kSlots;
-  uint64_t* v_full = k_empty + kSlots;
-  uint64_t* v_empty = v_full + kSlots;
-  uint64_t* s_full = v_empty + kSlots;
+  uint64_t* ring_full = q_ready + 1;
+  uint64_t* ring_empty = ring_full + kRing;
+  uint64_t* s_full = ring_empty + kRing;
   uint64_t* p_full = s_full + NQ;
   uint64_t* mma_done = p_full + NQ;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
@@ -167,11 +167,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 4 * NQ);  // one arrival per softmax warp
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], NQ);  // every row tile gives a slot back
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], NQ);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ring_full[s], 1);
+      mbar_init(&ring_empty[s], NQ);  // every row tile gives a slot back
     }
     for (int k = 0; k < NQ; ++k) mbar_init(&s_full[k], 1);
     for (int k = 0; k < NQ; ++k) mbar_init(&p_full[k], 4);
@@ -202,8 +200,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  auto slot_of = [](int j) { return j % kSlots; };
-  auto phase_of = [](int j) { return static_cast<uint32_t>((j / kSlots) & 1); };
+  // ring position r: K of tile r / 2 (r even) or its V (r odd)
+  auto slot_of = [](int r) { return r % kRing; };
+  auto phase_of = [](int r) { return static_cast<uint32_t>((r / kRing) & 1); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
@@ -213,38 +212,31 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     }
     const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
     const int box = min(bs, kTile);  // rows per TMA box, as the tensor maps were encoded
-    // tile j of K or V into its slot; false once a wait ran out
-    auto load = [&](const CUtensorMap* map, int off, uint64_t* full, uint64_t* empty, int j) -> bool {
-      const int s = slot_of(j), tile0 = start + j * kTile;
+    int issued = 0;
+    for (int p = 0; p < 2 * n_tiles; ++p) {
+      const int s = slot_of(p), tile0 = start + (p >> 1) * kTile;
       const int nbox = (min(kTile, end - tile0) + box - 1) / box;
       int ok = 1;
       if (lane == 0) {
-        if (j >= kSlots && !mbar_wait(&empty[s], phase_of(j) ^ 1u))
+        if (p >= kRing && !mbar_wait(&ring_empty[s], phase_of(p) ^ 1u))
           ok = 0;
         else
-          mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
+          mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       if (lane < nbox) {  // one copy per lane (at most 16)
         const int t = tile0 + lane * box;
         const int rows8 = (tbl[(t >> log2_bs) - first_blk] << (log2_bs - 3)) + ((t & (bs - 1)) >> 3);
-        tma_g2s_5d(smem + off + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, map, 0, 0, 0, rows8, g, &full[s]);
+        tma_g2s_5d(smem + C::kOffRing + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, (p & 1) ? &v_map : &k_map, 0,
+                   0, 0, rows8, g, &ring_full[s]);
       }
       __syncwarp();
-      return true;
-    };
-    int nk = 0, nv = 0;
-    while (nv < n_tiles) {
-      if (!load(&k_map, C::kOffK, k_full, k_empty, nk)) break;
-      ++nk;
-      if (!load(&v_map, C::kOffV, v_full, v_empty, nv)) break;
-      ++nv;
+      issued = p + 1;
     }
     if (lane == 0) {
-      if (nv < n_tiles) flag_error(a.err, RRA_ERR_TIMEOUT);
+      if (issued < 2 * n_tiles) flag_error(a.err, RRA_ERR_TIMEOUT);
       // no copy may still be landing when the CTA exits
-      for (int j = max(nk - kSlots, 0); j < nk; ++j) mbar_wait(&k_full[slot_of(j)], phase_of(j));
-      for (int j = max(nv - kSlots, 0); j < nv; ++j) mbar_wait(&v_full[slot_of(j)], phase_of(j));
+      for (int p = max(issued - kRing, 0); p < issued; ++p) mbar_wait(&ring_full[slot_of(p)], phase_of(p));
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
@@ -253,12 +245,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
       bool ok = mbar_wait(q_ready, 0);
       tc::fence_after_sync();
       auto issue_s = [&](int k, int j) -> bool {
-        const int s = slot_of(j);
+        const int s = slot_of(2 * j);
         if (k == 0) {
-          if (!mbar_wait(&k_full[s], phase_of(j))) return false;
+          if (!mbar_wait(&ring_full[s], phase_of(2 * j))) return false;
           tc::fence_after_sync();
         }
-        const uint32_t k_base = base + C::kOffK + s * C::kTileBytes, s_col = tmem + C::kColS + kTile * k;
+        const uint32_t k_base = base + C::kOffRing + s * C::kTileBytes, s_col = tmem + C::kColS + kTile * k;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * 1024 + (kk & 3) * 32, 1024, C::kGroupBytes);
@@ -275,9 +267,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
 #pragma unroll
       for (int k = 0; k < NQ; ++k) ok = ok && issue_s(k, 0);
       for (int j = 0; ok && j < n_tiles; ++j) {
-        const int s = slot_of(j);
-        const uint32_t v_base = base + C::kOffV + s * C::kTileBytes;
-        ok = mbar_wait(&v_full[s], phase_of(j));
+        const int s = slot_of(2 * j + 1);
+        const uint32_t v_base = base + C::kOffRing + s * C::kTileBytes;
+        ok = mbar_wait(&ring_full[s], phase_of(2 * j + 1));
 #pragma unroll
         for (int k = 0; k < NQ; ++k) {
           if (!ok || !mbar_wait(&p_full[k], j & 1)) {
@@ -353,18 +345,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
       }
       tc::fence_after_sync();
       if (r == 0) {
-        mbar_arrive(&k_empty[slot_of(j)]);
-        if (j > 0) mbar_arrive(&v_empty[slot_of(j - 1)]);
+        mbar_arrive(&ring_empty[slot_of(2 * j)]);
+        if (j > 0) mbar_arrive(&ring_empty[slot_of(2 * j - 1)]);
       }
       if (j == n_tiles - 1 && last_valid < kTile) {
         // keys past the prefix: their V rows are whatever the slot held; zeros keep 0 * V at 0 (both
         // row tiles' threads write them, each before its own P.V)
-        if (!warp_wait(&v_full[slot_of(j)], phase_of(j))) {
+        if (!warp_wait(&ring_full[slot_of(2 * j + 1)], phase_of(2 * j + 1))) {
           ok = false;
           break;
         }
         if (r >= last_valid && r < kTile) {
-          uint8_t* vrow = smem + C::kOffV + slot_of(j) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
+          uint8_t* vrow = smem + C::kOffRing + slot_of(2 * j + 1) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
