@@ -299,14 +299,13 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     const int64_t tiles = (prefix_len + tile - 1) / tile;
     const int64_t per_cta = nq * rra::kSharedPrefixRows;
     const int64_t units = Hkv * ((rows + per_cta - 1) / per_cta);
-    const int64_t max_chunk = std::max<int64_t>(1, int64_t(rra::kSharedPrefixTableEntries) * block_size / tile);
     const int64_t resident = (nq == 2 ? 1 : 2) * sms;
     int64_t best = 0, best_cost = INT64_MAX;
     // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
     const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
     const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, 40);
     for (int64_t s = lo; s <= hi; ++s) {
-      const int64_t chunk = std::min((tiles + s - 1) / s, max_chunk), n = (tiles + chunk - 1) / chunk;
+      const int64_t chunk = (tiles + s - 1) / s, n = (tiles + chunk - 1) / chunk;
       const int64_t waves = (units * n + resident - 1) / resident;
       const int64_t cost = waves * (chunk + 6);
       if (cost < best_cost) {

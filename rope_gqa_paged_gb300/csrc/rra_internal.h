@@ -198,12 +198,11 @@ cudaError_t launch_decode_verify(const DecodeArgs& a, const CUtensorMap& k_map, 
 // Largest gamma of the one-launch verify step.
 constexpr int kVerifyFusedMaxGammaHost = 8;
 // Shared-prefix attention (a.seq_lens or a.positions, the prefix fields, a.gamma, a.hpc set): query rows
-// of a prefix row tile, row tiles per CTA for that many rows per KV head, the most blocks of one chunk.
+// of a prefix row tile, row tiles per CTA for that many rows per KV head.
 constexpr int kSharedPrefixRows = 128;
 // keys of a tile: 64 (128 at head dim 64) for one row tile per CTA, 128 for two (NQ)
 __host__ __device__ constexpr int shared_prefix_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
 __host__ __device__ constexpr int shared_prefix_nq(int64_t rows) { return rows > kSharedPrefixRows ? 2 : 1; }
-constexpr int kSharedPrefixTableEntries = 2048;
 // tokens of an own-token stage, the most blocks of one own-token chunk
 __host__ __device__ constexpr int own_stage_tokens(int D) { return 2048 / D; }
 constexpr int kOwnMaxBlocks = 128;

@@ -57,10 +57,7 @@ struct Cfg {
   static constexpr int kTileBytes = kTile / 8 * kGroupBytes;
   static constexpr int kQHalfBytes = kRows * 128;          // NQ 2: Q tiles, K-major, 64-dim halves
   static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
-#ifndef SP_RING2
-#define SP_RING2 4
-#endif
-  static constexpr int kRing = NQ == 2 ? (D == 64 ? 6 : SP_RING2) : 6;  // slots: K_0, V_0, K_1, V_1, ...
+  static constexpr int kRing = NQ == 2 && D == 128 ? 4 : 6;  // slots: K_0, V_0, K_1, V_1, ...
   // Tensor Memory columns
   static constexpr uint32_t kColO = 0;                     // O_k: D columns each
   static constexpr uint32_t kColS = NQ * D;                // S_k: kTile columns each, P over their first half
@@ -72,8 +69,7 @@ struct Cfg {
   // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ], mma_done
   static constexpr int kNumBars = 1 + 2 * kRing + 2 * NQ + 1;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
-  static constexpr int kOffTable = kOffTmemSlot + 16;
-  static constexpr int kSmemBytes = 1024 + kOffTable + kSharedPrefixTableEntries * 4;
+  static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
   static constexpr int kSoftmaxThreads = 128 * NQ;
   static constexpr int kThreads = kSoftmaxThreads + 64;    // + producer warp + MMA warp
   static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
@@ -163,7 +159,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   uint64_t* p_full = s_full + NQ;
   uint64_t* mma_done = p_full + NQ;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
-  int32_t* tbl = reinterpret_cast<int32_t*>(smem + C::kOffTable);
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 4 * NQ);  // one arrival per softmax warp
@@ -185,18 +180,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   // only when this wait is over: every kernel before this one has then completed.
   pdl_wait();
   pdl_launch_dependents();
-  const int first_blk = start >> a.log2_bs;
-  {
-    const int n_blk = ((end - 1) >> a.log2_bs) - first_blk + 1;
-    for (int i = threadIdx.x; i < n_blk; i += C::kThreads) {
-      int id = a.prefix_blocks[first_blk + i];
-      if (id < 0 || id >= a.num_blocks) {
-        flag_error(a.err, RRA_ERR_BLOCK_ID);
-        id = 0;
-      }
-      tbl[i] = id;
-    }
-  }
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
@@ -212,26 +195,37 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     }
     const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
     const int box = min(bs, kTile);  // rows per TMA box, as the tensor maps were encoded
-    int issued = 0;
-    for (int p = 0; p < 2 * n_tiles; ++p) {
-      const int s = slot_of(p), tile0 = start + (p >> 1) * kTile;
-      const int nbox = (min(kTile, end - tile0) + box - 1) / box;
-      int ok = 1;
-      if (lane == 0) {
-        if (p >= kRing && !mbar_wait(&ring_empty[s], phase_of(p) ^ 1u))
-          ok = 0;
-        else
-          mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
+    // group of 8 rows where this lane's box of tile j starts (the id loads a tile ahead of its use)
+    auto block_of = [&](int j) {
+      const int t = start + j * kTile + lane * box;
+      return lane < kTile / box && t < end ? __ldcg(a.prefix_blocks + (t >> log2_bs)) : 0;
+    };
+    int issued = 0, next = block_of(0);
+    for (int j = 0; j < n_tiles && issued == 2 * j; ++j) {
+      const int tile0 = start + j * kTile, nbox = (min(kTile, end - tile0) + box - 1) / box;
+      int id = next;
+      next = block_of(j + 1);
+      if (id < 0 || id >= a.num_blocks) {
+        flag_error(a.err, RRA_ERR_BLOCK_ID);
+        id = 0;
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      if (lane < nbox) {  // one copy per lane (at most 16)
-        const int t = tile0 + lane * box;
-        const int rows8 = (tbl[(t >> log2_bs) - first_blk] << (log2_bs - 3)) + ((t & (bs - 1)) >> 3);
-        tma_g2s_5d(smem + C::kOffRing + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, (p & 1) ? &v_map : &k_map, 0,
-                   0, 0, rows8, g, &ring_full[s]);
+      const int rows8 = (id << (log2_bs - 3)) + (((tile0 + lane * box) & (bs - 1)) >> 3);
+      for (int p = 2 * j; p < 2 * j + 2; ++p) {
+        const int s = slot_of(p);
+        int ok = 1;
+        if (lane == 0) {
+          if (p >= kRing && !mbar_wait(&ring_empty[s], phase_of(p) ^ 1u))
+            ok = 0;
+          else
+            mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        if (lane < nbox)  // one copy per lane (at most 16)
+          tma_g2s_5d(smem + C::kOffRing + s * C::kTileBytes + lane * (box >> 3) * C::kGroupBytes, (p & 1) ? &v_map : &k_map,
+                     0, 0, 0, rows8, g, &ring_full[s]);
+        __syncwarp();
+        issued = p + 1;
       }
-      __syncwarp();
-      issued = p + 1;
     }
     if (lane == 0) {
       if (issued < 2 * n_tiles) flag_error(a.err, RRA_ERR_TIMEOUT);

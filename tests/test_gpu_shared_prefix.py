@@ -157,10 +157,10 @@ def test_prefix_ends_inside_a_tile(R, P, pre):
     check(c.run(R, 0, pre)[0], *c.expect())
 
 
-def test_small_blocks_bound_a_chunk(R):
-    """One prefix chunk holds at most 2048 blocks: 8-token blocks force a second chunk."""
+def test_long_prefix_in_small_blocks(R):
+    """More than 2000 blocks of 8 tokens in one prefix chunk."""
     c = Case([17000, 16800], 1, 4, 1, 64, 8, 16704, seed=5)
-    assert c.plan(R, 0, 1)[1] == 2
+    assert c.plan(R, 0, 1)[1] == 1
     check(c.run(R, 0, 1)[0], *c.expect())
 
 
