@@ -292,48 +292,70 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   const int n_rep = Hq / Hkv;
   const int64_t rows = int64_t(B) * gamma * n_rep;
   if (capacity > (int64_t(1) << 30) || Hkv > 65535 || int64_t(B) * gamma * Hq > INT32_MAX) return RRA_ERANGE;
-  const int64_t sms = std::max(1, sm_count());
-  const bool pass = prefix_len > 0 && rows > 0 && (prefix_splits > 0 || (B > 1 && prefix_len >= 256));
-  if (pass) {
-    const int nq = rra::shared_prefix_nq(rows), tile = rra::shared_prefix_tile(D, nq);
-    const int64_t tiles = (prefix_len + tile - 1) / tile;
-    const int64_t per_cta = nq * rra::kSharedPrefixRows;
-    const int64_t units = Hkv * ((rows + per_cta - 1) / per_cta);
-    const int64_t resident = (nq == 2 ? 1 : 2) * sms;
-    int64_t best = 0, best_cost = INT64_MAX;
-    // chunks whose last wave is fullest; a CTA's start and epilogue cost about as much as 6 tiles
-    const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
-    const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, 40);
-    for (int64_t s = lo; s <= hi; ++s) {
-      const int64_t chunk = (tiles + s - 1) / s, n = (tiles + chunk - 1) / chunk;
-      const int64_t waves = (units * n + resident - 1) / resident;
-      const int64_t cost = waves * (chunk + 6);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = chunk;
-      }
-    }
-    p->prefix_chunk = static_cast<int>(best * tile);
-    p->prefix_splits = static_cast<int>((tiles + best - 1) / best);
-  }
   // own tokens: the fewest head slices of at most 16 rows
   const int slices = (n_rep + 16 / gamma - 1) / (16 / gamma);
   p->hpc = (n_rep + slices - 1) / slices;
-  const int tok = rra::own_stage_tokens(D);
-  const int64_t stages = std::max<int64_t>(1, (capacity - (pass ? prefix_len : 0) + tok - 1) / tok);
-  // a chunk spans at most kOwnMaxBlocks blocks, wherever in a block it starts
-  const int64_t most = std::max<int64_t>(1, int64_t(rra::kOwnMaxBlocks - 1) * block_size / tok);
-  int64_t chunk;
-  if (num_splits > 0) {
-    chunk = (stages + num_splits - 1) / num_splits;
-  } else {
-    const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), target = 2 * 8 * sms;
-    chunk = (stages * units + target - 1) / target;
-    chunk = std::max<int64_t>(chunk, 256 / tok);
+  const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), sms = std::max(1, sm_count());
+  // Splits of `tokens` own tokens per sequence. Chunks of 256 tokens while that makes at most two waves of
+  // the eight CTAs that fit an SM (ragged sequences fill the second one by halves; 48 sequences of up
+  // to 1500 tokens: 62 us with 256, 70 us with 512 and 768); longer ones that make one wave beyond
+  // (16 sequences of 6144 tokens x 8 heads: 69.6 us with 9 splits, 75 us with 19); shorter ones, down to
+  // 64, where not even half a wave would be there (a warp takes 0.3 us per 16 tokens: 4 sequences of 550
+  // tokens x 8 heads 13.0 us with 3 splits, 8.2 us with 9).
+  auto own_plan = [&](int64_t tokens, int64_t* chunk_tokens) -> int64_t {
+    const int tok = rra::own_stage_tokens(D);
+    const int64_t stages = std::max<int64_t>(1, (tokens + tok - 1) / tok), resident = 8 * sms;
+    int64_t chunk = 256 / tok;
+    if (num_splits > 0)
+      chunk = (stages + num_splits - 1) / num_splits;
+    else if (2 * units * ((stages + chunk - 1) / chunk) < resident)
+      chunk = std::min(chunk, std::max<int64_t>(64 / tok, 2 * stages * units / resident));
+    else if (units * ((stages + chunk - 1) / chunk) > 2 * resident)
+      chunk = std::max(chunk, (stages + std::max<int64_t>(1, resident / units) - 1) / std::max<int64_t>(1, resident / units));
+    // a chunk spans at most kOwnMaxBlocks blocks, wherever in a block it starts
+    chunk = std::min(chunk, std::max<int64_t>(1, int64_t(rra::kOwnMaxBlocks - 1) * block_size / tok));
+    const int64_t splits = (stages + chunk - 1) / chunk;
+    chunk = (stages + splits - 1) / splits;  // as even as they can be
+    *chunk_tokens = chunk * tok;
+    return (stages + chunk - 1) / chunk;
+  };
+  int64_t chunk = 0, splits = own_plan(capacity, &chunk);  // prefix and own tokens together
+  if (prefix_len > 0 && rows > 0) {
+    // What the two ways would take, in us. Rates measured on one GB300: own tokens 5.2 TB/s with up to 8
+    // rows per unit and 3.8 with more, 7 where most come from L2; a prefix CTA 6 us and per key tile 0.8
+    // us (two CTAs per SM) or 1.75 us (two row tiles); partials 7 TB/s, written and read. Sequences are taken to fill half of the capacity.
+    const double own_rate = 1e6 * (p->hpc * gamma > 8 ? 3.8 : 5.2), row_bytes = 8.0 * D * B * gamma * Hq;
+    const double token_bytes = 4.0 * D * units;  // of one token of every sequence, as often as it is read
+    const double own_bytes = token_bytes * (capacity - prefix_len) / 2;
+    auto merge = [&](int64_t s) { return s > 1 ? 2.0 + s * row_bytes / 7e6 : 0.0; };
+    double best = (token_bytes * prefix_len + own_bytes) / 7e6 + 3.0 + merge(splits);
+    int64_t own_chunk = 0;
+    const int64_t own_splits = own_plan(capacity - prefix_len, &own_chunk);
+    const int nq = rra::shared_prefix_nq(rows), tile = rra::shared_prefix_tile(D, nq);
+    const int64_t tiles = (prefix_len + tile - 1) / tile;
+    const int64_t row_ctas = (rows + nq * rra::kSharedPrefixRows - 1) / (nq * rra::kSharedPrefixRows);
+    const int64_t ctas = Hkv * row_ctas, resident = (nq == 2 ? 1 : 2) * sms;
+    const double tile_us = nq == 1 ? 0.8 : 1.75;
+    const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
+    const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, std::max<int64_t>(1, 2 * resident / ctas));
+    for (int64_t s = lo; s <= hi; ++s) {
+      const int64_t len = (tiles + s - 1) / s, n = (tiles + len - 1) / len;
+      const int64_t waves = (ctas * n + resident - 1) / resident;
+      const double pass_us = waves * (len * tile_us + 6.0);
+      // meanwhile own-token CTAs run on the SMs left over, and one beside each prefix CTA
+      const double left = std::max(0.0, 1.0 - double(ctas * n) / resident);
+      const double rest = std::max(0.0, own_bytes - own_rate * (left + 0.12 * (1 - left)) * pass_us);
+      const double us = pass_us + rest / own_rate + merge(n + own_splits);
+      if (us < best || prefix_splits > 0) {
+        best = us;
+        p->prefix_chunk = static_cast<int>(len * tile);
+        p->prefix_splits = static_cast<int>(n);
+        chunk = own_chunk;
+        splits = own_splits;
+      }
+    }
   }
-  chunk = std::min(std::max<int64_t>(chunk, 1), most);
-  p->chunk = static_cast<int>(chunk * tok);
-  const int64_t splits = (stages + chunk - 1) / chunk;
+  p->chunk = static_cast<int>(chunk);
   if (splits > 65535 || p->prefix_splits > 65535) return RRA_ERANGE;
   p->splits = static_cast<int>(splits);
   return RRA_OK;

@@ -24,17 +24,22 @@
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
 // so S may overwrite the P before it, and one commit per S says that everything before it is
 // complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back to
-// the producer. The lane is an elected one (elect_one) and the commits few: with a lane chosen by
-// its index and three commits per tile of 64 keys, 512 rows x 8 heads x 16384 keys took 230 us
-// against ## us. (A second MMA warp, one per row tile, was slower.)
+// the producer. A row tile's chain is softmax, P.V, S, softmax, ...; the first half of P.V runs while
+// the second half of the softmax does. What this took, 512 rows x 8 heads x 16384 keys in two chunks
+// (137 GFLOP, with the merge): 244 us with a lane chosen by its index, key tiles of 64 and three
+// commits a tile; 164 us with tiles of 128 and one commit; 151 us with an elected lane (elect_one);
+// 121 us with one ring of four slots and rows that leave by bulk copies; 109 us with P in two
+// halves and paired float32 instructions (1263 TFLOP/s). Slower: a second MMA warp; three ring slots,
+// with or without L2 prefetches; a part of the ex2 as polynomials on the FMA pipe (the softmax is
+// bound by its instructions, not by the special-function units).
 //
 // Two shapes of CTA:
 // * NQ = 1 (up to 128 rows per KV head): key tiles of 64 (128 at head dim 64), Q in Tensor Memory, 256 of
 //   its columns, two CTAs per SM: while one is in its softmax the other's MMAs run, and two
 //   CTAs' copies together keep up with HBM, which bounds this case (the prefix is read once).
 // * NQ = 2 (more rows): key tiles of 128, one CTA per SM, K and V serve 256 rows, Q in shared memory; one
-//   row tile's MMAs run while the other is in its softmax. Bound: those two in turn, 1024 clocks of MMAs
-//   and 1024 of ex2 (16 a clock) per row tile and key tile.
+//   row tile's MMAs run while the other is in its softmax. Bound: that chain, some 1300 clocks per row
+//   tile and key tile, of which the MMAs are 1024.
 //
 // Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain); the MMA lane waits for
 // its last commit and the producer for its last copies before Tensor Memory is released.
@@ -48,6 +53,7 @@ namespace spx {
 
 constexpr int kRows = kSharedPrefixRows;        // rows of a tile: M of every MMA
 constexpr float kRescaleLog2 = 8.f;             // move the running max only when it grows by more
+constexpr int kParts = 2;                        // of a P tile, each handed to the MMAs as soon as it is there
 
 template <int D, int NQ>
 struct Cfg {
@@ -66,8 +72,8 @@ struct Cfg {
   // shared memory
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffBar = kOffRing + kRing * kTileBytes;
-  // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ], mma_done
-  static constexpr int kNumBars = 1 + 2 * kRing + 2 * NQ + 1;
+  // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ][kParts], mma_done
+  static constexpr int kNumBars = 1 + 2 * kRing + NQ + NQ * kParts + 1;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
   static constexpr int kSoftmaxThreads = 128 * NQ;
@@ -106,6 +112,42 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the special-function 
   return y;
 }
 
+// Two float32 operations in one instruction, on pairs (lo, hi).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ float lo2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t c) {
+  uint64_t z;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(x), "l"(y), "l"(c));
+  return z;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Eight columns of this thread's row times alpha.
+__device__ __forceinline__ void scale_cols8(uint32_t taddr, float alpha) {
+  uint32_t v[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // N (a multiple of 32) consecutive 32-bit columns of this thread's row.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&s)[N]) {
@@ -120,12 +162,16 @@ __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&s)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&s)[N]) {
+  if constexpr (N == 16) {
+    tc::tmem_st16(taddr, s);
+  } else {
 #pragma unroll
-  for (int c = 0; c < N / 32; ++c) {
-    uint32_t t[32];
+    for (int c = 0; c < N / 32; ++c) {
+      uint32_t t[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t[i] = s[32 * c + i];
-    tc::tmem_st32(taddr + 32 * c, t);
+      for (int i = 0; i < 32; ++i) t[i] = s[32 * c + i];
+      tc::tmem_st32(taddr + 32 * c, t);
+    }
   }
 }
 
@@ -157,7 +203,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   uint64_t* ring_empty = ring_full + kRing;
   uint64_t* s_full = ring_empty + kRing;
   uint64_t* p_full = s_full + NQ;
-  uint64_t* mma_done = p_full + NQ;
+  uint64_t* mma_done = p_full + NQ * kParts;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
 
   if (threadIdx.x == 0) {
@@ -167,7 +213,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
       mbar_init(&ring_empty[s], NQ);  // every row tile gives a slot back
     }
     for (int k = 0; k < NQ; ++k) mbar_init(&s_full[k], 1);
-    for (int k = 0; k < NQ; ++k) mbar_init(&p_full[k], 4);
+    for (int k = 0; k < NQ * kParts; ++k) mbar_init(&p_full[k], 4);
     mbar_init(mma_done, 1);
     fence_barrier_init();
   }
@@ -266,17 +312,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         ok = mbar_wait(&ring_full[s], phase_of(2 * j + 1));
 #pragma unroll
         for (int k = 0; k < NQ; ++k) {
-          if (!ok || !mbar_wait(&p_full[k], j & 1)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            if (kk % (kTile / 16 / kParts) == 0) {
+              ok = ok && mbar_wait(&p_full[k * kParts + kk / (kTile / 16 / kParts)], j & 1);
+              if (!ok) break;
+              tc::fence_after_sync();
+            }
             tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + 8 * kk,
                             tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV,
                             (j > 0 || kk > 0) ? 1u : 0u);
-          if (j + 1 < n_tiles) ok = issue_s(k, j + 1);
+          }
+          if (ok && j + 1 < n_tiles) ok = issue_s(k, j + 1);
         }
       }
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
@@ -367,13 +414,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
 #pragma unroll
           for (int c = 0; c < kTile; ++c) sv[c] = c < vis ? sv[c] : __float_as_uint(-INFINITY);
         }
-        float mx[8];
+        float mx[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(sv[c]);
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1]));
 #pragma unroll
-        for (int c = 8; c < kTile; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(sv[c]));
-        const float rmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        for (int c = 8; c < kTile; c += 2)
+          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+        const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float m_new = fmaxf(m_use, rmax * sl);
         const bool rescale = m_new > m_use + kRescaleLog2;  // also the first finite max
         float alpha = 1.f;
@@ -381,34 +428,41 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
           alpha = ex2(m_use - m_new);
           m_use = m_new;
         }
-        const float mref = m_use == -INFINITY ? 0.f : m_use;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pw[kTile / 2];
-#pragma unroll
-        for (int c = 0; c < kTile / 2; ++c) {
-          const float e0 = ex2(fmaf(__uint_as_float(sv[2 * c]), sl, -mref));
-          const float e1 = ex2(fmaf(__uint_as_float(sv[2 * c + 1]), sl, -mref));
-          ls[c & 3] += e0 + e1;
-          pw[c] = pack_bf16x2(e0, e1);
-        }
-        st_cols<kTile / 2>(s_col, pw);
-        l = l * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
         if (j > 0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tc::tmem_ld32(o_col + 32 * c, v);
-            tc::tmem_wait_ld();
+          for (int c = 0; c < D / 8; ++c) scale_cols8(o_col + 8 * c, alpha);  // (few registers: S is held)
+        }
+        const float mref = m_use == -INFINITY ? 0.f : m_use;
+        const uint64_t sl2 = pack2(sl, sl), mref2 = pack2(-mref, -mref);
+        uint64_t ls[2] = {0, 0};
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * alpha);
-            tc::tmem_st32(o_col + 32 * c, v);
+        for (int h = 0; h < kParts; ++h) {
+          uint32_t pw[kTile / 2 / kParts];
+#pragma unroll
+          for (int c = 0; c < kTile / 2 / kParts; ++c) {
+            const int cc = h * (kTile / 2 / kParts) + c;
+            const uint64_t x = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
+            const float e0 = ex2(lo2(x)), e1 = ex2(hi2(x));
+            ls[c & 1] = add2(ls[c & 1], pack2(e0, e1));
+            pw[c] = pack_bf16x2(e0, e1);
+          }
+          st_cols<kTile / 2 / kParts>(s_col + h * (kTile / 2 / kParts), pw);
+          tc::tmem_wait_st();
+          if (h + 1 < kParts) {
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[k * kParts + h]);
           }
         }
-        tc::tmem_wait_st();
+        const uint64_t lsum = add2(ls[0], ls[1]);
+        l = l * alpha + (lo2(lsum) + hi2(lsum));
+      } else if (kParts > 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[k * kParts]);
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[k]);
+      if (lane == 0) mbar_arrive(&p_full[k * kParts + kParts - 1]);
     }
     // ------------------------------------------------------------------ epilogue: this chunk's partial rows
     if (ok && warp_wait(mma_done, 0)) {
