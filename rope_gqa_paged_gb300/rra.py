@@ -541,19 +541,12 @@ def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs
         raise TypeError("u_accept and u_sample are float32")
     if u_accept.shape != ids or u_sample.shape != (B,):
         raise ValueError("u_accept: [B, gamma]; u_sample: [B]")
-    if tokens_out is None and n_accepted is None and positions_out is None:
-        # one allocation for all (each costs as much as the launch)
-        n = B * (gamma + 1)
-        buf = torch.empty((n + (2 * B if positions is not None else B),), dtype=_I32, device=target_probs.device)
-        tokens_out, n_accepted = buf.as_strided((B, gamma + 1), (gamma + 1, 1), 0), buf.as_strided((B,), (1,), n)
-        if positions is not None:
-            positions_out = buf.as_strided((B,), (1,), n + B)
     if tokens_out is None:
-        tokens_out = draft_tokens.new_empty((B, gamma + 1))
+        tokens_out = torch.empty((B, gamma + 1), dtype=_I32, device=target_probs.device)
     if n_accepted is None:
-        n_accepted = draft_tokens.new_empty((B,))
+        n_accepted = torch.empty((B,), dtype=_I32, device=target_probs.device)
     if positions is not None and positions_out is None:
-        positions_out = draft_tokens.new_empty((B,))
+        positions_out = torch.empty((B,), dtype=_I32, device=target_probs.device)
     row = (B,)
     st = lib().rra_accept_draft(
         target_probs.data_ptr(), pb, pt, q_ptr, qb, qt, _i32(draft_tokens, ids, "draft_tokens"),
