@@ -34,23 +34,24 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
   static constexpr int kTileBytes = kTok / 8 * kGroupBytes;  // K (or V) of a stage: 4 KB
-  static constexpr int kStages = 3;
+  static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kOffBar = kStages * 2 * kTileBytes;
   static constexpr int kSmemBytes = 1024 + kOffBar + kStages * 8;
   static constexpr int kIds = kOwnMaxBlocks / 32;          // block ids per lane
 };
 
-// 16 tokens for NT tiles of 8 rows. k / v: shared addresses of the slice's first group of K and V (v_gen:
-// V's generic address); tok0: its first token; lim[n][j]: the last token that row 8 n + 2 (lane % 4) + j
-// attends. CHECK: tokens from tok0 + valid on are none of the chunk's (their V rows are zeroed, so that
-// nothing stale reaches the tensor cores), and rows may not see all tokens.
+// The kTok tokens of a stage for NT tiles of 8 rows. k / v: shared addresses of K and V (v_gen: V's generic
+// address); tok0: the first token; lim[n][j]: the last token that row 8 n + 2 (lane % 4) + j attends.
+// CHECK: tokens from tok0 + valid on are none of the chunk's (their V rows are zeroed, so that nothing stale
+// reaches the tensor cores), and rows may not see all tokens.
 template <int D, int NT, bool CHECK>
 __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (&qb)[NT][D / 16][2], uint32_t k, uint32_t v,
                                      uint8_t* v_gen, int tok0, int valid, const int (&lim)[NT][2], int lane,
                                      float scale_log2) {
   using C = Cfg<D>;
-  if (CHECK && valid < 16) {
-    for (int i = lane; i < (16 - valid) * C::kHalves * 8; i += 32) {
+  constexpr int U = C::kTok / 16;
+  if (CHECK && valid < C::kTok) {
+    for (int i = lane; i < (C::kTok - valid) * C::kHalves * 8; i += 32) {
       const int r = valid + i / (C::kHalves * 8), h = (i / 8) % C::kHalves, c = i % 8;
       *reinterpret_cast<uint4*>(v_gen + (r >> 3) * C::kGroupBytes + h * 1024 + (r & 7) * 128 + 16 * c) =
           make_uint4(0u, 0u, 0u, 0u);
@@ -58,30 +59,38 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
     __syncwarp();
   }
   const int mat = lane >> 3, r8 = lane & 7;
-  float s[NT][2][4];  // two accumulators: half the chain of dependent products
+  float s[NT][U][2][4];  // two accumulators: half the chain of dependent products
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s[n][0][c] = s[n][1][c] = 0.f;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    uint32_t a[4];
-    ldsm_x4(k + (mat & 1) * C::kGroupBytes + (kk >> 2) * 1024 + swz(r8, ((kk & 3) << 1) + (mat >> 1)), a);
+      for (int c = 0; c < 4; ++c) s[n][u][0][c] = s[n][u][1][c] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma_bf16(s[n][kk & 1], a, qb[n][kk][0], qb[n][kk][1]);
-  }
-  uint32_t b0[NT], b1[NT];
-  const int ta = tok0 + (lane >> 2), tb = ta + 8;
+  for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t a[4];
+      ldsm_x4(k + (2 * u + (mat & 1)) * C::kGroupBytes + (kk >> 2) * 1024 + swz(r8, ((kk & 3) << 1) + (mat >> 1)), a);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16(s[n][u][kk & 1], a, qb[n][kk][0], qb[n][kk][1]);
+    }
+  uint32_t b[NT][U][2];
+  const int t_lane = lane >> 2;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float x[2][2], mnew[2];
+    float x[2][2 * U], mnew[2];
     bool grow = false;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float sa = s[n][0][j] + s[n][1][j], sb = s[n][0][2 + j] + s[n][1][2 + j];
-      x[j][0] = !CHECK || (ta <= lim[n][j] && (lane >> 2) < valid) ? sa * scale_log2 : -INFINITY;
-      x[j][1] = !CHECK || (tb <= lim[n][j] && (lane >> 2) + 8 < valid) ? sb * scale_log2 : -INFINITY;
-      float mx = fmaxf(x[j][0], x[j][1]);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < 2 * U; ++h) {  // token 8 h + lane / 4
+        const float sum = s[n][h >> 1][0][2 * (h & 1) + j] + s[n][h >> 1][1][2 * (h & 1) + j];
+        const int t = 8 * h + t_lane;
+        x[j][h] = !CHECK || (tok0 + t <= lim[n][j] && t < valid) ? sum * scale_log2 : -INFINITY;
+        mx = fmaxf(mx, x[j][h]);
+      }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -104,24 +113,28 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
         st[n].o[i][3] *= alpha[1];
       }
     }
-    float p[2][2];
+    float p[2][2 * U];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float mref = st[n].m[j] == -INFINITY ? 0.f : st[n].m[j];
-      p[j][0] = exp2f(x[j][0] - mref);
-      p[j][1] = exp2f(x[j][1] - mref);
-      st[n].l[j] += p[j][0] + p[j][1];
+#pragma unroll
+      for (int h = 0; h < 2 * U; ++h) {
+        p[j][h] = exp2f(x[j][h] - mref);
+        st[n].l[j] += p[j][h];
+      }
     }
-    b0[n] = movmatrix_trans(pack_bf16x2(p[0][0], p[1][0]));
-    b1[n] = movmatrix_trans(pack_bf16x2(p[0][1], p[1][1]));
+#pragma unroll
+    for (int h = 0; h < 2 * U; ++h) b[n][h >> 1][h & 1] = movmatrix_trans(pack_bf16x2(p[0][h], p[1][h]));
   }
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    uint32_t a[4];
-    ldsm_x4_trans(v + (mat >> 1) * C::kGroupBytes + (i >> 2) * 1024 + swz(r8, ((i & 3) << 1) + (mat & 1)), a);
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma_bf16(st[n].o[i], a, b0[n], b1[n]);
-  }
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t a[4];
+      ldsm_x4_trans(v + (2 * u + (mat >> 1)) * C::kGroupBytes + (i >> 2) * 1024 + swz(r8, ((i & 3) << 1) + (mat & 1)), a);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_bf16(st[n].o[i], a, b[n][u][0], b[n][u][1]);
+    }
 }
 
 template <int D, int NT>
@@ -265,15 +278,11 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     uint8_t* kst = smem + 2 * s * C::kTileBytes;
     uint8_t* vst = kst + C::kTileBytes;
     const int tok0 = start + it * kTok;
-#pragma unroll
-    for (int u = 0; u < kTok / 16; ++u) {
-      const int t0 = tok0 + 16 * u, valid = end - t0, off = 2 * u * C::kGroupBytes;
-      if (valid >= 16 && t0 + 15 <= p0)
-        step<D, NT, false>(st, qb, smem_addr(kst + off), smem_addr(vst + off), vst + off, t0, 16, lim, lane, a.scale_log2);
-      else if (valid > 0)
-        step<D, NT, true>(st, qb, smem_addr(kst + off), smem_addr(vst + off), vst + off, t0, min(valid, 16), lim, lane,
-                          a.scale_log2);
-    }
+    const int valid = min(end - tok0, kTok);
+    if (valid == kTok && tok0 + kTok - 1 <= p0)
+      step<D, NT, false>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, kTok, lim, lane, a.scale_log2);
+    else
+      step<D, NT, true>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, valid, lim, lane, a.scale_log2);
     __syncwarp();  // every lane has read the stage
     if (issued < n_stages) {
       issue(issued);

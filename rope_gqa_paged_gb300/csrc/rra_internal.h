@@ -204,7 +204,7 @@ constexpr int kSharedPrefixRows = 128;
 __host__ __device__ constexpr int shared_prefix_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
 __host__ __device__ constexpr int shared_prefix_nq(int64_t rows) { return rows > kSharedPrefixRows ? 2 : 1; }
 // tokens of an own-token stage, the most blocks of one own-token chunk
-__host__ __device__ constexpr int own_stage_tokens(int D) { return 2048 / D; }
+__host__ __device__ constexpr int own_stage_tokens(int) { return 32; }
 constexpr int kOwnMaxBlocks = 128;
 // The pools as {64 dims, 8 rows, D / 64 halves, groups of 8 rows, Hkv}: boxes of min(block size, prefix tile)
 // rows (prefix_splits > 0) and of min(block size, own stage) rows.
