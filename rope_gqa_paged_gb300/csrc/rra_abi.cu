@@ -296,22 +296,23 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   const int slices = (n_rep + 16 / gamma - 1) / (16 / gamma);
   p->hpc = (n_rep + slices - 1) / slices;
   const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), sms = std::max(1, sm_count());
-  // Splits of `tokens` own tokens per sequence. Chunks of 256 tokens while that makes at most two waves of
-  // the eight CTAs that fit an SM (ragged sequences fill the second one by halves; 48 sequences of up
-  // to 1500 tokens: 62 us with 256, 70 us with 512 and 768); longer ones that make one wave beyond
-  // (16 sequences of 6144 tokens x 8 heads: 69.6 us with 9 splits, 75 us with 19); shorter ones, down to
-  // 64, where not even half a wave would be there (a warp takes 0.3 us per 16 tokens: 4 sequences of 550
-  // tokens x 8 heads 13.0 us with 3 splits, 8.2 us with 9).
+  // Splits of `tokens` own tokens per sequence: chunks of 256 tokens, which suit ragged sequences (48 of up to
+  // 1500 tokens, 8 units each: 58.6 us with 6 splits, 68 us with 2), but from 6 splits on not more than make
+  // four units per SM (8 sequences of 6144 tokens, 8 units each: 44 us with 10 splits, 51 us with 24), nor
+  // more than that at all where 256 tokens would make over 16 units per SM (16 such sequences: 66.8 us with
+  // 5, 72.6 us with 9; 32: 121 us with 2, 138 us with 4). Chunks are shorter, down to 64 tokens, where not
+  // even four units per SM would be there (a warp takes 0.36 to 0.44 us per 16 tokens: 4 sequences of 550
+  // tokens, 8 units each, 13.0 us with 3 splits, 8.2 us with 9).
   auto own_plan = [&](int64_t tokens, int64_t* chunk_tokens) -> int64_t {
     const int tok = rra::own_stage_tokens(D);
-    const int64_t stages = std::max<int64_t>(1, (tokens + tok - 1) / tok), resident = 8 * sms;
-    int64_t chunk = 256 / tok;
-    if (num_splits > 0)
-      chunk = (stages + num_splits - 1) / num_splits;
-    else if (2 * units * ((stages + chunk - 1) / chunk) < resident)
-      chunk = std::min(chunk, std::max<int64_t>(64 / tok, 2 * stages * units / resident));
-    else if (units * ((stages + chunk - 1) / chunk) > 2 * resident)
-      chunk = std::max(chunk, (stages + std::max<int64_t>(1, resident / units) - 1) / std::max<int64_t>(1, resident / units));
+    const int64_t stages = std::max<int64_t>(1, (tokens + tok - 1) / tok), four = 4 * sms;
+    const int64_t fine = (stages * tok + 255) / 256, even = std::max<int64_t>(1, (four + units / 2) / units);
+    int64_t n = num_splits;
+    if (n == 0 && units * fine < four)
+      n = std::max(fine, std::min(stages * tok / 64, even));
+    else if (n == 0)
+      n = units * fine > 4 * four ? even : std::min(fine, std::max<int64_t>(even, 6));
+    int64_t chunk = (stages + n - 1) / n;
     // a chunk spans at most kOwnMaxBlocks blocks, wherever in a block it starts
     chunk = std::min(chunk, std::max<int64_t>(1, int64_t(rra::kOwnMaxBlocks - 1) * block_size / tok));
     const int64_t splits = (stages + chunk - 1) / chunk;
@@ -323,7 +324,8 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   if (prefix_len > 0 && rows > 0) {
     // What the two ways would take, in us. Rates measured on one GB300: own tokens 5.2 TB/s with up to 8
     // rows per unit and 3.8 with more, 7 where most come from L2; a prefix CTA 6 us and per key tile 0.8
-    // us (two CTAs per SM) or 1.75 us (two row tiles); partials 7 TB/s, written and read. Sequences are taken to fill half of the capacity.
+    // us (two CTAs per SM) or 1.75 us (two row tiles); partials 7 TB/s, written and
+    // read. Sequences are taken to fill half of the capacity.
     const double own_rate = 1e6 * (p->hpc * gamma > 8 ? 3.8 : 5.2), row_bytes = 8.0 * D * B * gamma * Hq;
     const double token_bytes = 4.0 * D * units;  // of one token of every sequence, as often as it is read
     const double own_bytes = token_bytes * (capacity - prefix_len) / 2;
@@ -342,9 +344,9 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
       const int64_t len = (tiles + s - 1) / s, n = (tiles + len - 1) / len;
       const int64_t waves = (ctas * n + resident - 1) / resident;
       const double pass_us = waves * (len * tile_us + 6.0);
-      // meanwhile own-token CTAs run on the SMs left over, and one beside each prefix CTA
+      // meanwhile own-token CTAs run on the SMs left over, and at 0.4 of the rate beside prefix CTAs
       const double left = std::max(0.0, 1.0 - double(ctas * n) / resident);
-      const double rest = std::max(0.0, own_bytes - own_rate * (left + 0.12 * (1 - left)) * pass_us);
+      const double rest = std::max(0.0, own_bytes - own_rate * (left + 0.4 * (1 - left)) * pass_us);
       const double us = pass_us + rest / own_rate + merge(n + own_splits);
       if (us < best || prefix_splits > 0) {
         best = us;
