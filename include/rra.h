@@ -413,7 +413,7 @@ RRA_API int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int
  *   target_probs  dt [B, gamma + 1, V], draft_probs dt [B, gamma, V]: V consecutive values per row, rows
  *                 `stride_t` and sequences `stride_b` elements apart (>= 0, any alignment of the element
  *                 type). Values in [0, 1] (others count as the nearer end, NaN as 0), rows that sum to
- *                 about 1 (below 8). draft_probs NULL: a drafter without probabilities, q_j(x_j) = 1.
+ *                 about 1 (from 8 on the sums overflow and any token may be drawn). draft_probs NULL: a drafter without probabilities, q_j(x_j) = 1.
  *   draft_tokens  int32 [B, gamma]; draft_lens int32 [B], 0..gamma tokens of sequence b (NULL: gamma;
  *                 outside: RRA_ERR_SEQ_LEN and clamped)
  *   u_accept, u_sample  float32 [B, gamma] and [B], uniform random numbers in [0, 1)

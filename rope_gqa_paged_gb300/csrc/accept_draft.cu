@@ -309,10 +309,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(cons
   const T* q = n < len && a.q != nullptr ? qrow + n * a.q_st : nullptr;
   // without the drafter's probabilities the rejected token alone is taken out of p
   int skip = n < len && a.q == nullptr && at >= 0 && at < V ? at : -1;
-  if (scribe) {
-    for (int j = lane; j <= gamma; j += 32) {
-      if (j != n) a.tokens_out[static_cast<size_t>(b) * (gamma + 1) + j] = j < n ? x : -1;
-    }
+  if (scribe) {  // (V - 1 until the draw replaces it, behind the cluster's barrier: always a token)
+    for (int j = lane; j <= gamma; j += 32)
+      a.tokens_out[static_cast<size_t>(b) * (gamma + 1) + j] = j < n ? x : j == n ? V - 1 : -1;
     if (lane == 0) {
       a.n_accepted[b] = n;
       if (a.positions_out != nullptr) a.positions_out[b] = a.positions[b] + n + 1;
@@ -361,10 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(cons
   int f0 = rank * kWarps * per_warp, step = per_warp, f1 = vecs;
   bool here = false;
   if (total <= 0) {
-    if (scribe && lane == 0) {
-      flag_error(a.err, RRA_ERR_PROBS);
-      *token_out = V - 1;
-    }
+    if (scribe && lane == 0) flag_error(a.err, RRA_ERR_PROBS);
   } else {
     for (int level = 0;; ++level) {
       const int64_t* sums = warp_sums[level & 1];

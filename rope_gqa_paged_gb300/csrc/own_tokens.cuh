@@ -3,17 +3,24 @@
 //
 // A unit is (sequence, KV head, slice of its query heads, chunk): up to 16 rows (hpc heads x gamma new
 // tokens) that read the same keys. One warp takes one unit, alone in its CTA: it issues its own TMA
-// copies into a ring of three 8 KB stages (16 tokens of K and V at head dim 128, 32 at 64; boxes of
-// 8-row groups as in shared_prefix.cuh) and consumes them, so there is no producer to wake, no
+// copies into a ring of stages of 32 tokens of K and V (two of 16 KB at head dim 128, three of 8 KB at 64;
+// boxes of 8-row groups as in shared_prefix.cuh) and consumes them, so there is no producer to wake, no
 // barrier between warps and no merge of warps at the end of a unit, which for units of a few
-// hundred tokens cost as much as the streaming itself (the decode and verify kernels, whose CTAs of
-// five warps share a unit: ## us against ## us for 512 sequences of 1 to 256 own tokens). Eight or
-// nine such CTAs an SM keep some 200 KB of copies in flight, which HBM, the bound, needs; the small CTAs
-// also fit beside a prefix CTA that is still at work.
+// hundred tokens cost as much as the streaming itself (512 sequences of 1 to 256 own tokens behind
+// 16384 shared ones: the whole call took 162 us with the decode kernel, whose CTAs of five warps share a
+// unit, and 151 us with one-warp CTAs of 16 tokens per stage). The small CTAs also fit beside a prefix
+// CTA that is still at work.
 //
-// Per 16 tokens (rows on N, tokens on M, as in decode_mma.cuh):
-//   S^T [16 tokens x 8 NT rows] = K Q^T, softmax online in base 2, O^T [D x 8 NT rows] += V^T P^T
-// P is rounded to bf16 (2^-8 of each weight); maxima, sums and O stay in float32.
+// Per stage (rows on N, tokens on M, as in decode_mma.cuh):
+//   S^T [32 tokens x 8 NT rows] = K Q^T, softmax online in base 2, O^T [D x 8 NT rows] += V^T P^T
+// P is rounded to bf16 (half a step, 2^-8 of each weight); maxima, sums and O stay in float32.
+//
+// Bound: HBM where units fill the SMs (1216 units of 1536 tokens, 8 KV heads of 128 dims: 7.0 TB/s with 8 rows,
+// 6.5 with 16); with one unit per SM the warp's chain of products, shuffles and exponentials (0.36
+// us per 16 tokens with 8 rows, 0.44 with 16; stages of 16 tokens took 0.66). K and V of 32 tokens arrive
+// together, so that the loads of V need not wait for the softmax: slots given back one by one took
+// 0.45 and 0.60 us (and 5 % less time on full SMs, where 24 KB per CTA let eight of them fit instead of
+// six); a ring of twice to four times the depth changed nothing.
 //
 // Every unit leaves (o, m, l) in slot prefix_splits + split of its rows, or writes the rows when there
 // is one slot. The kernel before this one (shared_prefix.cuh) may still be computing the prefix's
@@ -33,7 +40,7 @@ struct Cfg {
   static constexpr int kTok = own_stage_tokens(D);         // tokens per stage
   static constexpr int kHalves = D / 64;
   static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
-  static constexpr int kTileBytes = kTok / 8 * kGroupBytes;  // K (or V) of a stage: 4 KB
+  static constexpr int kTileBytes = kTok / 8 * kGroupBytes;  // K (or V) of a stage
   static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kOffBar = kStages * 2 * kTileBytes;
   static constexpr int kSmemBytes = 1024 + kOffBar + kStages * 8;

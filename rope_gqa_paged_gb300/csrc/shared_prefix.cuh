@@ -1,14 +1,12 @@
 // Attention of a whole batch over a prefix that all its sequences share, on the fifth-generation
-// tensor cores, and the merge of its partials with those of the sequences' own tokens: the parts of
-// rra_shared_prefix_attn that are not the decode and verify kernels.
+// tensor cores, and the merge of its partials with those of the sequences' own tokens (own_tokens.cuh).
 //
 // Softmax over the tokens [0, n) splits at the prefix length P by log-sum-exp: with m_i, l_i, o_i
 // the maximum, the sum and the unnormalised output over part i, out = sum 2^(m_i - M) o_i / sum
 // 2^(m_i - M) l_i. The part [0, P) has the same K and V for every sequence, so for one KV head it is
 // the attention of B x gamma x n_rep query rows over P keys: a pair of matrix products whose K and V
-// are read once for all the rows. The part [P, n) is decode_mma_kernel<SHARED> (one new token) or
-// decode_verify_kernel<SHARED> (more). Every part leaves (o, m, l) in a slot of the row; one warp per
-// row merges the slots (shared_merge_kernel).
+// are read once for all the rows. The part [P, n) is own_tokens_kernel's. Every part leaves
+// (o, m, l) in a slot of the row; one warp per row merges the slots (shared_merge_kernel).
 //
 // A prefix CTA takes one or two tiles of 128 of those rows (M of the MMAs) and a chunk of the prefix, in
 // key tiles. K and V tiles arrive by TMA through boxes of {64 dims, 8 rows, D / 64 halves, block rows /

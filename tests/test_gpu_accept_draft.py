@@ -295,3 +295,22 @@ def test_speculative_loop(R):
         np.testing.assert_array_equal(nxt.cpu().numpy(), pos.cpu().numpy() + want[1] + 1)
         total += int(want[1].sum())
     assert 0 < total < rounds * B * (gamma - 1)
+
+
+@pytest.mark.parametrize("V", [9, 1000, 1009, 16 * 4000 + 3, 128000])
+def test_rows_that_are_no_distribution(R, V):
+    """Rows that sum to 8 and more (scores passed for probabilities): some token of the vocabulary is written, and
+    nothing else changes."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    p = torch.randn(5, 4, V, generator=g, device=DEV).abs() * 3
+    p[0] = 1.0
+    q = torch.zeros(5, 3, V, device=DEV)
+    x = torch.randint(0, V, (5, 3), generator=g, device=DEV).int()
+    lens = torch.tensor([0, 1, 2, 3, 0], dtype=torch.int32, device=DEV)       # q = 0: every drafted token is kept
+    tokens = torch.full((5, 4), -77, dtype=torch.int32, device=DEV)
+    p.scatter_(2, torch.cat([x, x[:, :1]], 1)[:, :, None].long(), 0.5)
+    R.rra_accept_draft(p, x, torch.zeros(5, 3, device=DEV), torch.rand(5, generator=g, device=DEV), draft_probs=q,
+                       draft_lens=lens, tokens_out=tokens)
+    for b, n in enumerate(lens.tolist()):
+        row = tokens[b].tolist()
+        assert row[:n] == x[b, :n].tolist() and 0 <= row[n] < V and row[n + 1:] == [-1] * (3 - n)
