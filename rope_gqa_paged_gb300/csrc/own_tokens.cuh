@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     if (a.prefix_splits > 0 && blockIdx.x == 0 && split == 0 && b == 0) pdl_wait();
   };
 
-  pdl_launch_dependents();
   if (a.prefix_splits == 0) pdl_wait();
+  pdl_launch_dependents();
   const int start = a.first_token + split * a.chunk;
   const int first_blk = start >> a.log2_bs;
   int32_t ids[C::kIds];  // lane's block ids of the chunk, loaded before its length is known
