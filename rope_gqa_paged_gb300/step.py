@@ -234,7 +234,8 @@ class SharedPrefixStep(VerifyStep):
     sequences' own blocks from column prefix_len / block_size on (what stands before is not read).
     q / k_new / v_new are [B, gamma, H, D] and ``positions[b]`` is the first new token's position.
     ``seq_lens`` given to a call replaces positions + gamma as the attended lengths (two calls: append,
-    then attention); a length of 0 marks a padding row.
+    then attention); a length of 0 marks a padding row, whose output is zero. New tokens at positions
+    in the prefix are never written and set RRA_ERR_POSITION, those of padding rows too.
     """
 
     def __init__(self, batch: int, gamma: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -256,6 +257,10 @@ class SharedPrefixStep(VerifyStep):
         self.out = torch.empty(batch, gamma, n_q_heads, head_dim, dtype=self.dtype, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.graph = None
+
+    def rope_append(self, q, k_new, v_new, positions, stream=None) -> None:
+        # the append knows no prefix: positions in it become ones that it refuses, with all their gamma tokens
+        super().rope_append(q, k_new, v_new, torch.where(positions < self.prefix_len, -self.gamma, positions), stream)
 
     def attend(self, seq_lens, stream=None) -> torch.Tensor:
         """Attention of the already-appended gamma tokens over ``seq_lens`` tokens (they included)."""

@@ -363,3 +363,71 @@ def test_refusals(R):
         call(c.q, c.k.transpose(1, 2), c.v.transpose(1, 2), c.prefix, 512, c.table, c.lens, out)
     with pytest.raises(ValueError):
         call(c.q, c.k, c.v, c.prefix, 512, c.table, c.lens.cpu(), out)
+
+
+def test_two_call_step_with_padding(R):
+    """seq_lens given: a padding row (length 0) is zero, and its new tokens, at positions in the prefix that the
+    tables do list, leave the shared blocks as they were."""
+    P, gamma = 512, 3
+    c, k_new, v_new, pos = _step_case(31, gamma, 8, 2, 128, 16, P, [P + 40, P + 16, P + 300])
+    c.table[:, :P // 16] = c.prefix
+    step = R.SharedPrefixStep(c.B, gamma, 8, 2, 128, c.k, c.v, c.prefix, P, c.table, prefix_splits=2)
+    pos[1] = 0
+    lens = c.lens.clone()
+    lens[1] = 0
+    before = c.k[c.prefix.long()].clone(), c.v[c.prefix.long()].clone()
+    out = step(c.q, k_new, v_new, pos, lens)
+    assert step.error_bits() == R.RRA_ERR_POSITION
+    assert torch.equal(c.k[c.prefix.long()], before[0]) and torch.equal(c.v[c.prefix.long()], before[1])
+    assert not out[1].any()
+    c.lens_list[1], step.q_rot[1] = 0, 0
+    check(out, *c.expect(step.q_rot))
+
+
+def test_far_blocks(R):
+    """Block ids whose bytes lie beyond 2^32, in a pool of 6.4 GB; one block twice in the prefix."""
+    n, bs, Hkv, D, P = 49152, 64, 8, 128, 256
+    c = Case([P + 100, P + 1, P + 70], 2, 32, Hkv, D, bs, P, seed=32, poison=False)
+    small_k, small_v, ids = c.k, c.v, torch.arange(c.k.shape[0], device=DEV)
+    c.k = torch.zeros(n, bs, Hkv, D, device=DEV, dtype=torch.bfloat16)
+    c.v = torch.zeros(n, bs, Hkv, D, device=DEV, dtype=torch.bfloat16)
+    far = n - 1 - ids * 11                     # (block 32768 of 64 x 8 x 128 values starts at byte 2^32)
+    assert int(far.min()) > 32768
+    c.k[far], c.v[far] = small_k, small_v
+    c.prefix = far[c.prefix.long()].int()
+    c.prefix[2] = c.prefix[0]
+    c.table = torch.where(c.table >= 0, far[c.table.clamp(min=0).long()].int(), c.table)
+    for splits, pre in ((1, 1), (3, 2), (0, 0)):
+        out, err = c.run(R, splits, pre)
+        assert int(err) == 0
+        check(out, *c.expect(), what=f"{splits} {pre}")
+
+
+@pytest.mark.parametrize("gamma,Hq,Hkv,D,bs,P,lens", [
+    (16, 13, 1, 64, 1024, 1024, [1040, 1039, 0]),       # thirteen heads a group, one head per unit; one block ahead
+    (1, 17, 1, 128, 2048, 4096, [4097, 6144]),          # blocks longer than a chunk
+    (7, 22, 2, 128, 8, 8, [8, 15, 16, 40]),             # a prefix of one block of 8
+    (1, 8, 8, 64, 16, 800, [800, 800]),                 # nothing but the prefix, as long as the tables
+])
+def test_odd_groups_and_blocks(R, gamma, Hq, Hkv, D, bs, P, lens):
+    c = Case(lens, gamma, Hq, Hkv, D, bs, P, seed=33)
+    for splits, pre in ((0, 0), (1, 1), (5, 3)):
+        out, err = c.run(R, splits, pre)
+        assert int(err) == 0
+        check(out, *c.expect(), what=f"{splits} {pre}")
+
+
+def test_calls_in_turn_on_one_workspace(R):
+    """Calls of other shapes one after the other on a stream, without a wait between them, on one workspace that
+    no one has filled."""
+    cases = [Case([700, 0, 540], 1, 32, 8, 128, 16, 512, seed=34), Case([900] * 40, 4, 16, 2, 128, 32, 640, seed=35),
+             Case([300, 260], 2, 14, 2, 64, 8, 256, seed=36)]
+    plans = [(3, 2), (2, 5), (4, 0)]
+    ws = torch.full((max(c.plan(R, *p)[2] for c, p in zip(cases, plans)),), 0xFF, dtype=torch.uint8, device=DEV)
+    outs = [[torch.full_like(c.q, NAN) for _ in range(4)] for c in cases]
+    for i in range(4):
+        for c, p, o in zip(cases, plans, outs):
+            c.run(R, *p, ws=ws, out=o[i])
+    for c, o in zip(cases, outs):
+        check(o[0], *c.expect())
+        assert all(torch.equal(o[0], x) for x in o[1:])
