@@ -51,11 +51,11 @@ namespace spx {
 
 constexpr int kRows = kSharedPrefixRows;        // rows of a tile: M of every MMA
 constexpr float kRescaleLog2 = 8.f;             // move the running max only when it grows by more
-constexpr int kParts = 2;                        // of a P tile, each handed to the MMAs as soon as it is there
 
 template <int D, int NQ>
 struct Cfg {
   static constexpr int kTile = shared_prefix_tile(D, NQ);  // keys per tile
+  static constexpr int kParts = kTile == 128 ? 4 : 2;      // of a P tile, each handed to the MMAs as soon as it is there
   static constexpr int kHalves = D / 64;
   static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
   static constexpr int kTileBytes = kTile / 8 * kGroupBytes;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
   using C = Cfg<D, NQ>;
-  constexpr int kTile = C::kTile, kRing = C::kRing;
+  constexpr int kTile = C::kTile, kRing = C::kRing, kParts = C::kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
         l = l * alpha + (lo2(lsum) + hi2(lsum));
       } else if (kParts > 1) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[k * kParts]);
+        if (lane == 0)
+          for (int h = 0; h + 1 < kParts; ++h) mbar_arrive(&p_full[k * kParts + h]);
       }
       tc::fence_before_sync();
       __syncwarp();
