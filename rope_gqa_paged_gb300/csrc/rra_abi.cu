@@ -296,11 +296,12 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   const int slices = (n_rep + 16 / gamma - 1) / (16 / gamma);
   p->hpc = (n_rep + slices - 1) / slices;
   const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), sms = std::max(1, sm_count());
-  // Splits of `tokens` own tokens per sequence: chunks of 256 tokens, which suit ragged sequences (48 of up to
-  // 1500 tokens, 8 units each: 58.6 us with 6 splits, 68 us with 2), but from 6 splits on not more than make
-  // four units per SM (8 sequences of 6144 tokens, 8 units each: 44 us with 10 splits, 51 us with 24), nor
-  // more than that at all where 256 tokens would make over 16 units per SM (16 such sequences: 66.8 us with
-  // 5, 72.6 us with 9; 32: 121 us with 2, 138 us with 4). Chunks are shorter, down to 64 tokens, where not
+  // Splits of `tokens` own tokens per sequence. Up to 16 units per SM: chunks of 256 tokens, but from 4 splits on
+  // not more than make four units per SM (8 sequences of 6144 tokens, 8 units each: 44 us with 10 splits, 51 us
+  // with 24; 48 ragged ones of up to 1500, 8 units each: 58 us with 4, 68 us with 2; 16 of 651 to 1757, 16 each: 37 us
+  // with 4, 43 us with 6). Beyond: four units per SM (16 sequences of 6144 tokens, 8 units each: 66.8 us with 5,
+  // 72.6 us with 9), but no more than 1024 tokens in one (64 of 3000 tokens: 120 us with 3 splits, 132 us with 2; 16 of
+  // 64 to 6144 tokens, 32 each: 125 us with 6, 132 us with 4). Chunks are shorter, down to 64 tokens, where not
   // even four units per SM would be there (a warp takes 0.36 to 0.44 us per 16 tokens: 4 sequences of 550
   // tokens, 8 units each, 13.0 us with 3 splits, 8.2 us with 9).
   auto own_plan = [&](int64_t tokens, int64_t* chunk_tokens) -> int64_t {
@@ -311,7 +312,7 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     if (n == 0 && units * fine < four)
       n = std::max(fine, std::min(stages * tok / 64, even));
     else if (n == 0)
-      n = units * fine > 4 * four ? even : std::min(fine, std::max<int64_t>(even, 6));
+      n = units * fine > 4 * four ? std::max(even, (fine + 3) / 4) : std::min(fine, std::max<int64_t>(even, 4));
     int64_t chunk = (stages + n - 1) / n;
     // a chunk spans at most kOwnMaxBlocks blocks, wherever in a block it starts
     chunk = std::min(chunk, std::max<int64_t>(1, int64_t(rra::kOwnMaxBlocks - 1) * block_size / tok));

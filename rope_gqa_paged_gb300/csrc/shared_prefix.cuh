@@ -501,20 +501,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
   }
 }
 
-// One warp per output row: the prefix_splits partials of the prefix and those of the sequence's own
-// chunks that hold tokens. Rows of a sequence whose position is refused are not written.
+// Output rows from the prefix_splits partials of the prefix and those of the sequence's own chunks that hold
+// tokens; WARPS warps per row, each with every WARPS-th four partials. Rows of a sequence whose position is
+// refused are not written.
 // Bound: latency (length, then partials and maxima together, then the sums); partials come from L2, four at a
 // time and the next four ahead. (One by one behind the maxima: 16 sequences of 8192 tokens with one KV head 23.3
 // us instead of 20.3. Eight at a time: 19.5 us there, but 136 us instead of 133 for the 16384 rows of three partials
 // of 512 sequences.)
 constexpr int kMergeWarps = 4;
 
-template <int D>
+template <int D, int WARPS>
 __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const DecodeArgs a) {
   constexpr int E = D / 32;  // dims per lane
   constexpr int kBatch = 4;  // partials loaded at a time, the first before the maxima are known
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  __shared__ float part[WARPS > 1 ? WARPS - 1 : 1][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = WARPS > 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kMergeWarps + warp;
+  const int w0 = WARPS > 1 ? warp : 0;
   if (row >= static_cast<int64_t>(a.B) * a.gamma * a.Hq) return;
   const int b = static_cast<int>(row / (static_cast<int64_t>(a.gamma) * a.Hq));
   // (the lengths are older than the kernels that wrote the partials, which let this one start)
@@ -546,9 +549,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   pdl_wait();  // by every warp: what follows this kernel relies on the two before it being complete
   pdl_launch_dependents();
   if (refused) return;
-  load(0);
-  float M = -INFINITY, l = 0.f;  // over the partials taken so far
-  float acc[E] = {};
+  load(kBatch * w0);
+  float M = -INFINITY, l = 0.f;  // over the partials of all warps so far
+  float acc[E] = {};             // over this warp's
   for (int s0 = 0; s0 < n; s0 += 32) {
     const float2 x = s0 + lane < n ? __ldcg(ml + s0 + lane) : make_float2(-INFINITY, 0.f);
     float m = x.x;
@@ -564,13 +567,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
     M = m;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= keep;
-    for (int s = s0; s < min(n, s0 + 32); s += kBatch) {
+    for (int s = s0 + kBatch * w0; s < min(n, s0 + 32); s += kBatch * WARPS) {
       float v[kBatch][E];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) v[k][e] = next[k][e];
-      if (s + kBatch < n) load(s + kBatch);
+      load(s + kBatch * WARPS);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const float ws = __shfl_sync(0xffffffffu, w, s - s0 + k);  // (0 from n on)
@@ -578,6 +581,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
         for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, v[k][e], acc[e]);
       }
     }
+  }
+  if constexpr (WARPS > 1) {  // (always added up in the same order)
+    if (warp > 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[warp - 1][lane * E + e] = acc[e];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int i = 0; i < WARPS - 1; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += part[i][lane * E + e];
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * D + lane * E);
@@ -601,8 +616,12 @@ cudaError_t launch_prefix(const DecodeArgs& a, const CUtensorMap& km, const CUte
 template <int D>
 cudaError_t launch_merge(const DecodeArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.gamma * a.Hq;
+  // Four warps per row where one would go through more than two batches and the SMs hold all of the warps (384
+  // rows of 72 partials: 15.6 us the call, 21.3 with one warp; 16384 rows of 9: 178 us, 166 with one).
+  if (a.num_splits > 8 && rows * kMergeWarps <= int64_t(64) * current_sm_count())
+    return launch_pdl(shared_merge_kernel<D, kMergeWarps>, dim3(static_cast<unsigned>(rows)), dim3(32 * kMergeWarps), 0, st, a);
   const dim3 grid(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
-  return launch_pdl(shared_merge_kernel<D>, grid, dim3(32 * kMergeWarps), 0, st, a);
+  return launch_pdl(shared_merge_kernel<D, 1>, grid, dim3(32 * kMergeWarps), 0, st, a);
 }
 
 }  // namespace spx
