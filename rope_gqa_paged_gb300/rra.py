@@ -541,20 +541,28 @@ def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs
         raise TypeError("u_accept and u_sample are float32")
     if u_accept.shape != ids or u_sample.shape != (B,):
         raise ValueError("u_accept: [B, gamma]; u_sample: [B]")
-    if tokens_out is None:
-        tokens_out = torch.empty((B, gamma + 1), dtype=_I32, device=target_probs.device)
+    row, device = (B,), target_probs.device
+    if tokens_out is None:  # (made here, so not checked below: the call takes longer on the host than on the GPU)
+        tokens_out = torch.empty((B, gamma + 1), dtype=_I32, device=device)
+        tokens_ptr = tokens_out.data_ptr()
+    else:
+        tokens_ptr = _i32(tokens_out, (B, gamma + 1), "tokens_out")
     if n_accepted is None:
-        n_accepted = torch.empty((B,), dtype=_I32, device=target_probs.device)
-    if positions is not None and positions_out is None:
-        positions_out = torch.empty((B,), dtype=_I32, device=target_probs.device)
-    row = (B,)
+        n_accepted = torch.empty(row, dtype=_I32, device=device)
+        kept_ptr = n_accepted.data_ptr()
+    else:
+        kept_ptr = _i32(n_accepted, row, "n_accepted")
+    next_ptr = None
+    if positions_out is not None:
+        next_ptr = _i32(positions_out, row, "positions_out")
+    elif positions is not None:
+        positions_out = torch.empty(row, dtype=_I32, device=device)
+        next_ptr = positions_out.data_ptr()
     st = lib().rra_accept_draft(
         target_probs.data_ptr(), pb, pt, q_ptr, qb, qt, _i32(draft_tokens, ids, "draft_tokens"),
         _i32(draft_lens, row, "draft_lens") if draft_lens is not None else None, _ptr(u_accept), _ptr(u_sample),
-        _i32(positions, row, "positions") if positions is not None else None,
-        _i32(tokens_out, (B, gamma + 1), "tokens_out"), _i32(n_accepted, row, "n_accepted"),
-        _i32(positions_out, row, "positions_out") if positions_out is not None else None, B, gamma, V, code,
-        _ptr(err_flag), _stream(stream, target_probs))
+        _i32(positions, row, "positions") if positions is not None else None, tokens_ptr, kept_ptr, next_ptr, B, gamma,
+        V, code, _ptr(err_flag), _stream(stream, target_probs))
     if st != 0:
         raise RraError("rra_accept_draft", st)
     return (tokens_out, n_accepted) if positions_out is None else (tokens_out, n_accepted, positions_out)
