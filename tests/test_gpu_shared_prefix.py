@@ -431,3 +431,20 @@ def test_calls_in_turn_on_one_workspace(R):
     for c, o in zip(cases, outs):
         check(o[0], *c.expect())
         assert all(torch.equal(o[0], x) for x in o[1:])
+
+
+def test_two_streams_at_once(R):
+    """Calls that overlap on two streams, each with its own workspace."""
+    a, b = Case([700, 540] * 8, 1, 32, 8, 128, 16, 512, seed=41), Case([2000, 1300, 0] * 5, 4, 16, 4, 128, 32, 1024, seed=42)
+    plans = [(2, 2), (3, 3)]
+    ws = [torch.zeros(c.plan(R, *p)[2], dtype=torch.uint8, device=DEV) for c, p in zip((a, b), plans)]
+    outs = [torch.full_like(c.q, NAN) for c in (a, b)]
+    streams, err = [torch.cuda.Stream(), torch.cuda.Stream()], torch.zeros(1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, p, w, o, s in zip((a, b), plans, ws, outs, streams):
+            c.run(R, *p, ws=w, err=err, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for c, o in zip((a, b), outs):
+        check(o, *c.expect())
