@@ -369,8 +369,10 @@ RRA_API int rra_prefill_step(const void* q, const void* k_new, const void* v_new
  *   workspace       of rra_shared_prefix_plan's bytes (may be NULL when that is 0). It needs no filling and
  *                   keeps nothing between calls: calls of any shapes may take turns on one; calls
  *                   sharing it must not overlap on the GPU.
- * Other arguments, error bits and statuses as in rra_verify_attn; RRA_EUNSUPPORTED where prefix_len
- * is not a multiple of block_size.
+ * Slots past L_b are never used, whatever they hold. A token that some rows attend and others of its
+ * batch or sequence do not (a later new token, a prefix token past a shorter L_b) weighs 0 for those,
+ * so its V has to be finite. Other arguments, error bits and statuses as in rra_verify_attn;
+ * RRA_EUNSUPPORTED where prefix_len is not a multiple of block_size.
  */
 RRA_API int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_pool,
                                    const int32_t* prefix_blocks, int prefix_len, const int32_t* block_table,

@@ -1377,8 +1377,13 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   if (st == RRA_OK && p.prefix_splits > 0) {
     const int nq = rra::shared_prefix_nq(int64_t(B) * gamma * (Hq / Hkv));
     const int group_rows = std::min(block_size, rra::shared_prefix_tile(D, nq));
-    st = encode_group_map(&maps.k_prefix, k_pool, num_blocks, block_size, Hkv, D, group_rows);
-    if (st == RRA_OK) st = encode_group_map(&maps.v_prefix, v_pool, num_blocks, block_size, Hkv, D, group_rows);
+    if (group_rows == own_rows) {  // (blocks of up to 32 tokens)
+      maps.k_prefix = maps.k_own;
+      maps.v_prefix = maps.v_own;
+    } else {
+      st = encode_group_map(&maps.k_prefix, k_pool, num_blocks, block_size, Hkv, D, group_rows);
+      if (st == RRA_OK) st = encode_group_map(&maps.v_prefix, v_pool, num_blocks, block_size, Hkv, D, group_rows);
+    }
   }
   if (st != RRA_OK) return st;
   rra::DecodeArgs a{};
