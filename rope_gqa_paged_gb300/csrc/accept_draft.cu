@@ -21,9 +21,11 @@
 // Bound: HBM (one row of p, and one of q where a token was rejected) for large batches, latency for
 // small ones. One cluster of CTAs takes a sequence: each CTA decides n for itself (two dependent
 // loads), sums its part of the vocabulary, and the CTAs exchange their sums through distributed
-// shared memory: one launch, no workspace, no atomics. The CTA whose part holds the border looks for
-// it again (in L1 or L2): its warps split the run that holds it until 256 values are left, which one
-// warp scans. (One warp scanning its whole run, 32 values a step: 64 rows of 128000 values in 33 us, 23 us so.)
+// shared memory: one launch, no workspace, no atomics. The CTA whose part holds the border looks for it again
+// in the run of the warp that holds it, one to four vectors per thread, then in one thread's values. (64 rows of
+// 128000 float32 values: 33 us with one warp going through the run 32 values a step, 19.3 with the run split
+// among the warps until 256 values are left and 8 of them per lane, 19.1 so; 256 rows of 100003 bf16 values 29.8
+// and 28.5. The sums without any search: 16.0 and 23.2.)
 // Rows of any alignment load in aligned 16-byte vectors of p; where q's rows lie at another offset its
 // two vectors are shifted together. Only vectors wholly inside the row are read so.
 #include <cuda_bf16.h>
@@ -42,7 +44,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;   // 64 registers
 constexpr int kMaxCluster = 16;
 constexpr int kMaxGamma = 32;   // one lane of a warp per drafted token
-constexpr int kScan = 8;        // values per lane of the last warp's scan
+constexpr int kScan = 4;        // most vectors per thread of the last search
 
 struct AcceptArgs {
   const void* p;                // [B, gamma + 1, V] with these strides (elements)
@@ -229,21 +231,64 @@ __device__ __forceinline__ int64_t sum_vectors(const T* p, const T* q, int head,
   return sum;
 }
 
-// One lane's part of the sum of p - min(p, q) over the vectors [n0, n1) of a row (vector n holds the
-// elements n E - head .. n E - head + E - 1, 16-byte aligned in p), in units of 2^-60; q may be
+// Vector n of a row holds its elements n E - head .. n E - head + E - 1, 16-byte aligned in p; those of
+// [lo, hi) lie wholly inside the row, in q as well, whose vectors have them from element `off` on.
+template <typename T>
+struct Layout {
+  int head, lo, hi;
+  uint32_t off;
+  __device__ __forceinline__ Layout(const T* p, const T* q, int V) {
+    constexpr int E = Elem<T>::kPerChunk;
+    head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    off = q == nullptr ? 0u
+                       : static_cast<uint32_t>(((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) /
+                                               sizeof(T));
+    // n E - head >= 0 (>= off) and n E - head + E (- off + 2 E) <= V
+    lo = (head + static_cast<int>(off) + E - 1) / E;
+    hi = max((V + head - (off != 0 ? E - static_cast<int>(off) : 0)) / E, 0);
+  }
+};
+
+// Sum of p - min(p, q) over vector n of a row; element `skip` counts as 0 (there is no q then).
+template <typename T>
+__device__ __forceinline__ int64_t vector_rest(const T* p, const T* q, int V, const Layout<T>& at, int n, int skip) {
+  constexpr int E = Elem<T>::kPerChunk;
+  const int v0 = n * E - at.head;
+  float x[E], y[E];
+  if (n >= at.lo && n < at.hi) {
+    unpack_probs<T, E>(*reinterpret_cast<const uint4*>(p + v0), x);
+    if (q != nullptr) {
+      const uint4* qv = reinterpret_cast<const uint4*>(q + v0 - static_cast<int>(at.off));
+      unpack_probs<T, E>(at.off != 0 ? shift_vectors<T>(qv[0], qv[1], at.off * sizeof(T)) : qv[0], y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const bool in = v0 + e >= 0 && v0 + e < V;
+      x[e] = in ? load_prob(p + v0 + e) : 0.f;
+      y[e] = in && q != nullptr ? load_prob(q + v0 + e) : 0.f;
+    }
+  }
+  UnitSum<kLevels<T>> sp, sm;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    if (v0 + e == skip) x[e] = 0.f;
+    if (v0 + e + 1 == skip) x[e + 1] = 0.f;
+    sp.add(x[e], x[e + 1]);
+    if (q != nullptr) sm.add(fminf(x[e], y[e]), fminf(x[e + 1], y[e + 1]));
+  }
+  return sp.value(E) - (q != nullptr ? sm.value(E) : 0);
+}
+
+// One lane's part of the sum of p - min(p, q) over the vectors [n0, n1) of a row, in units of 2^-60; q may be
 // nullptr (the sum of p). The vectors that reach over the row's ends go value by value.
 template <typename T>
 __device__ __forceinline__ int64_t sum_rest(const T* p, const T* q, int V, int n0, int n1, int lane) {
   constexpr int E = Elem<T>::kPerChunk;
-  const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-  // q's vectors: those of p lie `off` elements into them
-  const uint32_t off =
-      static_cast<uint32_t>(((reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) & 15) / sizeof(T));
-  const bool shifted = q != nullptr && off != 0;
-  // vectors with n E - head >= 0 (>= off) and n E - head + E (- off + 2 E) <= V
-  const int lo = (head + (shifted ? static_cast<int>(off) : 0) + E - 1) / E;
-  const int hi = max((V + head - (shifted ? E - static_cast<int>(off) : 0)) / E, 0);
-  const int i0 = min(max(n0, lo), n1), i1 = max(min(n1, hi), i0);
+  const Layout<T> at(p, q, V);
+  const int head = at.head, i0 = min(max(n0, at.lo), n1), i1 = max(min(n1, at.hi), i0);
+  const uint32_t off = at.off;
+  const bool shifted = off != 0;
   int64_t sum = 0;
   if (q == nullptr)
     sum = sum_vectors<T, Rows::kOne>(p, q, head, 0, i0, i1, lane);
@@ -263,11 +308,87 @@ __device__ __forceinline__ int64_t sum_rest(const T* p, const T* q, int V, int n
   return sum;
 }
 
+struct Shared {
+  int64_t warp_sums[2][kWarps], cta_sum[2], scan_sums[kWarps], hit_before;
+  int hit;
+};
+
+// This warp's sum over the vectors [n0, n1), to every lane.
+template <typename T>
+__device__ __forceinline__ int64_t run_sum(const T* p, const T* q, int V, int skip, int head, int n0, int n1, int lane) {
+  constexpr int E = Elem<T>::kPerChunk;
+  int64_t s = warp_sum(sum_rest<T>(p, q, V, n0, n1, lane));
+  if (skip >= 0 && skip >= n0 * E - head && skip < n1 * E - head) s -= units<T>(load_prob(p + skip));
+  return s;
+}
+
+// The lowest token whose inclusive sum exceeds `border`, by the CTA whose part holds it: its warps' runs of
+// `step` vectors start at f0 and end before f1, `before` is the sum of what precedes them. The run of the warp that
+// holds the border is split among the warps until a thread has at most kScan vectors; the threads' sums then
+// give the thread, and one warp looks through its values. (Its own function, so that the sums' loop keeps the
+// registers to itself.)
+template <typename T>
+__device__ __noinline__ void find_border(const T* p, const T* q, int V, int skip, int f0, int step, int f1, int64_t before,
+                                         int64_t border, int32_t* token_out, Shared& sh) {
+  constexpr int E = Elem<T>::kPerChunk;
+  static_assert(kScan * E <= 32, "a lane per value of a thread's vectors");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Layout<T> at(p, q, V);
+  for (int level = 0;; ++level) {
+    // (sums are never negative, so the first warp whose inclusive sum exceeds the border holds it)
+    const int64_t* sums = sh.warp_sums[level & 1];
+    int w = 0;
+    for (; w < kWarps - 1 && border >= before + sums[w]; ++w) before += sums[w];
+    f0 = min(f0 + w * step, f1);
+    f1 = min(f0 + step, f1);
+    if (f1 - f0 <= kScan * kThreads) break;
+    step = (f1 - f0 + kWarps - 1) / kWarps;
+    const int n0 = min(f0 + warp * step, f1);
+    const int64_t s = run_sum<T>(p, q, V, skip, at.head, n0, min(n0 + step, f1), lane);
+    if (lane == 0) sh.warp_sums[(level & 1) ^ 1][warp] = s;
+    __syncthreads();
+  }
+  const int c = (f1 - f0 + kThreads - 1) / kThreads;  // consecutive vectors per thread
+  const int m0 = f0 + static_cast<int>(threadIdx.x) * c, m1 = min(m0 + c, f1);
+  int64_t mine = 0;
+  for (int n = m0; n < m1; ++n) mine += vector_rest<T>(p, q, V, at, n, skip);
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sh.scan_sums[warp] = incl;
+  if (threadIdx.x == 0) sh.hit = -1;
+  __syncthreads();
+  int64_t excl = before + incl - mine;
+  for (int w = 0; w < warp; ++w) excl += sh.scan_sums[w];
+  if (excl <= border && border < excl + mine) {
+    sh.hit = m0;
+    sh.hit_before = excl;
+  }
+  __syncthreads();
+  if (warp == 0 && sh.hit >= 0) {
+    const int v = sh.hit * E - at.head + lane;
+    int64_t val = 0;
+    if (lane < c * E && v >= 0 && v < V && v != skip) {
+      const float pv = load_prob(p + v);
+      val = units<T>(pv) - (q != nullptr ? units<T>(fminf(pv, load_prob(q + v))) : 0);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, val, d);
+      if (lane >= d) val += y;
+    }
+    const uint32_t over = __ballot_sync(0xffffffffu, sh.hit_before + val > border);
+    if (over != 0 && lane == __ffs(over) - 1) *token_out = v;
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(const AcceptArgs a) {
   constexpr int E = Elem<T>::kPerChunk;
-  __shared__ int64_t warp_sums[2][kWarps];
-  __shared__ int64_t cta_sum[2];
+  __shared__ Shared sh;
   const int b = blockIdx.y, C = gridDim.x;
   const int rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -322,30 +443,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(cons
   const int head = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
   const int vecs = (V + head + E - 1) / E;
   const int per_warp = (vecs + C * kWarps - 1) / (C * kWarps);
-  // this warp's sum over the vectors [n0, n1), to every lane; `sums` gets it for the CTA
-  auto run_sum = [&](int n0, int n1, int64_t* sums) {
-    int64_t s = warp_sum(sum_rest<T>(p, q, V, n0, n1, lane));
-    if (skip >= 0 && skip >= n0 * E - head && skip < n1 * E - head) s -= units<T>(load_prob(p + skip));
-    if (lane == 0) sums[warp] = s;
-  };
-  int64_t total, before;
+  int64_t total, before, own;
   // a second time, over p itself, where nothing is left (p <= q everywhere, by rounding)
   for (int pass = 0;; ++pass) {
     const int n0 = min((rank * kWarps + warp) * per_warp, vecs);
-    run_sum(n0, min(n0 + per_warp, vecs), warp_sums[0]);
+    const int64_t run = run_sum<T>(p, q, V, skip, head, n0, min(n0 + per_warp, vecs), lane);
+    if (lane == 0) sh.warp_sums[0][warp] = run;
     __syncthreads();
     if (threadIdx.x == 0) {
       int64_t s = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += warp_sums[0][w];
-      cta_sum[pass] = s;
+      for (int w = 0; w < kWarps; ++w) s += sh.warp_sums[0][w];
+      sh.cta_sum[pass] = s;
     }
     __syncthreads();
     cluster_arrive();
     cluster_wait();
-    const int64_t c = lane < C ? ld_cluster(&cta_sum[pass], lane) : 0;
+    const int64_t c = lane < C ? ld_cluster(&sh.cta_sum[pass], lane) : 0;
     total = warp_sum(c);
     before = warp_sum(lane < rank ? c : 0);
+    own = __shfl_sync(0xffffffffu, c, rank);
     if (total > 0 || pass == 1) break;
     q = nullptr;
     skip = -1;
@@ -353,69 +470,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(cons
   cluster_arrive();  // this CTA has read the others' sums
 
   // ---- the border u * total, and the CTA whose part holds it
-  const float uc = fminf(fmaxf(u_last, 0.f), 1.f - 0x1p-24f);
-  const int64_t border = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(total), __float2ull_rz(uc * 0x1p64f)));
-  int32_t* token_out = a.tokens_out + static_cast<size_t>(b) * (gamma + 1) + n;
-  // (sums are never negative, so the first warp whose inclusive sum exceeds the border holds it)
-  int f0 = rank * kWarps * per_warp, step = per_warp, f1 = vecs;
-  bool here = false;
   if (total <= 0) {
     if (scribe && lane == 0) flag_error(a.err, RRA_ERR_PROBS);
   } else {
-    for (int level = 0;; ++level) {
-      const int64_t* sums = warp_sums[level & 1];
-      int w = 0;
-      bool found = false;
-      if (before <= border) {
-        for (; w < kWarps && !found; ++w) {
-          if (border < before + sums[w]) {
-            found = true;
-            break;
-          }
-          before += sums[w];
-        }
-      }
-      if (!found) break;  // (in another CTA)
-      f0 += w * step;
-      f1 = min(f0 + step, f1);
-      here = true;
-      if ((f1 - f0) * E <= 32 * kScan) break;
-      step = (f1 - f0 + kWarps - 1) / kWarps;
-      const int n0 = min(f0 + warp * step, f1);
-      run_sum(n0, min(n0 + step, f1), warp_sums[(level & 1) ^ 1]);
-      __syncthreads();
-    }
-    if (here && warp == 0) {  // at most 256 values: each lane takes kScan consecutive ones
-      const int v0 = max(f0 * E - head, 0) + lane * kScan, v1 = min(f1 * E - head, V);
-      int64_t val[kScan], c = 0;
-#pragma unroll
-      for (int k = 0; k < kScan; ++k) {
-        const int v = v0 + k;
-        const float pv = v < v1 ? load_prob(p + v) : 0.f;
-        const float qv = v < v1 && q != nullptr ? load_prob(q + v) : 0.f;
-        val[k] = v == skip ? 0 : units<T>(pv) - units<T>(fminf(pv, qv));
-        c += val[k];
-      }
-      const int64_t own = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
-        if (lane >= d) c += y;
-      }
-      const uint32_t over = __ballot_sync(0xffffffffu, before + c > border);
-      if (over != 0 && lane == __ffs(over) - 1) {
-        int64_t sum = before + c - own;
-        int at_k = kScan - 1;
-#pragma unroll
-        for (int k = kScan - 1; k >= 0; --k) {  // from the back: the lowest k that exceeds stays
-          int64_t incl = sum;
-#pragma unroll
-          for (int i = 0; i <= k; ++i) incl += val[i];
-          if (incl > border) at_k = k;
-        }
-        *token_out = v0 + at_k;
-      }
-    }
+    const float uc = fminf(fmaxf(u_last, 0.f), 1.f - 0x1p-24f);
+    const int64_t border = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(total), __float2ull_rz(uc * 0x1p64f)));
+    if (before <= border && border < before + own)
+      find_border<T>(p, q, V, skip, rank * kWarps * per_warp, per_warp, vecs, before, border,
+                     a.tokens_out + static_cast<size_t>(b) * (gamma + 1) + n, sh);
   }
   cluster_wait();  // no CTA's sums go away while another may still read them
 }
@@ -487,9 +549,10 @@ extern "C" int rra_accept_draft(const void* target_probs, int64_t target_stride_
   a.V = V;
   a.err = err_flag;
   // CTAs per sequence: 16 while they leave every CTA an SM of its own (one sequence of 32000 float32
-  // values: 5.0 us, 6.5 us with 8). Otherwise the most, up to 8, with which the whole grid is resident at
-  // once (64 x 128000 float32: 19.3 us with 8, 23.8 with 4, 27.8 with 16, whose clusters wait for 16 free
-  // places of one GPC; 256 x 100003 bf16: 29.6 us with 2, 37.2 with 8 in four turns).
+  // values: 5.6 us, 1.5 us more with 8). Otherwise the largest power of two, up to 8, with which the whole grid is
+  // resident at once (64 x 128000 float32: 19.1 us with 8, 4.5 more with 4, 8 more with 16, whose clusters wait
+  // for 16 free places of one GPC; 256 x 100003 bf16: 28.5 us with 2, 8 more with 8 in four turns; sizes between
+  // the powers gain nothing: 100 x 128000 float32 28.7 us with 4, 28.9 with 6).
   const int64_t sms = std::max(1, rra::current_sm_count());
   int clusters = int64_t(B) * rra::kMaxCluster <= sms ? rra::kMaxCluster : 8;
   while (clusters > 1 && int64_t(clusters) * B > rra::kCtasPerSm * sms) clusters /= 2;
