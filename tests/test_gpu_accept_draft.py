@@ -84,6 +84,14 @@ def test_sizes(R, B, gamma, V, drafter, dt):
         assert 0 < kept.mean() < gamma                       # the case has kept and rejected tokens
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("drafter", [True, False])
+@pytest.mark.parametrize("B,V", [(2, 2000003), (640, 40001), (1, 9000001)])
+def test_long_runs(R, B, V, drafter, dt):
+    """Parts of the vocabulary that one search of the CTA does not cover: few CTAs per sequence, or a huge one."""
+    same(R, *make(B, 1, V, dt, drafter, seed=V, sharp=1.0))
+
+
 @pytest.mark.parametrize("drafter", [True, False])
 def test_ragged_drafts(R, drafter):
     p, q, x, u, ul = make(50, 6, 700, torch.float32, drafter, seed=1)
