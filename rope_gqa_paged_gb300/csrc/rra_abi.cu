@@ -342,8 +342,9 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     const double tile_us = nq == 1 ? 0.8 : 1.45;
     const int64_t lo = prefix_splits > 0 ? std::min<int64_t>(prefix_splits, tiles) : 1;
     const int64_t hi = prefix_splits > 0 ? lo : std::min<int64_t>(tiles, std::max<int64_t>(1, 2 * resident / ctas));
-    for (int64_t s = lo; s <= hi; ++s) {
-      const int64_t len = (tiles + s - 1) / s, n = (tiles + len - 1) / len;
+    for (int64_t s = lo, len; s <= hi; s = len > 1 ? (tiles + len - 2) / (len - 1) : hi + 1) {  // each len once
+      len = (tiles + s - 1) / s;
+      const int64_t n = (tiles + len - 1) / len;
       const int64_t waves = (ctas * n + resident - 1) / resident;
       const double pass_us = waves * (len * tile_us + 6.0);
       // meanwhile own-token CTAs run on the SMs left over, and at 0.4 of the rate beside prefix CTAs
