@@ -22,14 +22,15 @@
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
 // so S may overwrite the P before it, and one commit per S says that everything before it is
 // complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back to
-// the producer. A row tile's chain is softmax, P.V, S, softmax, ...; the first half of P.V runs while
-// the second half of the softmax does. What this took, 512 rows x 8 heads x 16384 keys in two chunks
+// the producer. A row tile's chain is softmax, P.V, S, softmax, ...; the first parts of P.V run while
+// the last of the softmax do. What this took, 512 rows x 8 heads x 16384 keys in two chunks
 // (137 GFLOP, with the merge): 244 us with a lane chosen by its index, key tiles of 64 and three
 // commits a tile; 164 us with tiles of 128 and one commit; 151 us with an elected lane (elect_one);
 // 121 us with one ring of four slots and rows that leave by bulk copies; 109 us with P in two
-// halves and paired float32 instructions (1263 TFLOP/s). Slower: a second MMA warp; three ring slots,
-// with or without L2 prefetches; a part of the ex2 as polynomials on the FMA pipe (the softmax is
-// bound by its instructions, not by the special-function units).
+// halves and paired float32 instructions (1263 TFLOP/s); 2 % less with P in four parts (6 % more in
+// eight). Slower: a second MMA warp; three ring slots, with or without L2 prefetches; a part of the ex2 as
+// polynomials on the FMA pipe; two threads per row (1.57 us per key tile of two row tiles, 1.42 so); the first
+// part of P before the row's max is known.
 //
 // Two shapes of CTA:
 // * NQ = 1 (up to 128 rows per KV head): key tiles of 64 (128 at head dim 64), Q in Tensor Memory, 256 of
@@ -37,7 +38,7 @@
 //   CTAs' copies together keep up with HBM, which bounds this case (the prefix is read once).
 // * NQ = 2 (more rows): key tiles of 128, one CTA per SM, K and V serve 256 rows, Q in shared memory; one
 //   row tile's MMAs run while the other is in its softmax. Bound: that chain, some 1300 clocks per row
-//   tile and key tile, of which the MMAs are 1024.
+//   tile and key tile, of which the MMAs are 1024 (S takes Q and K from shared memory at its full rate).
 //
 // Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain); the MMA lane waits for
 // its last commit and the producer for its last copies before Tensor Memory is released.
