@@ -371,7 +371,9 @@ RRA_API int rra_prefill_step(const void* q, const void* k_new, const void* v_new
  *                   sharing it must not overlap on the GPU.
  * Slots past L_b are never used, whatever they hold. A token that some rows attend and others of its
  * batch or sequence do not (a later new token, a prefix token past a shorter L_b) weighs 0 for those,
- * so its V has to be finite. Other arguments, error bits and statuses as in rra_verify_attn;
+ * so its V has to be finite. Softmax weights enter the product with V as bf16 (half a step: 2^-8 of each), in
+ * sequences of up to 256 + gamma - 1 tokens as two bf16 parts (2^-16), as in the verify calls; maxima, sums and the
+ * partial outputs are float32. Other arguments, error bits and statuses as in rra_verify_attn;
  * RRA_EUNSUPPORTED where prefix_len is not a multiple of block_size.
  */
 RRA_API int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_pool,

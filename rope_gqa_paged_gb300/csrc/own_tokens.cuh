@@ -13,7 +13,9 @@
 //
 // Per stage (rows on N, tokens on M, as in decode_mma.cuh):
 //   S^T [32 tokens x 8 NT rows] = K Q^T, softmax online in base 2, O^T [D x 8 NT rows] += V^T P^T
-// P is rounded to bf16 (half a step, 2^-8 of each weight); maxima, sums and O stay in float32.
+// P is rounded to bf16 (half a step, 2^-8 of each weight); in sequences of about kShortRow tokens or fewer, where
+// such errors do not average out, P enters as that and the bf16 of its remainder (2^-16), as in the verify
+// kernel, and all their tokens are one unit's. Maxima, sums and O stay in float32.
 //
 // Bound: HBM where units fill the SMs (1216 units of 1536 tokens, 8 KV heads of 128 dims: 7.0 TB/s with 8 rows,
 // 6.5 with 16); with one unit per SM the warp's chain of products, shuffles and exponentials (0.36
@@ -28,6 +30,8 @@
 // start after it had waited for them), and its first CTA waits for that kernel, so that the merge
 // finds both complete.
 #pragma once
+
+#include <type_traits>
 
 #include "decode_mma.cuh"
 #include "shared_prefix.cuh"
@@ -50,8 +54,8 @@ struct Cfg {
 // The kTok tokens of a stage for NT tiles of 8 rows. k / v: shared addresses of K and V (v_gen: V's generic
 // address); tok0: the first token; lim[n][j]: the last token that row 8 n + 2 (lane % 4) + j attends.
 // CHECK: tokens from tok0 + valid on are none of the chunk's (their V rows are zeroed, so that nothing stale
-// reaches the tensor cores), and rows may not see all tokens.
-template <int D, int NT, bool CHECK>
+// reaches the tensor cores), and rows may not see all tokens. SPLIT_P: P as a bf16 part and its remainder's.
+template <int D, int NT, bool CHECK, bool SPLIT_P>
 __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (&qb)[NT][D / 16][2], uint32_t k, uint32_t v,
                                      uint8_t* v_gen, int tok0, int valid, const int (&lim)[NT][2], int lane,
                                      float scale_log2) {
@@ -82,7 +86,7 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma_bf16(s[n][u][kk & 1], a, qb[n][kk][0], qb[n][kk][1]);
     }
-  uint32_t b[NT][U][2];
+  uint32_t b[NT][U][2], b_lo[NT][U][2];
   const int t_lane = lane >> 2;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -131,7 +135,12 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2 * U; ++h) b[n][h >> 1][h & 1] = movmatrix_trans(pack_bf16x2(p[0][h], p[1][h]));
+    for (int h = 0; h < 2 * U; ++h) {
+      uint32_t hi, lo;
+      split_bf16x2(p[0][h], p[1][h], hi, lo);
+      b[n][h >> 1][h & 1] = movmatrix_trans(hi);
+      if constexpr (SPLIT_P) b_lo[n][h >> 1][h & 1] = movmatrix_trans(lo);
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -140,7 +149,10 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
       uint32_t a[4];
       ldsm_x4_trans(v + (2 * u + (mat >> 1)) * C::kGroupBytes + (i >> 2) * 1024 + swz(r8, ((i & 3) << 1) + (mat & 1)), a);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_bf16(st[n].o[i], a, b[n][u][0], b[n][u][1]);
+      for (int n = 0; n < NT; ++n) {
+        mma_bf16(st[n].o[i], a, b[n][u][0], b[n][u][1]);
+        if constexpr (SPLIT_P) mma_bf16(st[n].o[i], a, b_lo[n][u][0], b_lo[n][u][1]);
+      }
     }
 }
 
@@ -171,19 +183,20 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
 
   if (a.prefix_splits == 0) pdl_wait();
   pdl_launch_dependents();
-  const int start = a.first_token + split * a.chunk;
-  const int first_blk = start >> a.log2_bs;
+  int start = a.first_token + split * a.chunk, chunk = a.chunk;
+  int first_blk = start >> a.log2_bs;
   int32_t ids[C::kIds];  // lane's block ids of the chunk, loaded before its length is known
-  {
+  auto load_ids = [&]() {
     const int32_t* row = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
     const int prefix_blks = a.prefix_len >> a.log2_bs;
-    const int reach = min(((a.chunk - 1) >> a.log2_bs) + 2, a.max_blocks_per_seq - first_blk);
+    const int reach = min(((chunk - 1) >> a.log2_bs) + 2, a.max_blocks_per_seq - first_blk);
 #pragma unroll
     for (int k = 0; k < C::kIds; ++k) {
       const int i = lane + 32 * k, blk = first_blk + i;
       ids[k] = i < reach ? __ldcg((blk < prefix_blks ? a.prefix_blocks : row) + blk) : 0;
     }
-  }
+  };
+  load_ids();
   int p0, L;  // row (j, head) attends [0, p0 + j]
   if (a.positions != nullptr) {
     p0 = __ldcg(a.positions + b);
@@ -201,6 +214,15 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     }
     p0 = L - gamma;
   }
+  const bool short_seq = spx::short_sequence(a, L);
+  if (short_seq && a.prefix_splits > 0) {  // all its tokens are the first unit's
+    chunk = spx::kShortTokens;
+    start = split * chunk;
+    if (start < L) {
+      first_blk = 0;
+      load_ids();
+    }
+  }
   if (start >= L) {
     if (a.num_splits == 1)  // no merge: the empty sequence's rows are zero
       for (int i = lane; i < rows * D; i += 32)
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     leave();
     return;
   }
-  const int end = min(L, start + a.chunk);
+  const int end = min(L, start + chunk);
   const int n_stages = (end - start + kTok - 1) / kTok;
   {
     const int n_blk = ((end - 1) >> a.log2_bs) - first_blk + 1;
@@ -276,25 +298,32 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
   }
 
   bool ok = true;
-  for (int it = 0; it < n_stages; ++it) {
+  auto consume = [&](int it, auto split_p) {
     const int s = it % C::kStages;
     if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (it / C::kStages) & 1))) {
       ok = false;
-      break;
+      return;
     }
     uint8_t* kst = smem + 2 * s * C::kTileBytes;
     uint8_t* vst = kst + C::kTileBytes;
     const int tok0 = start + it * kTok;
     const int valid = min(end - tok0, kTok);
-    if (valid == kTok && tok0 + kTok - 1 <= p0)
-      step<D, NT, false>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, kTok, lim, lane, a.scale_log2);
+    if (!split_p.value && valid == kTok && tok0 + kTok - 1 <= p0)
+      step<D, NT, false, split_p.value>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, kTok, lim, lane, a.scale_log2);
     else
-      step<D, NT, true>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, valid, lim, lane, a.scale_log2);
+      step<D, NT, true, split_p.value>(st, qb, smem_addr(kst), smem_addr(vst), vst, tok0, valid, lim, lane, a.scale_log2);
     __syncwarp();  // every lane has read the stage
     if (issued < n_stages) {
       issue(issued);
       ++issued;
     }
+  };
+  if (short_seq) {
+#pragma unroll 1
+    for (int it = 0; ok && it < n_stages; ++it) consume(it, std::true_type());
+  } else {
+#pragma unroll 1
+    for (int it = 0; ok && it < n_stages; ++it) consume(it, std::false_type());
   }
   if (!ok) {  // no copy may still be landing when the CTA exits
     if (lane == 0) {

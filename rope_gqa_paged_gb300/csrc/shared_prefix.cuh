@@ -16,8 +16,9 @@
 //   softmax           warpgroup k, one row per thread: the S row into registers, running max (moved only
 //                     when it grows by more than 2^8), P as bf16 pairs over the S columns
 //   O_k += P V_j      kTile / 16 MMAs (M 128, N D, K 16), P the A operand from Tensor Memory, V MN-major
-// P is rounded to bf16 (half a step, 2^-8 of each weight, below what the bf16 output keeps); maxima,
-// sums and O stay in float32.
+// P is rounded to bf16 (half a step, 2^-8 of each weight); maxima, sums and O stay in float32. Sequences of so few
+// tokens that such errors do not average out are own_tokens_kernel's alone, which holds their P to 2^-16 (as a branch
+// here, a second P.V with the remainders of P, took 140 us instead of 137 for 512 sequences behind 16384 tokens).
 //
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
 // so S may overwrite the P before it, and one commit per S says that everything before it is
@@ -173,6 +174,13 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&s)[N]) 
     }
   }
 }
+
+// Sequences whose first new token attends at most this many tokens (L the attended length) hold P to 2^-16, as
+// the verify kernel's do. Where the prefix has a pass of its own, one unit of the own-token kernel reads all
+// their tokens, at most kShortTokens - 1.
+constexpr int kShortRow = 256;
+constexpr int kShortTokens = kShortRow + 16;
+__device__ __forceinline__ bool short_sequence(const DecodeArgs& a, int L) { return L - a.gamma < kShortRow; }
 
 // L_b of sequence b, cut to the cache; the caller flags what is out of range.
 __device__ __forceinline__ int attended_length(const DecodeArgs& a, int b) {
@@ -344,7 +352,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     int lim = a.prefix_len;
     if (real) {
       const int b = bt / a.gamma, j_new = bt - b * a.gamma;
-      lim = min(max(attended_length(a, b) - a.gamma + 1 + j_new, 0), a.prefix_len);
+      const int L = attended_length(a, b);
+      lim = short_sequence(a, L) ? 0 : min(L - a.gamma + 1 + j_new, a.prefix_len);
     }
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + lane_base + C::kColO + D * k;
@@ -525,7 +534,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   const int L = attended_length(a, b);
   const int p0 = a.positions != nullptr ? __ldcg(a.positions + b) : a.prefix_len;
   const bool refused = a.positions != nullptr && (p0 < a.prefix_len || p0 + a.gamma > a.capacity);
-  const int n = a.prefix_splits + (max(L - a.first_token, 0) + a.chunk - 1) / a.chunk;
+  const int n = a.prefix_splits + (a.prefix_splits > 0 && short_sequence(a, L)
+                                       ? min(L, 1)
+                                       : (max(L - a.first_token, 0) + a.chunk - 1) / a.chunk);
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
   const float* o = a.ws_o + row * a.num_splits * D + lane * E;
   float next[kBatch][E];

@@ -88,13 +88,6 @@ struct VerifyState {
   float m[2], l[2];   // rows lane/4 and lane/4 + 8 (running max in log2 units, lane-partial sum)
 };
 
-// (lo, hi) rounded to bf16 pairs: `hi` holds the nearest bf16 values, `lo` the bf16 rounding of
-// what they leave out.
-__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(a, b);
-  lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
-}
-
 // One 16-token slice of a stage for one warp. t0: the slice's first row in the stage; tok0: its
 // token index; lim0 / lim1: the last token rows lane/4 and lane/4 + 8 may attend (-1: padding).
 // CHECK: rows at or past `valid` of the stage are not tokens of this chunk; their V rows are
