@@ -383,8 +383,18 @@ RRA_API int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const 
                                    int prefix_splits, void* workspace, size_t ws_bytes, int32_t* err_flag,
                                    void* stream);
 
+/* RoPE and append of the gamma new tokens at positions[b] .. positions[b] + gamma - 1 behind a shared prefix:
+ * rra_rope_append_verify on a bf16 pool, but for tokens at positions below prefix_len, which are not written and set
+ * RRA_ERR_POSITION as positions past the cache do. Arguments and statuses as in rra_shared_prefix_attn; q_out may
+ * be q. */
+RRA_API int rra_shared_prefix_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                                     void* q_out, void* k_pool, void* v_pool, int prefix_len,
+                                     const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks,
+                                     int B, int gamma, int Hq, int Hkv, int D, double rope_base, int rope_style,
+                                     int32_t* err_flag, void* stream);
+
 /* The whole step: RoPE and append of the gamma new tokens at positions[b] .. positions[b] + gamma - 1
- * (rra_rope_append_verify), then the attention with L_b = positions[b] + gamma. positions[b] must be at
+ * (rra_shared_prefix_append), then the attention with L_b = positions[b] + gamma. positions[b] must be at
  * least prefix_len: tokens below it would land in the shared blocks. They are not written, set
  * RRA_ERR_POSITION and leave that sequence's output unwritten, as positions past the cache do. q_out
  * receives q_rot and must not overlap q. */

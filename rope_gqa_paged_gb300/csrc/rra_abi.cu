@@ -1445,6 +1445,20 @@ int rra_shared_prefix_attn(const void* q_rot, const void* k_pool, const void* v_
                               prefix_splits, workspace, ws_bytes, err_flag, stream, false);
 }
 
+int rra_shared_prefix_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
+                             void* k_pool, void* v_pool, int prefix_len, const int32_t* block_table,
+                             int max_blocks_per_seq, int block_size, int num_blocks, int B, int gamma, int Hq, int Hkv,
+                             int D, double rope_base, int rope_style, int32_t* err_flag, void* stream) {
+  if (!pow2(block_size)) return block_size <= 0 ? RRA_EINVAL : RRA_EUNSUPPORTED;
+  if (gamma < 1 || max_blocks_per_seq < 1 || prefix_len < 0) return RRA_EINVAL;
+  if (prefix_len > int64_t(max_blocks_per_seq) * block_size) return RRA_EINVAL;
+  if (gamma > 16 || block_size < 8 || prefix_len % block_size != 0) return RRA_EUNSUPPORTED;
+  if (B > 0 && block_table == nullptr) return RRA_EINVAL;
+  return rope_append_launch(q, k_new, v_new, positions, q_out, k_pool, v_pool, block_table, max_blocks_per_seq,
+                            block_size, num_blocks, 0, B, gamma, Hq, Hkv, D, rope_base, rope_style, RRA_BF16, prefix_len,
+                            err_flag, stream);
+}
+
 int rra_shared_prefix_step(const void* q, const void* k_new, const void* v_new, const int32_t* positions, void* q_out,
                            void* k_pool, void* v_pool, const int32_t* prefix_blocks, int prefix_len,
                            const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks, void* out,

@@ -78,6 +78,8 @@ _SIGNATURES = {
     "rra_shared_prefix_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
                                         _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_f64, _c_int, _c_f32, _c_int,
                                         _c_int, _vp, _c_size, _vp, _vp]),
+    "rra_shared_prefix_append": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int,
+                                          _c_int, _c_int, _c_int, _c_int, _c_int, _c_f64, _c_int, _vp, _vp]),
     "rra_accept_draft": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "rra_shared_prefix_plan": (_c_int, [_c_int] * 10 + [_vp, _vp, _vp]),
@@ -480,6 +482,28 @@ def rra_shared_prefix_attn(q_rot, k_pool, v_pool, prefix_blocks, prefix_len: int
         raise RraError("rra_shared_prefix_attn", st)
 
 
+def _new_tokens(q, k_new, v_new, q_out, Hkv: int) -> None:
+    """Checks the new tokens' types and shapes beside queries that _shared_layout has looked at."""
+    if not k_new.dtype == v_new.dtype == q_out.dtype == _BF16:
+        raise TypeError("shared-prefix attention takes bf16 new tokens")
+    if k_new.numel() * q.shape[-2] != q.numel() * Hkv or v_new.shape != k_new.shape or q_out.shape != q.shape:
+        raise ValueError("k_new and v_new: [B, gamma, Hkv, D]; q_out: the shape of q")
+
+
+def rra_shared_prefix_append(q, k_new, v_new, positions, q_out, k_pool, v_pool, prefix_len: int, block_table,
+                             rope_base: float = 10000.0, rope_style: int = 0, err_flag=None, stream=None) -> None:
+    """RoPE on q and k_new (token j at positions[b] + j) and append of the gamma new tokens, but for those at
+    positions below prefix_len (a multiple of the block size), which are refused."""
+    B, gamma, Hq, D, num_blocks, block_size, Hkv, cols = _shared_layout(q, k_pool, v_pool, None, 0, block_table,
+                                                                        positions, q_out)
+    _new_tokens(q, k_new, v_new, q_out, Hkv)
+    st = lib().rra_shared_prefix_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q_out), _ptr(k_pool),
+                                        _ptr(v_pool), prefix_len, _ptr(block_table), cols, block_size, num_blocks, B,
+                                        gamma, Hq, Hkv, D, rope_base, rope_style, _ptr(err_flag), _stream(stream, q))
+    if st != 0:
+        raise RraError("rra_shared_prefix_append", st)
+
+
 def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, prefix_blocks, prefix_len: int,
                            block_table, out, rope_base: float = 10000.0, rope_style: int = 0, scale: float = 0.0,
                            num_splits: int = 0, prefix_splits: int = 0, workspace=None, err_flag=None,
@@ -487,10 +511,7 @@ def rra_shared_prefix_step(q, k_new, v_new, positions, q_out, k_pool, v_pool, pr
     """RoPE + append of the gamma new tokens at positions[b] (at least prefix_len), then their attention."""
     B, gamma, Hq, D, num_blocks, block_size, Hkv, cols = _shared_layout(q, k_pool, v_pool, prefix_blocks, prefix_len,
                                                                         block_table, positions, out)
-    if not k_new.dtype == v_new.dtype == q_out.dtype == _BF16:
-        raise TypeError("shared-prefix attention takes bf16 new tokens")
-    if k_new.numel() != B * gamma * Hkv * D or v_new.shape != k_new.shape or q_out.shape != q.shape:
-        raise ValueError("k_new and v_new: [B, gamma, Hkv, D]; q_out: the shape of q")
+    _new_tokens(q, k_new, v_new, q_out, Hkv)
     st = lib().rra_shared_prefix_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(q_out), _ptr(k_pool),
                                       _ptr(v_pool), _ptr(prefix_blocks), prefix_len, _ptr(block_table), cols,
                                       block_size, num_blocks, _ptr(out), B, gamma, Hq, Hkv, D, rope_base, rope_style,

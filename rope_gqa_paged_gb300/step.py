@@ -259,8 +259,8 @@ class SharedPrefixStep(VerifyStep):
         self.graph = None
 
     def rope_append(self, q, k_new, v_new, positions, stream=None) -> None:
-        # the append knows no prefix: positions in it become ones that it refuses, with all their gamma tokens
-        super().rope_append(q, k_new, v_new, torch.where(positions < self.prefix_len, -self.gamma, positions), stream)
+        rra.rra_shared_prefix_append(q, k_new, v_new, positions, self.q_rot, self.k_cache, self.v_cache, self.prefix_len,
+                                     self.block_table, self.rope_base, self.rope_style, self.err, stream)
 
     def attend(self, seq_lens, stream=None) -> torch.Tensor:
         """Attention of the already-appended gamma tokens over ``seq_lens`` tokens (they included)."""

@@ -176,3 +176,59 @@ def test_binding_refuses_drafts(rra, name, value, error):
     args[name] = value
     with pytest.raises(error):
         rra.rra_accept_draft(args["p"], args["x"], args["u"], args["ul"], draft_probs=args["draft_probs"])
+
+
+@host_only
+def test_append_refuses_before_any_launch(rra):
+    names = "q k_new v_new positions q_out k v prefix_len table cols bs blocks B gamma Hq Hkv D base style err stream".split()
+    call = _caller(rra.lib().rra_shared_prefix_append, names,
+                   [P, P, P, P, P, P, P, 512, P, 64, 16, 300, 4, 1, 32, 8, 128, 10000.0, 0, None, None])
+    assert call(B=0) == RRA_OK
+    for name in ("q", "k_new", "v_new", "positions", "q_out", "k", "v", "table"):
+        assert call(**{name: None}) == RRA_EINVAL, name
+    for name in ("q", "k_new", "v_new", "q_out", "k", "v"):
+        assert call(**{name: P + 8}) == RRA_EINVAL, name                       # misaligned
+    assert call(prefix_len=-16) == RRA_EINVAL and call(prefix_len=65 * 16) == RRA_EINVAL
+    assert call(prefix_len=500) == RRA_EUNSUPPORTED and call(bs=4, cols=256) == RRA_EUNSUPPORTED
+    assert call(bs=0) == RRA_EINVAL and call(bs=24) == RRA_EUNSUPPORTED
+    assert call(gamma=0) == RRA_EINVAL and call(gamma=17) == RRA_EUNSUPPORTED and call(D=96) == RRA_EUNSUPPORTED
+    assert call(cols=0, prefix_len=0) == RRA_EINVAL and call(blocks=0) == RRA_EINVAL
+    assert call(style=2) == RRA_EINVAL and call(base=0.5) == RRA_EINVAL
+
+
+@pytest.mark.parametrize("name,value,error", [
+    ("q", torch.zeros(2, 3, 8, 128), TypeError), ("k_new", torch.zeros(2, 3, 2, 128), TypeError),
+    ("k_new", torch.zeros(2, 3, 1, 128, dtype=BF), ValueError), ("v_new", torch.zeros(2, 3, 4, 128, dtype=BF), ValueError),
+    ("q_out", torch.zeros(2, 8, 128, dtype=BF), ValueError), ("positions", torch.zeros(2, dtype=torch.int64), TypeError),
+    ("positions", torch.zeros(3, dtype=I32), ValueError), ("q", torch.zeros(2, 3, 8, 128, dtype=BF), ValueError)])
+def test_binding_refuses_append(rra, name, value, error):                       # (the last: tensors of the CPU)
+    args = dict(q=torch.zeros(2, 3, 8, 128, dtype=BF), k_new=torch.zeros(2, 3, 2, 128, dtype=BF),
+                v_new=torch.zeros(2, 3, 2, 128, dtype=BF), positions=torch.zeros(2, dtype=I32),
+                q_out=torch.zeros(2, 3, 8, 128, dtype=BF), k=torch.zeros(40, 16, 2, 128, dtype=BF),
+                v=torch.zeros(40, 16, 2, 128, dtype=BF), prefix_len=64, table=torch.zeros(2, 8, dtype=I32))
+    args[name] = value
+    with pytest.raises(error):
+        rra.rra_shared_prefix_append(*args.values())
+
+
+def test_two_call_step_hands_on_the_callers_tensors(rra, monkeypatch):
+    """Nothing of the step runs outside the library: the calls get the very tensors and the stream that the caller
+    gave, not results of other kernels on whichever stream is torch's current one."""
+    from rope_gqa_paged_gb300 import step as step_module
+    calls = []
+    for name in [n for n in dir(rra) if n.startswith("rra_")]:
+        monkeypatch.setattr(rra, name, lambda *a, _name=name, **kw: calls.append((_name, list(a) + list(kw.values()))))
+    s = step_module.SharedPrefixStep.__new__(step_module.SharedPrefixStep)
+    own = {n: torch.zeros(1) for n in "q_rot k_cache v_cache block_table out workspace err prefix_blocks".split()}
+    s.__dict__.update(own, B=2, gamma=3, Hq=8, Hkv=2, D=128, prefix_len=64, num_splits=0, prefix_splits=0,
+                      rope_base=10000.0, rope_style=0, scale=0.0)
+    given = dict(q=torch.zeros(1), k_new=torch.zeros(1), v_new=torch.zeros(1), positions=torch.zeros(2, dtype=I32),
+                 seq_lens=torch.zeros(2, dtype=I32))
+    stream = object()
+    s(*given.values(), stream=stream)
+    known = {id(t) for t in list(own.values()) + list(given.values())}
+    assert len(calls) == 2
+    for name, args in calls:
+        assert any(a is stream for a in args), name
+        assert all(id(a) in known for a in args if isinstance(a, torch.Tensor)), name
+    assert any(a is given["positions"] for a in calls[0][1]) and any(a is given["seq_lens"] for a in calls[1][1])

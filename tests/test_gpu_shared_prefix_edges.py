@@ -1,4 +1,5 @@
-"""Shared-prefix attention at the edges of its range: rows of a few tokens.
+"""Shared-prefix attention at the edges of its range: rows of a few tokens, streams other than torch's current one, new
+tokens at the end of the prefix.
 
 Tolerance of rows that attend at most 256 tokens, per output element: the weights enter the second product as two bf16
 parts (2^-16 of each weight), the float32 scores (128 products of N(0,1) values: below 2^-13 of a weight), exponentials
@@ -72,3 +73,52 @@ def test_rows_do_not_depend_on_their_neighbours(R):
         assert torch.equal(out[b].view(torch.int16), short[b].view(torch.int16))
     a.lens_list = a.lens.tolist()
     check_short(a, short)
+
+
+def _step(R, c, seed, prefix_splits=2):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    new = [torch.randn(c.B, c.gamma, c.Hkv, c.D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+    step = R.SharedPrefixStep(c.B, c.gamma, c.Hq, c.Hkv, c.D, c.k, c.v, c.prefix, c.P, c.table,
+                              prefix_splits=prefix_splits)
+    return step, new, (c.lens - c.gamma).int()
+
+
+def test_two_call_step_on_another_stream(R):
+    """The two calls on a stream of the caller's, while torch's current stream is busy: positions that the caller's
+    stream produces at the last moment, output and caches as those of the step in one call."""
+    lens = [600, 517, 730, 560]
+    want, got = (Case(lens, 3, 8, 2, 128, 16, 512, seed=80, poison=False) for _ in range(2))
+    one, new, pos = _step(R, want, 81)
+    ref = one(want.q, *new, pos).clone()
+    two, new2, _ = _step(R, got, 81)
+    late, late_lens = torch.full_like(pos, 100), torch.full_like(got.lens, 515)  # (stale values: in the prefix)
+    got.table[:, :32] = got.prefix
+    before = got.k[got.prefix.long()].clone(), got.v[got.prefix.long()].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)                            # the current stream: busy for some 25 ms
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+        late.copy_(pos)
+        late_lens.copy_(got.lens)
+    out = two(got.q, *new2, late, late_lens, stream=side)
+    side.synchronize()
+    assert one.error_bits() == two.error_bits() == 0
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    assert torch.equal(two.q_rot, one.q_rot) and torch.equal(got.k, want.k) and torch.equal(got.v, want.v)
+    assert torch.equal(got.k[got.prefix.long()], before[0]) and torch.equal(got.v[got.prefix.long()], before[1])
+    check(out, *got.expect(two.q_rot))
+
+
+@pytest.mark.parametrize("two_calls", [False, True])
+def test_new_tokens_on_both_sides_of_the_prefix_end(R, two_calls):
+    """Of new tokens that start inside the prefix, those inside it are not written and the others are, in both forms."""
+    c = Case([600, 512 + 1, 700], 3, 8, 2, 128, 16, 512, seed=82, poison=False)
+    c.table[:, :32] = c.prefix
+    step, new, pos = _step(R, c, 83)                         # (sequence 1: positions 510, 511 and 512)
+    before = c.k[c.prefix.long()].clone(), c.v[c.prefix.long()].clone()
+    block = int(c.table[1, 32])
+    step(c.q, *new, pos, c.lens if two_calls else None)
+    assert step.error_bits() == R.RRA_ERR_POSITION
+    assert torch.equal(c.k[c.prefix.long()], before[0]) and torch.equal(c.v[c.prefix.long()], before[1])
+    assert torch.equal(c.v[block, 0], new[1][1, 2])
