@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) accept_draft_kernel(cons
     if (x < 0 || x >= V) {
       if (scribe) flag_error(a.err, RRA_ERR_TOKEN);
     } else {
-      const float px = Elem<T>::load(prow + lane * a.p_st + x);
-      const float qx = a.q != nullptr ? Elem<T>::load(qrow + lane * a.q_st + x) : 1.f;
+      const float px = load_prob(prow + lane * a.p_st + x);
+      const float qx = a.q != nullptr ? load_prob(qrow + lane * a.q_st + x) : 1.f;
       keep = static_cast<double>(u) * static_cast<double>(qx) < static_cast<double>(px);
     }
   }
