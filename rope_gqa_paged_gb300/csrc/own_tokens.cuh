@@ -200,12 +200,12 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
   int p0, L;  // row (j, head) attends [0, p0 + j]
   if (a.positions != nullptr) {
     p0 = __ldcg(a.positions + b);
-    L = p0 + gamma;
-    if (p0 < a.prefix_len || L > a.capacity) {
+    if (p0 < a.prefix_len || p0 > a.capacity - gamma) {
       if (lane == 0 && blockIdx.x == 0 && split == 0) flag_error(a.err, RRA_ERR_POSITION);
       leave();
       return;
     }
+    L = p0 + gamma;
   } else {
     L = __ldcg(a.seq_lens + b);
     if (L < 0 || L > a.capacity) {

@@ -184,8 +184,8 @@ __device__ __forceinline__ bool short_sequence(const DecodeArgs& a, int L) { ret
 
 // L_b of sequence b, cut to the cache; the caller flags what is out of range.
 __device__ __forceinline__ int attended_length(const DecodeArgs& a, int b) {
-  const int L = a.positions != nullptr ? __ldcg(a.positions + b) + a.gamma : __ldcg(a.seq_lens + b);
-  return min(max(L, 0), a.capacity);
+  if (a.positions == nullptr) return min(max(__ldcg(a.seq_lens + b), 0), a.capacity);
+  return min(max(min(__ldcg(a.positions + b), a.capacity) + a.gamma, 0), a.capacity);
 }
 
 template <int D, int NQ>
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   // (the lengths are older than the kernels that wrote the partials, which let this one start)
   const int L = attended_length(a, b);
   const int p0 = a.positions != nullptr ? __ldcg(a.positions + b) : a.prefix_len;
-  const bool refused = a.positions != nullptr && (p0 < a.prefix_len || p0 + a.gamma > a.capacity);
+  const bool refused = a.positions != nullptr && (p0 < a.prefix_len || p0 > a.capacity - a.gamma);
   const int n = a.prefix_splits + (a.prefix_splits > 0 && short_sequence(a, L)
                                        ? min(L, 1)
                                        : (max(L - a.first_token, 0) + a.chunk - 1) / a.chunk);

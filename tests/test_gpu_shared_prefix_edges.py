@@ -1,5 +1,5 @@
 """Shared-prefix attention at the edges of its range: rows of a few tokens, streams other than torch's current one, new
-tokens at the end of the prefix.
+tokens at the end of the prefix, positions past any cache.
 
 Tolerance of rows that attend at most 256 tokens, per output element: the weights enter the second product as two bf16
 parts (2^-16 of each weight), the float32 scores (128 products of N(0,1) values: below 2^-13 of a weight), exponentials
@@ -122,3 +122,28 @@ def test_new_tokens_on_both_sides_of_the_prefix_end(R, two_calls):
     assert step.error_bits() == R.RRA_ERR_POSITION
     assert torch.equal(c.k[c.prefix.long()], before[0]) and torch.equal(c.v[c.prefix.long()], before[1])
     assert torch.equal(c.v[block, 0], new[1][1, 2])
+
+
+@pytest.mark.parametrize("P,splits,pre", [(512, 2, 2), (512, 0, 0), (0, 1, 0), (0, 3, 0)])
+@pytest.mark.parametrize("far", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 31 - 4, -2 ** 31, 2 ** 30])
+def test_positions_far_out_of_range_leave_the_output(R, P, splits, pre, far):
+    """Positions whose last token's would pass 2^31, with one and with several partials: flagged, the sequence's output
+    as it was, the other sequences' right."""
+    c = Case([P + 88, P + 60, P + 200], 3, 8, 2, 128, 16, P, seed=90, poison=False)
+    g = torch.Generator(device=DEV).manual_seed(91)
+    new = [torch.randn(c.B, 3, c.Hkv, c.D, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+    pos = (c.lens - 3).int()
+    pos[1] = far
+    step = R.SharedPrefixStep(c.B, 3, c.Hq, c.Hkv, c.D, c.k, c.v, c.prefix, P, c.table, num_splits=splits,
+                              prefix_splits=pre)
+    assert (step.splits + step.prefix_chunks == 1) == (splits == 1 and P == 0)
+    k0, v0 = c.k.clone(), c.v.clone()
+    step.out.fill_(5.0)
+    step.q_rot.zero_()
+    out = step(c.q, *new, pos)
+    assert step.error_bits() == R.RRA_ERR_POSITION
+    assert (out[1] == 5.0).all()
+    own = c.table[1, P // 16:].long()
+    assert torch.equal(c.k[own], k0[own]) and torch.equal(c.v[own], v0[own])
+    want, mag = c.expect(step.q_rot)
+    check(out[[0, 2]], want[[0, 2]], mag[[0, 2]])
