@@ -224,15 +224,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     mbar_init(mma_done, 1);
     fence_barrier_init();
   }
+  // The kernel after this one reads the same inputs without waiting for this one, so it may start
+  // only when this wait is over: every kernel before this one has then completed.
+  pdl_wait();
+  pdl_launch_dependents();
+  // Tensor Memory only now: a kernel before this one that lets it start early and then allocates (decode_tc_kernel,
+  // prefill_tc_kernel) would wait for columns held here, while this CTA waits for that kernel. The two kernels
+  // after this one use none.
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, C::kTmemCols);
     tc::tmem_relinquish();
     tc::fence_before_sync();
   }
-  // The kernel after this one reads the same inputs without waiting for this one, so it may start
-  // only when this wait is over: every kernel before this one has then completed.
-  pdl_wait();
-  pdl_launch_dependents();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);

@@ -232,3 +232,19 @@ def test_two_call_step_hands_on_the_callers_tensors(rra, monkeypatch):
         assert any(a is stream for a in args), name
         assert all(id(a) in known for a in args if isinstance(a, torch.Tensor)), name
     assert any(a is given["positions"] for a in calls[0][1]) and any(a is given["seq_lens"] for a in calls[1][1])
+
+
+def test_tensor_memory_is_allocated_behind_the_wait():
+    """A kernel that may start before the one ahead of it ends takes Tensor Memory only when that one is complete: the one
+    ahead may still have to allocate its own, and neither would end. (Shown by the order in the source, never by running.)"""
+    import glob
+    import os
+    import re
+    found = 0
+    for path in glob.glob(os.path.join(_build.CSRC, "*.cu*")):
+        text = re.sub(r"//[^\n]*", "", open(path, encoding="utf-8").read())
+        for kernel in re.split(r"__global__", text)[1:]:
+            if "tc::tmem_alloc(" in kernel:
+                found += 1
+                assert 0 <= kernel.find("pdl_wait();") < kernel.index("tc::tmem_alloc("), path
+    assert found >= 3

@@ -1,5 +1,5 @@
 """Shared-prefix attention at the edges of its range: rows of a few tokens, streams other than torch's current one, new
-tokens at the end of the prefix, positions past any cache.
+tokens at the end of the prefix, positions past any cache, kernels beside it that hold Tensor Memory.
 
 Tolerance of rows that attend at most 256 tokens, per output element: the weights enter the second product as two bf16
 parts (2^-16 of each weight), the float32 scores (128 products of N(0,1) values: below 2^-13 of a weight), exponentials
@@ -147,3 +147,54 @@ def test_positions_far_out_of_range_leave_the_output(R, P, splits, pre, far):
     assert torch.equal(c.k[own], k0[own]) and torch.equal(c.v[own], v0[own])
     want, mag = c.expect(step.q_rot)
     check(out[[0, 2]], want[[0, 2]], mag[[0, 2]])
+
+
+def test_between_kernels_that_hold_tensor_memory(R):
+    """Calls on one stream without a wait between them, eagerly and in a graph: a decode step of one group of 128 heads and
+    a prefill (both hold all of an SM's Tensor Memory), shared-prefix calls of one and of two row tiles. Each gives what
+    it gives alone."""
+    g = torch.Generator(device=DEV).manual_seed(95)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device=DEV, dtype=torch.bfloat16)
+
+    one, two = (Case([600, 540, 530, 700], 1, 32, 8, 128, 16, 512, seed=96), Case([900] * 40, 4, 16, 2, 128, 32, 640, seed=97))
+    table = torch.arange(4 * 64, dtype=torch.int32, device=DEV).reshape(4, 64)
+    dec = R.DecodeStep(4, 128, 1, 128, randn(256, 16, 1, 128), randn(256, 16, 1, 128), table)
+    pre = R.PrefillStep(2, 200, 16, 2, 128, randn(2, 2, 256, 128), randn(2, 2, 256, 128))
+    dec_in = (randn(4, 128, 128), randn(4, 1, 128), randn(4, 1, 128), torch.tensor([900, 1000, 7, 500], dtype=torch.int32, device=DEV))
+    pre_in = (randn(2, 200, 16, 128), randn(2, 200, 2, 128), randn(2, 200, 2, 128), torch.zeros(2, dtype=torch.int32, device=DEV))
+    ws = [torch.zeros(c.plan(R, 2, 2)[2], dtype=torch.uint8, device=DEV) for c in (one, two)]
+    outs, err = [torch.empty_like(c.q) for c in (one, two)], torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def shared(i):
+        return (one, two)[i].run(R, 2, 2, ws=ws[i], err=err, out=outs[i])[0]
+
+    calls = [lambda: dec(*dec_in), lambda: shared(0), lambda: pre(*pre_in), lambda: shared(1), lambda: dec(*dec_in),
+             lambda: shared(1), lambda: pre(*pre_in), lambda: shared(0), lambda: shared(1)]
+    alone = []
+    for call in calls:
+        alone.append(call().clone())
+        torch.cuda.synchronize()
+    got = [torch.empty_like(x) for x in alone]
+
+    def row():
+        for call, o in zip(calls, got):
+            call()
+        for call, o in zip(calls, got):
+            o.copy_(call())
+
+    for _ in range(5):
+        row()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        row()
+    for o in got:
+        o.zero_()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, got))
+    assert int(err) == dec.error_bits() == pre.error_bits() == 0
