@@ -295,7 +295,8 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   // own tokens: the fewest head slices of at most 16 rows
   const int slices = (n_rep + 16 / gamma - 1) / (16 / gamma);
   p->hpc = (n_rep + slices - 1) / slices;
-  const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices), sms = std::max(1, sm_count());
+  const int64_t units = std::max<int64_t>(1, int64_t(B) * Hkv * slices);
+  const int64_t sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a GB300's)
   // Splits of `tokens` own tokens per sequence. Up to 16 units per SM: chunks of 256 tokens, but from 4 splits on
   // not more than make four units per SM (8 sequences of 6144 tokens, 8 units each: 44 us with 10 splits, 51 us
   // with 24; 48 ragged ones of up to 1500, 8 units each: 58 us with 4, 68 us with 2; 16 of 651 to 1757, 16 each: 37 us
@@ -324,15 +325,24 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   int64_t chunk = 0, splits = own_plan(capacity, &chunk);  // prefix and own tokens together
   if (prefix_len > 0 && rows > 0) {
     // What the two ways would take, in us. Rates measured on one GB300: own tokens 5.2 TB/s with up to 8
-    // rows per unit and 4.2 with more, 7 where most come from L2; a prefix CTA 6 us and per key tile 0.8
-    // us (two CTAs per SM) or 1.45 us (two row tiles); partials 7 TB/s, written and read. Sequences are taken
-    // to fill half of the capacity. (Against the best of 20 other choices, 66 random shapes: 51 equal it within 1 %,
-    // the worst takes 16 % more.)
+    // rows per unit and 4.2 with more, 7 where the prefix comes from L2; a prefix CTA 6 us and per key tile 0.8
+    // us (two CTAs per SM) or 1.45 us (two row tiles); partials 7 TB/s, written and read.
+    // How many own tokens the sequences hold is not known here: the capacity says how many they may. So the choice
+    // is by two sums, that with sequences that fill half of the capacity (at most 4096 tokens: tables are as wide as the
+    // longest sequence may become) and 0.15 of that with next to none. The first
+    // alone takes a long pass on a few SMs for free, or none at all, as soon as the tables are a few times wider
+    // than their sequences (64 sequences of up to 1024 tokens behind 32768: 58 us with tables of that width, 104 with four
+    // times the room for own tokens, 360 with sixteen times); the second alone cuts the prefix finer than pays beside
+    // own tokens (48 x 4 rows behind 8192: 62 us with 6 chunks, 55 with 3).
     const double own_rate = 1e6 * (p->hpc * gamma > 8 ? 4.2 : 5.2), row_bytes = 8.0 * D * B * gamma * Hq;
     const double token_bytes = 4.0 * D * units;  // of one token of every sequence, as often as it is read
-    const double own_bytes = token_bytes * (capacity - prefix_len) / 2;
+    const double own_bytes = token_bytes * std::min(0.5 * (capacity - prefix_len), 4096.0);
     auto merge = [&](int64_t s) { return s > 1 ? 2.0 + s * row_bytes / 7e6 : 0.0; };
-    double best = (token_bytes * prefix_len + own_bytes) / 7e6 + 3.0 + merge(splits);
+    auto cost = [](double half_full, double empty) { return half_full + 0.15 * empty; };
+    const double together_us = token_bytes * prefix_len / 7e6 + 3.0;
+    int64_t prefix_as_own_chunk = 0;
+    double best = cost(together_us + own_bytes / own_rate + merge(splits),
+                       together_us + merge(std::min(splits, own_plan(prefix_len, &prefix_as_own_chunk))));
     int64_t own_chunk = 0;
     const int64_t own_splits = own_plan(capacity - prefix_len, &own_chunk);
     const int nq = rra::shared_prefix_nq(rows), tile = rra::shared_prefix_tile(D, nq);
@@ -350,7 +360,7 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
       // meanwhile own-token CTAs run on the SMs left over, and at 0.4 of the rate beside prefix CTAs
       const double left = std::max(0.0, 1.0 - double(ctas * n) / resident);
       const double rest = std::max(0.0, own_bytes - own_rate * (left + 0.4 * (1 - left)) * pass_us);
-      const double us = pass_us + rest / own_rate + merge(n + own_splits);
+      const double us = cost(pass_us + rest / own_rate + merge(n + own_splits), pass_us + merge(n + 1));
       if (us < best || prefix_splits > 0) {
         best = us;
         p->prefix_chunk = static_cast<int>(len * tile);

@@ -248,3 +248,39 @@ def test_tensor_memory_is_allocated_behind_the_wait():
                 found += 1
                 assert 0 <= kernel.find("pdl_wait();") < kernel.index("tc::tmem_alloc("), path
     assert found >= 3
+
+
+WIDE = [dict(B=16, Hkv=8, prefix=2048, own=6144), dict(B=16, Hkv=1, prefix=2048, own=6144),
+        dict(B=16, Hkv=32, prefix=2048, own=6144), dict(B=64, Hkv=8, prefix=32768, own=1024),
+        dict(B=512, Hkv=8, prefix=16384, own=256, bs=32), dict(B=48, gamma=4, Hkv=8, prefix=8192, own=1500),
+        dict(B=21, gamma=3, Hq=42, Hkv=6, D=64, bs=8, prefix=1000, own=700), dict(B=8, Hkv=8, prefix=8192, own=100),
+        dict(B=128, gamma=8, Hkv=4, prefix=4096, own=500)]
+
+
+def _widths(kw):
+    """The plan with tables of the sequences' width, with 2, 4 and 16 times the room for own tokens, of 131072 tokens."""
+    kw = dict(kw)
+    own, bs = kw.pop("own"), kw.get("bs", 16)
+    for room in (own, 2 * own, 4 * own, 16 * own, 131072 - kw["prefix"]):
+        yield _plan(rra_module(), cols=-(-(kw["prefix"] + room) // bs), **kw)
+
+
+def rra_module():
+    from rope_gqa_paged_gb300 import rra as binding
+    return binding
+
+
+@pytest.mark.parametrize("kw", WIDE)
+def test_wide_tables_keep_the_prefix_pass(rra, kw):
+    """A table may be wider than any sequence now is: the prefix is still read once, by a pass of at most twice the time (6
+    us and 0.8 or 1.45 us for each of a chunk's key tiles of 64 or 128)."""
+    rows = kw["B"] * kw.get("gamma", 1) * (kw.get("Hq", 32) // kw["Hkv"])
+    tiles = -(-kw["prefix"] // (128 if rows > 128 or kw.get("D") == 64 else 64))
+
+    def pass_us(chunks):
+        return 6 + -(-tiles // chunks) * (1.45 if rows > 128 else 0.8)
+
+    (st, _, chunks, _), *wide = _widths(kw)
+    assert st == RRA_OK and chunks >= 1
+    for st, _, n, _ in wide:
+        assert st == RRA_OK and n >= 1 and pass_us(n) <= 2 * pass_us(chunks) and n <= 2 * chunks
