@@ -41,7 +41,7 @@ namespace own {
 
 template <int D>
 struct Cfg {
-  static constexpr int kTok = own_stage_tokens(D);         // tokens per stage
+  static constexpr int kTok = kOwnStage;                    // tokens per stage
   static constexpr int kHalves = D / 64;
   static constexpr int kGroupBytes = 1024 * kHalves;       // 8 rows: their 64-dim halves, 1 KB each
   static constexpr int kTileBytes = kTok / 8 * kGroupBytes;  // K (or V) of a stage
@@ -49,6 +49,10 @@ struct Cfg {
   static constexpr int kOffBar = kStages * 2 * kTileBytes;
   static constexpr int kSmemBytes = 1024 + kOffBar + kStages * 8;
   static constexpr int kIds = kOwnMaxBlocks / 32;          // block ids per lane
+  // Stages of a segment of a long chunk, for blocks of 8 tokens (twice and four times as many for 16 and more): at most
+  // kOwnMaxBlocks blocks, and whole turns of the ring with both phases of its barriers.
+  static constexpr int kSegStages = D == 128 ? 32 : 30;
+  static_assert(kSegStages % (2 * kStages) == 0 && kSegStages * kTok / 8 <= kOwnMaxBlocks, "segments");
 };
 
 // The kTok tokens of a stage for NT tiles of 8 rows. k / v: shared addresses of K and V (v_gen: V's generic
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
   pdl_launch_dependents();
   int start = a.first_token + split * a.chunk, chunk = a.chunk;
   int first_blk = start >> a.log2_bs;
-  int32_t ids[C::kIds];  // lane's block ids of the chunk, loaded before its length is known
+  int32_t ids[C::kIds];  // lane's block ids of the chunk (of a segment of a long one), loaded before its length is known
   auto load_ids = [&]() {
     const int32_t* row = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
     const int prefix_blks = a.prefix_len >> a.log2_bs;
@@ -215,13 +219,12 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     p0 = L - gamma;
   }
   const bool short_seq = spx::short_sequence(a, L);
-  if (short_seq && a.prefix_splits > 0) {  // all its tokens are the first unit's
-    chunk = spx::kShortTokens;
-    start = split * chunk;
-    if (start < L) {
-      first_blk = 0;
-      load_ids();
-    }
+  const bool alone = short_seq && a.prefix_splits > 0;  // all its tokens are the first unit's
+  const int fits = alone ? spx::kShortTokens : spx::own_chunk(a, L);
+  const bool moved = fits != chunk;
+  if (moved) {
+    chunk = fits;
+    start = (alone ? 0 : a.first_token) + split * chunk;
   }
   if (start >= L) {
     if (a.num_splits == 1)  // no merge: the empty sequence's rows are zero
@@ -229,17 +232,6 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
         static_cast<__nv_bfloat16*>(a.out)[out_row(i / D) * D + i % D] = __float2bfloat16_rn(0.f);
     leave();
     return;
-  }
-  const int end = min(L, start + chunk);
-  const int n_stages = (end - start + kTok - 1) / kTok;
-  {
-    const int n_blk = ((end - 1) >> a.log2_bs) - first_blk + 1;
-#pragma unroll
-    for (int k = 0; k < C::kIds; ++k)
-      if (lane + 32 * k < n_blk && (ids[k] < 0 || ids[k] >= a.num_blocks)) {
-        flag_error(a.err, RRA_ERR_BLOCK_ID);
-        ids[k] = 0;
-      }
   }
   if (lane == 0) {
     prefetch_tensormap(&k_map);
@@ -250,6 +242,10 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
   asm volatile("fence.proxy.async.global;" ::: "memory");  // the append's writes, for the copies
   __syncwarp();
 
+  // one segment, or more of a chunk that has grown
+  const int chunk_end = min(L, start + chunk);
+  const int seg_tokens = moved && !alone ? kTok * C::kSegStages << min(a.log2_bs - 3, 2) : chunk;
+  int end = 0, n_stages = 0, issued = 0;
   // stage st: tokens start + st kTok ..., one copy per box and lane, K in the even lanes and V in the odd ones
   const int bs = 1 << a.log2_bs, box = min(bs, kTok);
   auto issue = [&](int st) {
@@ -270,33 +266,31 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
       spx::tma_g2s_5d(dst, (lane & 1) ? &v_map : &k_map, 0, 0, 0, rows8, g, &full[s]);
     }
   };
-  int issued = 0;
-  for (; issued < min(C::kStages, n_stages); ++issued) issue(issued);
-
-  // Q^T as the B operand: tile n, lane holds row 8 n + lane / 4, dims 16 kk + 2 (lane % 4) + {0, 1} and (+ 8)
   uint32_t qb[NT][D / 16][2];
   int lim[NT][2];
   MmaWarpState<D> st[NT];
+  // Q^T as the B operand: tile n, lane holds row 8 n + lane / 4, dims 16 kk + 2 (lane % 4) + {0, 1} and (+ 8)
+  auto load_rows = [&]() {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = 8 * n + (lane >> 2);
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + out_row(r < rows ? r : 0) * D);
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + (lane >> 2);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + out_row(r < rows ? r : 0) * D);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      qb[n][kk][0] = r < rows ? __ldcg(q + kk * 8 + (lane & 3)) : 0u;
-      qb[n][kk][1] = r < rows ? __ldcg(q + kk * 8 + 4 + (lane & 3)) : 0u;
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qb[n][kk][0] = r < rows ? __ldcg(q + kk * 8 + (lane & 3)) : 0u;
+        qb[n][kk][1] = r < rows ? __ldcg(q + kk * 8 + 4 + (lane & 3)) : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int rr = 8 * n + 2 * (lane & 3) + j;
+        lim[n][j] = rr < rows ? p0 + rr % gamma : -1;
+        st[n].m[j] = -INFINITY;
+        st[n].l[j] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) st[n].o[i][0] = st[n].o[i][1] = st[n].o[i][2] = st[n].o[i][3] = 0.f;
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int rr = 8 * n + 2 * (lane & 3) + j;
-      lim[n][j] = rr < rows ? p0 + rr % gamma : -1;
-      st[n].m[j] = -INFINITY;
-      st[n].l[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) st[n].o[i][0] = st[n].o[i][1] = st[n].o[i][2] = st[n].o[i][3] = 0.f;
-  }
-
+  };
   bool ok = true;
   auto consume = [&](int it, auto split_p) {
     const int s = it % C::kStages;
@@ -318,12 +312,32 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
       ++issued;
     }
   };
-  if (short_seq) {
 #pragma unroll 1
-    for (int it = 0; ok && it < n_stages; ++it) consume(it, std::true_type());
-  } else {
+  for (bool again = false;; again = true) {
+    end = min(chunk_end, start + seg_tokens);
+    n_stages = (end - start + kTok - 1) / kTok;
+    if (again || moved) {
+      first_blk = start >> a.log2_bs;
+      load_ids();
+    }
+    const int n_blk = ((end - 1) >> a.log2_bs) - first_blk + 1;
+#pragma unroll
+    for (int k = 0; k < C::kIds; ++k)
+      if (lane + 32 * k < n_blk && (ids[k] < 0 || ids[k] >= a.num_blocks)) {
+        flag_error(a.err, RRA_ERR_BLOCK_ID);
+        ids[k] = 0;
+      }
+    for (issued = 0; issued < min(C::kStages, n_stages); ++issued) issue(issued);
+    if (!again) load_rows();
+    if (short_seq) {
 #pragma unroll 1
-    for (int it = 0; ok && it < n_stages; ++it) consume(it, std::false_type());
+      for (int it = 0; ok && it < n_stages; ++it) consume(it, std::true_type());
+    } else {
+#pragma unroll 1
+      for (int it = 0; ok && it < n_stages; ++it) consume(it, std::false_type());
+    }
+    if (!ok || end == chunk_end) break;
+    start = end;
   }
   if (!ok) {  // no copy may still be landing when the CTA exits
     if (lane == 0) {

@@ -274,7 +274,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Shared-prefix attention: how the sequences' own tokens and the prefix are cut.
 struct SharedPlan {
   int hpc = 1;            // query heads per own-token unit (with gamma tokens at most 16 rows)
-  int chunk = 0;          // own tokens per unit
+  int chunk = 0;          // own tokens per unit (more where a sequence has more than `splits` of these)
   int splits = 1;
   int prefix_splits = 0;  // 0: no separate pass, the own-token kernel reads the prefix too
   int prefix_chunk = 0;
@@ -305,8 +305,14 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
   // 64 to 6144 tokens, 32 each: 125 us with 6, 132 us with 4). Chunks are shorter, down to 64 tokens, where not
   // even four units per SM would be there (a warp takes 0.36 to 0.44 us per 16 tokens: 4 sequences of 550
   // tokens, 8 units each, 13.0 us with 3 splits, 8.2 us with 9).
+  // A table with room for more than 8192 own tokens says nothing about its sequences' lengths: chunks are then those of
+  // 2048 tokens, in at most 32 units per SM (at least 8 per sequence), and grow where a sequence has more. (Units that
+  // have nothing to do cost time too: 512 sequences behind 16384 tokens take 132 us with tables of their width, 158 with
+  // tables of 131072 tokens so, 611 with a unit for every 1024 tokens that those could hold.)
   auto own_plan = [&](int64_t tokens, int64_t* chunk_tokens) -> int64_t {
-    const int tok = rra::own_stage_tokens(D);
+    const int tok = rra::kOwnStage;
+    const int64_t room = tokens;
+    if (num_splits == 0 && tokens > 8192) tokens = 2048;
     const int64_t stages = std::max<int64_t>(1, (tokens + tok - 1) / tok), four = 4 * sms;
     const int64_t fine = (stages * tok + 255) / 256, even = std::max<int64_t>(1, (four + units / 2) / units);
     int64_t n = num_splits;
@@ -320,6 +326,7 @@ int make_plan_shared(int B, int gamma, int Hq, int Hkv, int D, int prefix_len, i
     const int64_t splits = (stages + chunk - 1) / chunk;
     chunk = (stages + splits - 1) / splits;  // as even as they can be
     *chunk_tokens = chunk * tok;
+    if (room > tokens) return std::min((room + chunk * tok - 1) / (chunk * tok), std::max<int64_t>(8, 32 * sms / units));
     return (stages + chunk - 1) / chunk;
   };
   int64_t chunk = 0, splits = own_plan(capacity, &chunk);  // prefix and own tokens together
@@ -1382,7 +1389,7 @@ static int shared_prefix_launch(const void* q_rot, const void* k_pool, const voi
   if (w.total > 0 && (workspace == nullptr || ws_bytes < w.total || !aligned16(workspace))) return RRA_EWORKSPACE;
   if (check_only) return RRA_OK;
   rra::SharedMaps maps{};
-  const int own_rows = std::min(block_size, rra::own_stage_tokens(D));
+  const int own_rows = std::min(block_size, rra::kOwnStage);
   st = encode_group_map(&maps.k_own, k_pool, num_blocks, block_size, Hkv, D, own_rows);
   if (st == RRA_OK) st = encode_group_map(&maps.v_own, v_pool, num_blocks, block_size, Hkv, D, own_rows);
   if (st == RRA_OK && p.prefix_splits > 0) {

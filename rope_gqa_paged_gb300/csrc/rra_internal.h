@@ -93,7 +93,8 @@ struct DecodeArgs {
   // Shared prefix (shared_prefix.cuh, own_tokens.cuh): the first prefix_len tokens of every sequence are
   // in prefix_blocks. With prefix_splits > 0 their attention is computed for all rows at once, in
   // chunks of prefix_chunk tokens whose partials fill slots [0, prefix_splits) of num_splits; the
-  // sequences' own tokens start at first_token (prefix_len, or 0 when prefix_splits is 0).
+  // sequences' own tokens start at first_token (prefix_len, or 0 when prefix_splits is 0), in units of `chunk` tokens, or
+  // of as many more as make a long sequence's units no more than the other slots.
   const int32_t* prefix_blocks;
   int prefix_len;
   int prefix_splits;
@@ -203,8 +204,8 @@ constexpr int kSharedPrefixRows = 128;
 // keys of a tile: 64 (128 at head dim 64) for one row tile per CTA, 128 for two (NQ)
 __host__ __device__ constexpr int shared_prefix_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
 __host__ __device__ constexpr int shared_prefix_nq(int64_t rows) { return rows > kSharedPrefixRows ? 2 : 1; }
-// tokens of an own-token stage, the most blocks of one own-token chunk
-__host__ __device__ constexpr int own_stage_tokens(int) { return 32; }
+// tokens of an own-token stage, the block ids that an own-token unit holds at a time
+constexpr int kOwnStage = 32;
 constexpr int kOwnMaxBlocks = 128;
 // The pools as {64 dims, 8 rows, D / 64 halves, groups of 8 rows, Hkv}: boxes of min(block size, prefix tile)
 // rows (prefix_splits > 0) and of min(block size, own stage) rows.

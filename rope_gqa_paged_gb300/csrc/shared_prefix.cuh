@@ -182,6 +182,14 @@ constexpr int kShortRow = 256;
 constexpr int kShortTokens = kShortRow + 16;
 __device__ __forceinline__ bool short_sequence(const DecodeArgs& a, int L) { return L - a.gamma < kShortRow; }
 
+// Own tokens per unit of a sequence of attended length L.
+__device__ __forceinline__ int own_chunk(const DecodeArgs& a, int L) {
+  const int slots = a.num_splits - a.prefix_splits, tokens = L - a.first_token;
+  if (tokens <= slots * a.chunk) return a.chunk;
+  const int stages = (tokens + kOwnStage - 1) / kOwnStage;
+  return (stages + slots - 1) / slots * kOwnStage;
+}
+
 // L_b of sequence b, cut to the cache; the caller flags what is out of range.
 __device__ __forceinline__ int attended_length(const DecodeArgs& a, int b) {
   if (a.positions == nullptr) return min(max(__ldcg(a.seq_lens + b), 0), a.capacity);
@@ -537,9 +545,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   const int L = attended_length(a, b);
   const int p0 = a.positions != nullptr ? __ldcg(a.positions + b) : a.prefix_len;
   const bool refused = a.positions != nullptr && (p0 < a.prefix_len || p0 > a.capacity - a.gamma);
+  const int chunk = own_chunk(a, L);
   const int n = a.prefix_splits + (a.prefix_splits > 0 && short_sequence(a, L)
                                        ? min(L, 1)
-                                       : (max(L - a.first_token, 0) + a.chunk - 1) / a.chunk);
+                                       : (max(L - a.first_token, 0) + chunk - 1) / chunk);
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
   const float* o = a.ws_o + row * a.num_splits * D + lane * E;
   float next[kBatch][E];

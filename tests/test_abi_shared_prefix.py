@@ -284,3 +284,14 @@ def test_wide_tables_keep_the_prefix_pass(rra, kw):
     assert st == RRA_OK and chunks >= 1
     for st, _, n, _ in wide:
         assert st == RRA_OK and n >= 1 and pass_us(n) <= 2 * pass_us(chunks) and n <= 2 * chunks
+
+
+@pytest.mark.parametrize("kw", WIDE)
+def test_wide_tables_keep_units_and_workspace_in_bounds(rra, kw):
+    """Room for 32 units per SM, for 8 of a sequence at least, however wide the table; the workspace with it."""
+    n_rep = kw.get("Hq", 32) // kw["Hkv"]
+    slices = -(-n_rep // (16 // kw.get("gamma", 1)))
+    units, rows = kw["B"] * kw["Hkv"] * slices, kw["B"] * kw.get("gamma", 1) * kw.get("Hq", 32)
+    for st, own, chunks, ws in _widths(kw):
+        assert st == RRA_OK and 1 <= own <= max(8, 32 * 152 // units)
+        assert ws <= rows * (own + chunks) * (kw.get("D", 128) + 2) * 4 + 256

@@ -1,5 +1,6 @@
 """Shared-prefix attention at the edges of its range: rows of a few tokens, streams other than torch's current one, new
-tokens at the end of the prefix, positions past any cache, kernels beside it that hold Tensor Memory.
+tokens at the end of the prefix, positions past any cache, kernels beside it that hold Tensor Memory, tables wider than
+their sequences.
 
 Tolerance of rows that attend at most 256 tokens, per output element: the weights enter the second product as two bf16
 parts (2^-16 of each weight), the float32 scores (128 products of N(0,1) values: below 2^-13 of a weight), exponentials
@@ -198,3 +199,55 @@ def test_between_kernels_that_hold_tensor_memory(R):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, got))
     assert int(err) == dec.error_bits() == pre.error_bits() == 0
+
+
+def widen(c, tokens):
+    """The same tables with room for `tokens` tokens a sequence (entries past the sequences unset)."""
+    c.table = torch.nn.functional.pad(c.table, (0, tokens // c.bs - c.cols), value=-9).contiguous()
+    c.cols = tokens // c.bs
+
+
+@pytest.mark.parametrize("B,gamma,Hq,Hkv,D,bs,P", [(6, 1, 32, 8, 128, 16, 512), (40, 4, 16, 2, 128, 32, 640),
+                                                   (5, 3, 42, 6, 64, 8, 264), (4, 1, 32, 1, 128, 128, 1024), (7, 2, 8, 8, 64, 16, 0)])
+@pytest.mark.parametrize("pre", [0, 2])
+def test_width_of_the_tables(R, B, gamma, Hq, Hkv, D, bs, P, pre):
+    """Tables as wide as the sequences, four times as wide, of 131072 tokens."""
+    lens = [P + (gamma + 1 + 211 * b * b) % 1900 for b in range(B - 1)] + [0]
+    c = Case(lens, gamma, Hq, Hkv, D, bs, P, seed=110 + B)
+    want = c.expect()
+    for tokens in (0, 4 * c.cols * bs, 131072):
+        if tokens:
+            widen(c, tokens)
+        out, err = c.run(R, 0, pre)
+        assert int(err) == 0
+        check(out, *want, what=f"plan {c.plan(R, 0, pre)}")
+
+
+@pytest.mark.parametrize("P,pre", [(0, 0), (264, 1)])
+def test_chunks_of_more_blocks_than_are_held(R, P, pre):
+    """So many units that eight chunks are all a sequence gets: chunks of 316 blocks of 8 tokens, whose ids are loaded some
+    120 at a time."""
+    lens = [P + 30 + b % 7 for b in range(79)] + [P + 20000]
+    c = Case([P + 1] * 80, 1, 16, 16, 64, 8, P, cols=(P + 64) // 8, seed=120)
+    own = c.table.shape[1] - P // 8
+    blocks = torch.randperm(2500, device=DEV, generator=torch.Generator(device=DEV).manual_seed(121)).int()
+    g = torch.Generator(device=DEV).manual_seed(122)
+    n0 = c.k.shape[0]
+    more = [torch.randn(2500, 8, 16, 64, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+    spare = [torch.randn(n0, 8, 16, 64, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+    c.k, c.v = torch.cat([spare[0], more[0]]), torch.cat([spare[1], more[1]])
+    ids = torch.randperm(n0, device=DEV, generator=g).int()
+    c.prefix = ids[:P // 8].contiguous()
+    c.table = torch.full((80, (P + 20480) // 8), -9, dtype=torch.int32, device=DEV)
+    c.table[:, P // 8:P // 8 + own] = ids[P // 8:P // 8 + 80 * own].reshape(80, own)
+    c.table[79, P // 8:P // 8 + 2500] = n0 + blocks
+    c.cols, c.lens_list = c.table.shape[1], lens
+    c.lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    splits, chunks, _ = c.plan(R, 0, pre)
+    assert splits == 8 and chunks == pre
+    out, err = c.run(R, 0, pre)
+    assert int(err) == 0
+    check(out, *c.expect())
+    c.table[79, P // 8 + 2000] = c.k.shape[0]                # a bad id far behind the first that are loaded
+    out, err = c.run(R, 0, pre)
+    assert int(err) == R.RRA_ERR_BLOCK_ID
