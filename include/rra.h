@@ -435,7 +435,8 @@ RRA_API int rra_shared_prefix_plan(int B, int gamma, int Hq, int Hkv, int D, int
  *   n_accepted    int32 [B]: n
  *   positions, positions_out  int32 [B]: with positions_out (may equal positions), positions[b] + n + 1,
  *                 the first new token's position of the next verify step. Both may be NULL.
- * gamma is 1..32, B at most 65535, V at most 2^30. dt is bf16 or fp32. */
+ * No output may lie over another output or an input, but positions_out over positions (RRA_EINVAL, for the int32 and the
+ * random-number arrays). gamma is 1..32, B at most 65535, V at most 2^30. dt is bf16 or fp32. */
 RRA_API int rra_accept_draft(const void* target_probs, int64_t target_stride_b, int64_t target_stride_t,
                              const void* draft_probs, int64_t draft_stride_b, int64_t draft_stride_t,
                              const int32_t* draft_tokens, const int32_t* draft_lens, const float* u_accept,

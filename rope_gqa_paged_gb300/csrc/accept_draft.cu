@@ -530,6 +530,27 @@ extern "C" int rra_accept_draft(const void* target_probs, int64_t target_stride_
   if ((reinterpret_cast<uintptr_t>(target_probs) & mask) || (reinterpret_cast<uintptr_t>(draft_probs) & mask))
     return RRA_EINVAL;
   if (target_stride_b < 0 || target_stride_t < 0 || draft_stride_b < 0 || draft_stride_t < 0) return RRA_EINVAL;
+  // A sequence's inputs are read by every CTA of its cluster, its outputs written by one of them: none may lie over another
+  // array (positions_out over positions, element on element, is one thread's).
+  {
+    struct Range {
+      const void* p;
+      size_t n;
+    };
+    const size_t b = size_t(B) * 4, bg = b * gamma;
+    const Range outs[] = {{tokens_out, b + bg}, {n_accepted, b}, {positions_out, b}};
+    const Range ins[] = {{draft_tokens, bg}, {u_accept, bg}, {draft_lens, b}, {u_sample, b}, {positions, b}};
+    const auto meet = [](const Range& x, const Range& y) {
+      const uintptr_t i = reinterpret_cast<uintptr_t>(x.p), j = reinterpret_cast<uintptr_t>(y.p);
+      return i != 0 && j != 0 && i < j + y.n && j < i + x.n;
+    };
+    for (int i = 0; i < 3; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (meet(outs[i], outs[j])) return RRA_EINVAL;
+      for (const Range& in : ins)
+        if (meet(outs[i], in) && !(i == 2 && in.p == positions && positions_out == positions)) return RRA_EINVAL;
+    }
+  }
   rra::AcceptArgs a{};
   a.p = target_probs;
   a.p_sb = target_stride_b;

@@ -295,3 +295,35 @@ def test_wide_tables_keep_units_and_workspace_in_bounds(rra, kw):
     for st, own, chunks, ws in _widths(kw):
         assert st == RRA_OK and 1 <= own <= max(8, 32 * 152 // units)
         assert ws <= rows * (own + chunks) * (kw.get("D", 128) + 2) * 4 + 256
+
+
+@host_only
+def test_acceptance_refuses_outputs_over_other_arrays(rra):
+    """Every CTA of a sequence's cluster reads its inputs, one writes its outputs."""
+    names = ("p p_sb p_st q q_sb q_st tokens lens u u_last pos tokens_out kept pos_out B gamma V dt err stream").split()
+    apart = dict(tokens=1 << 16, lens=2 << 16, u=3 << 16, u_last=4 << 16, pos=5 << 16, tokens_out=6 << 16, kept=7 << 16,
+                 pos_out=8 << 16)
+    call = _caller(rra.lib().rra_accept_draft, names,
+                   [P, 500, 100, P, 400, 100] + list(apart.values()) + [3, 4, 100, rra.RRA_F32, None, None])
+    bytes_of = dict(tokens=48, lens=12, u=48, u_last=12, pos=12, tokens_out=60, kept=12, pos_out=12)
+    for out in ("tokens_out", "kept", "pos_out"):
+        for name, at in apart.items():
+            if name == out:
+                continue
+            for shift in (0, bytes_of[name] - 4, 4 - bytes_of[out]):
+                if {name, out} == {"pos", "pos_out"} and shift == 0:
+                    continue
+                assert call(**{out: at + shift}) == RRA_EINVAL, (out, name, shift)
+
+
+def test_acceptance_checks_overlaps_last(rra):
+    """Arrays side by side, and next positions in place, pass the check (shown on a call that fails at the launch or runs an
+    empty batch: nothing is dereferenced on the host)."""
+    if torch.cuda.is_available():
+        pytest.skip("host-only argument checks; never given fake pointers on a GPU")
+    names = ("p p_sb p_st q q_sb q_st tokens lens u u_last pos tokens_out kept pos_out B gamma V dt err stream").split()
+    side = [65536, 65536 + 48, 65536 + 60, 65536 + 108, 65536 + 120, 65536 + 132, 65536 + 192, 65536 + 204]
+    call = _caller(rra.lib().rra_accept_draft, names,
+                   [P, 500, 100, P, 400, 100] + side + [3, 4, 100, rra.RRA_F32, None, None])
+    ecuda = -5
+    assert call() == ecuda and call(pos_out=side[4]) == ecuda
