@@ -28,7 +28,8 @@
 // is one slot. The kernel before this one (shared_prefix.cuh) may still be computing the prefix's
 // partials: this one reads only what that kernel's predecessors wrote (past L1; that kernel let it
 // start after it had waited for them), and its first CTA waits for that kernel, so that the merge
-// finds both complete.
+// finds both complete. Assumed, since the documentation promises it to the grid that waits and not to one that this
+// grid lets start: what was visible to the prefix kernel after its wait is so here, read from L2.
 #pragma once
 
 #include <type_traits>

@@ -6,7 +6,7 @@
 // 2^(m_i - M) l_i. The part [0, P) has the same K and V for every sequence, so for one KV head it is
 // the attention of B x gamma x n_rep query rows over P keys: a pair of matrix products whose K and V
 // are read once for all the rows. The part [P, n) is own_tokens_kernel's. Every part leaves
-// (o, m, l) in a slot of the row; one warp per row merges the slots (shared_merge_kernel).
+// (o, m, l) in a slot of the row; one warp per row, or four, merges the slots (shared_merge_kernel).
 //
 // A prefix CTA takes one or two tiles of 128 of those rows (M of the MMAs) and a chunk of the prefix, in
 // key tiles. K and V tiles arrive by TMA through boxes of {64 dims, 8 rows, D / 64 halves, block rows /
@@ -21,7 +21,8 @@
 // here, a second P.V with the remainders of P, took 140 us instead of 137 for 512 sequences behind 16384 tokens).
 //
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
-// so S may overwrite the P before it, and one commit per S says that everything before it is
+// so S may overwrite the P before it (assumed: the PTX documentation promises it for MMAs of one shape and
+// accumulator; prefill_tc_kernel relies on the same), and one commit per S says that everything before it is
 // complete: the softmax that waits for it may rescale O, and its thread gives K_j and V_(j-1) back to
 // the producer. A row tile's chain is softmax, P.V, S, softmax, ...; the first parts of P.V run while
 // the last of the softmax do. What this took, 512 rows x 8 heads x 16384 keys in two chunks
@@ -41,7 +42,8 @@
 //   row tile's MMAs run while the other is in its softmax. Bound: that chain, some 1300 clocks per row
 //   tile and key tile, of which the MMAs are 1024 (S takes Q and K from shared memory at its full rate).
 //
-// Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain); the MMA lane waits for
+// Every wait is bounded (a timeout sets RRA_ERR_TIMEOUT and the roles drain), but for the allocation's, for columns
+// that only CTAs already at work can hold; the MMA lane waits for
 // its last commit and the producer for its last copies before Tensor Memory is released.
 #pragma once
 

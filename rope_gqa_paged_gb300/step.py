@@ -263,7 +263,8 @@ class SharedPrefixStep(VerifyStep):
                                      self.block_table, self.rope_base, self.rope_style, self.err, stream)
 
     def attend(self, seq_lens, stream=None) -> torch.Tensor:
-        """Attention of the already-appended gamma tokens over ``seq_lens`` tokens (they included)."""
+        """Attention of the already-appended gamma tokens over ``seq_lens`` tokens (they included): lengths, as
+        ``DecodeStep.attend`` takes them, not first positions as ``VerifyStep.attend``."""
         rra.rra_shared_prefix_attn(self.q_rot, self.k_cache, self.v_cache, self.prefix_blocks, self.prefix_len,
                                    self.block_table, seq_lens, self.out, self.scale, self.num_splits,
                                    self.prefix_splits, self.workspace, self.err, stream)
