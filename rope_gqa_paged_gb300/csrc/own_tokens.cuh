@@ -15,7 +15,7 @@
 //   S^T [32 tokens x 8 NT rows] = K Q^T, softmax online in base 2, O^T [D x 8 NT rows] += V^T P^T
 // P is rounded to bf16 (half a step, 2^-8 of each weight); in sequences of about kShortRow tokens or fewer, where
 // such errors do not average out, P enters as that and the bf16 of its remainder (2^-16), as in the verify
-// kernel, and all their tokens are one unit's. Maxima, sums and O stay in float32.
+// kernel, and behind a prefix of more than that all their tokens are one unit's. Maxima, sums and O stay in float32.
 //
 // Bound: HBM where units fill the SMs (1216 units of 1536 tokens, 8 KV heads of 128 dims: 7.0 TB/s with 8 rows,
 // 6.5 with 16); with one unit per SM the warp's chain of products, shuffles and exponentials (0.36
@@ -161,7 +161,8 @@ __device__ __forceinline__ void step(MmaWarpState<D> (&st)[NT], const uint32_t (
     }
 }
 
-template <int D, int NT>
+// ALONE: of short sequences behind a prefix that has a pass of its own, all tokens are the first unit's.
+template <int D, int NT, bool ALONE>
 __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ CUtensorMap k_map,
                                                         const __grid_constant__ CUtensorMap v_map, const DecodeArgs a) {
   using C = Cfg<D>;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
     p0 = L - gamma;
   }
   const bool short_seq = spx::short_sequence(a, L);
-  const bool alone = short_seq && a.prefix_splits > 0;  // all its tokens are the first unit's
+  const bool alone = ALONE && short_seq && a.prefix_splits > 0;
   const int fits = alone ? spx::kShortTokens : spx::own_chunk(a, L);
   const bool moved = fits != chunk;
   if (moved) {
@@ -381,11 +382,11 @@ __global__ void __launch_bounds__(32) own_tokens_kernel(const __grid_constant__ 
   leave();
 }
 
-template <int D, int NT>
+template <int D, int NT, bool ALONE>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using C = Cfg<D>;
   static int done[64] = {0};
-  auto kern = own_tokens_kernel<D, NT>;
+  auto kern = own_tokens_kernel<D, NT, ALONE>;
   cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const int n_rep = a.Hq / a.Hkv;

@@ -17,8 +17,11 @@
 //                     when it grows by more than 2^8), P as bf16 pairs over the S columns
 //   O_k += P V_j      kTile / 16 MMAs (M 128, N D, K 16), P the A operand from Tensor Memory, V MN-major
 // P is rounded to bf16 (half a step, 2^-8 of each weight); maxima, sums and O stay in float32. Sequences of so few
-// tokens that such errors do not average out are own_tokens_kernel's alone, which holds their P to 2^-16 (as a branch
-// here, a second P.V with the remainders of P, took 140 us instead of 137 for 512 sequences behind 16384 tokens).
+// tokens that such errors do not average out have their P held to 2^-16. Behind a prefix of up to kShortRow tokens that
+// is a second P.V here (SPLIT_P), for every row, with the bf16 remainders of P, which lie over the second half of the S
+// columns (300 sequences of up to 100 tokens behind 128 shared: 25 us, 23.5 without it, 34 with those sequences read one
+// by one). Behind a longer one they end inside the prefix or just past it, are few, and own_tokens_kernel's alone (a
+// choice between the two products in the loop over key tiles took 140 us instead of 137 for 512 sequences behind 16384).
 //
 // One lane issues the MMAs, PV(0, j - 1), S(0, j), PV(1, j - 1), S(1, j), ...; they run in issue order,
 // so S may overwrite the P before it (assumed: the PTX documentation promises it for MMAs of one shape and
@@ -178,11 +181,14 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&s)[N]) 
 }
 
 // Sequences whose first new token attends at most this many tokens (L the attended length) hold P to 2^-16, as
-// the verify kernel's do. Where the prefix has a pass of its own, one unit of the own-token kernel reads all
+// the verify kernel's do. Where a longer prefix has a pass of its own, one unit of the own-token kernel reads all
 // their tokens, at most kShortTokens - 1.
 constexpr int kShortRow = 256;
 constexpr int kShortTokens = kShortRow + 16;
 __device__ __forceinline__ bool short_sequence(const DecodeArgs& a, int L) { return L - a.gamma < kShortRow; }
+__device__ __forceinline__ bool read_alone(const DecodeArgs& a, int L) {
+  return a.prefix_splits > 0 && a.prefix_len > kShortRow && short_sequence(a, L);
+}
 
 // Own tokens per unit of a sequence of attended length L.
 __device__ __forceinline__ int own_chunk(const DecodeArgs& a, int L) {
@@ -198,7 +204,7 @@ __device__ __forceinline__ int attended_length(const DecodeArgs& a, int b) {
   return min(max(min(__ldcg(a.positions + b), a.capacity) + a.gamma, 0), a.capacity);
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool SPLIT_P>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const DecodeArgs a) {
@@ -343,6 +349,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
                             tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV,
                             (j > 0 || kk > 0) ? 1u : 0u);
           }
+          if constexpr (SPLIT_P) {
+            if (ok) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + kTile / 2 + 8 * kk,
+                                tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, 1024, C::kGroupBytes), C::kIdescPV, 1u);
+            }
+          }
           if (ok && j + 1 < n_tiles) ok = issue_s(k, j + 1);
         }
       }
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
     if (real) {
       const int b = bt / a.gamma, j_new = bt - b * a.gamma;
       const int L = attended_length(a, b);
-      lim = short_sequence(a, L) ? 0 : min(L - a.gamma + 1 + j_new, a.prefix_len);
+      lim = read_alone(a, L) ? 0 : min(L - a.gamma + 1 + j_new, a.prefix_len);
     }
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + lane_base + C::kColO + D * k;
@@ -459,15 +473,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtasPerSm)
 #pragma unroll
         for (int h = 0; h < kParts; ++h) {
           uint32_t pw[kTile / 2 / kParts];
+          [[maybe_unused]] uint32_t lw[kTile / 2 / kParts];
 #pragma unroll
           for (int c = 0; c < kTile / 2 / kParts; ++c) {
             const int cc = h * (kTile / 2 / kParts) + c;
             const uint64_t x = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
             const float e0 = ex2(lo2(x)), e1 = ex2(hi2(x));
             ls[c & 1] = add2(ls[c & 1], pack2(e0, e1));
-            pw[c] = pack_bf16x2(e0, e1);
+            if constexpr (SPLIT_P)
+              split_bf16x2(e0, e1, pw[c], lw[c]);
+            else
+              pw[c] = pack_bf16x2(e0, e1);
           }
           st_cols<kTile / 2 / kParts>(s_col + h * (kTile / 2 / kParts), pw);
+          if constexpr (SPLIT_P) st_cols<kTile / 2 / kParts>(s_col + kTile / 2 + h * (kTile / 2 / kParts), lw);
           tc::tmem_wait_st();
           if (h + 1 < kParts) {
             tc::fence_before_sync();
@@ -548,7 +567,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   const int p0 = a.positions != nullptr ? __ldcg(a.positions + b) : a.prefix_len;
   const bool refused = a.positions != nullptr && (p0 < a.prefix_len || p0 > a.capacity - a.gamma);
   const int chunk = own_chunk(a, L);
-  const int n = a.prefix_splits + (a.prefix_splits > 0 && short_sequence(a, L)
+  const int n = a.prefix_splits + (read_alone(a, L)
                                        ? min(L, 1)
                                        : (max(L - a.first_token, 0) + chunk - 1) / chunk);
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml) + row * a.num_splits;
@@ -626,11 +645,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) shared_merge_kernel(const De
   for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D, int NQ>
+template <int D, int NQ, bool SPLIT_P>
 cudaError_t launch_prefix(const DecodeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   using C = Cfg<D, NQ>;
   static int done[64] = {0};
-  auto kern = shared_prefix_kernel<D, NQ>;
+  auto kern = shared_prefix_kernel<D, NQ, SPLIT_P>;
   cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   // row tiles innermost: CTAs that read the same keys run side by side and share them through L2
