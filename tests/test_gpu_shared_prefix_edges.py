@@ -53,7 +53,7 @@ def test_rows_of_few_tokens_without_a_prefix_pass(R, Hq, Hkv, D, gamma, splits):
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (8, 8, 128), (32, 1, 128), (14, 2, 64), (64, 1, 64)])
 @pytest.mark.parametrize("gamma", [1, 4])
-@pytest.mark.parametrize("P,pre", [(8, 1), (64, 1), (264, 1), (264, 5), (1000, 3)])
+@pytest.mark.parametrize("P,pre", [(8, 1), (64, 1), (256, 1), (256, 3), (264, 1), (264, 5), (1000, 3)])
 def test_rows_of_few_tokens_in_the_prefix_pass(R, Hq, Hkv, D, gamma, P, pre):
     """One and two row tiles per CTA, rows of few tokens in one of them or in both, beside rows of many."""
     few = [n for n in FEW if n < P + 64]
