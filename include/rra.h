@@ -68,7 +68,8 @@ enum {
   RRA_ERR_TIMEOUT = 8,    /* an in-kernel pipeline wait gave up (~1 s): results are invalid */
   RRA_ERR_WORKSPACE = 16, /* the workspace's split counters were not zero: results are invalid */
   RRA_ERR_TOKEN = 32,     /* a drafted token outside [0, V): it counts as rejected */
-  RRA_ERR_PROBS = 64      /* a row of probabilities without any: token V - 1 was drawn */
+  RRA_ERR_PROBS = 64,     /* a row of probabilities without any: token V - 1 was drawn; a row of logits without a distribution */
+  RRA_ERR_TREE = 128      /* a drafted node's parent that is no earlier node and not -1: it counts as -1 */
 };
 
 /* Steps 1-2: RoPE on q and k_new at positions[b], then append rotated k and raw v.
@@ -443,6 +444,59 @@ RRA_API int rra_accept_draft(const void* target_probs, int64_t target_stride_b, 
                              const float* u_sample, const int32_t* positions, int32_t* tokens_out,
                              int32_t* n_accepted, int32_t* positions_out, int B, int gamma, int V, rra_dtype dt,
                              int32_t* err_flag, void* stream);
+
+/* --- A tree of drafted tokens ---
+ *
+ * The verify calls check a chain of drafted tokens; these check a tree of them in one pass
+ * ([Opt-2026] §五, speculative decoding, with several continuations of each token). Sequence b has
+ * p_b = positions[b] cached tokens and n_b nodes (tree_lens[b], at most N). Node j follows node
+ * parents[b, j] < j, or the last cached token (-1); its depth is the number of its ancestors among the nodes. It
+ * sits in cache slot p_b + j, is rotated for position p_b + depth (a token's position if its path is the one that
+ * is kept), and its queries attend the cached tokens [0, p_b), its ancestors and itself. A chain
+ * (parents[b, j] = j - 1) is the verify step.
+ *
+ *   q, q_out, out  bf16 [B, N, Hq, D]; k_new, v_new bf16 [B, N, Hkv, D]; caches as in the verify calls (paged blocks of
+ *                  at least 8 tokens, or contiguous). N is 1..128.
+ *   parents        int32 [B, N]; an entry outside [-1, j) sets RRA_ERR_TREE and counts as -1
+ *   tree_lens      int32 [B], 0..N (NULL: N everywhere; outside: RRA_ERR_SEQ_LEN and clamped). Nodes from n_b on are
+ *                  neither rotated nor appended nor attended, and their rows of `out` are zero. A sequence with n_b = 0 is
+ *                  a padding row: its position is not looked at.
+ * A sequence whose p_b + n_b tokens do not fit the cache, or with p_b < 0, sets RRA_ERR_POSITION and is left out: nothing of it is
+ * written. Values that a row does not attend must be finite in V all the same (0 times them is added up); keys may
+ * be anything. */
+
+/* RoPE of q and k_new (half-split or interleaved, as rra_rope_append) at positions p_b + depth, rotated k and raw v into slots
+ * p_b + j. q_out may be q. A slot whose block id is outside the pool is not written (RRA_ERR_BLOCK_ID). */
+RRA_API int rra_tree_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                            const int32_t* parents, const int32_t* tree_lens, void* q_out, void* k_cache, void* v_cache,
+                            const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks,
+                            int max_len, int B, int N, int Hq, int Hkv, int D, double rope_base, int rope_style,
+                            int32_t* err_flag, void* stream);
+
+/* The attention of the nodes over a cache that holds them already. The keys of the whole batch are cut into `num_splits`
+ * runs of equal length (0: chosen by the library, fewer where there are too few keys); the workspace of rra_tree_plan's bytes (may be NULL when
+ * that is 0) needs no filling and holds nothing between calls. Softmax weights enter P.V as bf16, those of sequences of fewer
+ * than 256 cached tokens as two bf16 parts (2^-16); maxima, sums and partial outputs are float32. `out` must not lie over
+ * q_rot. scale as in rra_decode_attn_contig. */
+RRA_API int rra_tree_attn(const void* q_rot, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                          int max_blocks_per_seq, const int32_t* positions, const int32_t* parents,
+                          const int32_t* tree_lens, int block_size, int num_blocks, int max_len, void* out, int B,
+                          int N, int Hq, int Hkv, int D, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                          int32_t* err_flag, void* stream);
+
+/* rra_tree_append, then rra_tree_attn on q_out, the second starting while the first still runs (it reads cached
+ * tokens meanwhile). q_out must not lie over q, k_new or v_new, `out` not over any of them. */
+RRA_API int rra_tree_step(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                          const int32_t* parents, const int32_t* tree_lens, void* q_out, void* k_cache, void* v_cache,
+                          const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks,
+                          int max_len, void* out, int B, int N, int Hq, int Hkv, int D, double rope_base,
+                          int rope_style, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                          int32_t* err_flag, void* stream);
+
+/* The most runs rra_tree_attn and rra_tree_step cut the batch's keys into, and their workspace bytes (max_tokens and block_size as in
+ * rra_decode_num_splits). Queries the current device's SM count when num_splits == 0. */
+RRA_API int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int block_size, int num_splits,
+                          int* splits, size_t* workspace_bytes);
 
 /* Bytes of a K+V cache: 2 * n_layers * n_kv_heads * head_dim * seq_len * batch * dtype_bytes
  * ([Opt-2026] §四 memory formula; [KVC-GQA-RoPE] §5.3). Host only; returns 0 when an

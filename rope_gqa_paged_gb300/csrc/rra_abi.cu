@@ -398,6 +398,55 @@ SharedWs shared_ws(int64_t rows, int D, const SharedPlan& p) {
   return w;
 }
 
+// Attention of drafted trees: row tiles per CTA, CTAs per KV head's rows, runs of key tiles.
+struct TreePlan {
+  int nq = 1, row_ctas = 1, ranges = 1, min_tiles = 1;
+  int rows = 0;
+  int64_t capacity = 0;
+};
+
+int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int block_size, int requested, TreePlan* p) {
+  const int st = check_shapes(B, Hq, Hkv, D, RRA_BF16);
+  if (st != RRA_OK) return st;
+  if (block_size < 0 || N < 1 || max_tokens < 1 || requested < 0) return RRA_EINVAL;
+  if (block_size > 0 && (!pow2(block_size) || block_size < 8)) return RRA_EUNSUPPORTED;
+  if (N > rra::kTreeMaxNodes) return RRA_EUNSUPPORTED;
+  const int n_rep = Hq / Hkv;
+  const int64_t rows = int64_t(N) * n_rep;
+  if (max_tokens > (int64_t(1) << 30) || Hkv > 65535 || rows > 65535 || int64_t(B) * Hkv > INT32_MAX) return RRA_ERANGE;
+  p->rows = static_cast<int>(rows);
+  p->capacity = max_tokens;
+  p->nq = rows > rra::kTreeRows ? 2 : 1;
+  p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
+  const int tile = rra::tree_tile(D, p->nq);
+  const int64_t tiles = int64_t(B) * Hkv * ((max_tokens + tile - 1) / tile);
+  if (tiles > (int64_t(1) << 40)) return RRA_ERANGE;
+  if (requested > 0) {
+    p->ranges = std::min(requested, rra::kMaxSplits);
+  } else {
+    const int sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a GB300's)
+    p->ranges = std::max(1, (p->nq == 2 ? 1 : 2) * sms / p->row_ctas);
+    p->min_tiles = 256 / tile;
+  }
+  p->ranges = static_cast<int>(std::min<int64_t>(p->ranges, std::max<int64_t>(1, (tiles + p->min_tiles - 1) / p->min_tiles)));
+  return RRA_OK;
+}
+
+// Workspace: partials o [ranges, 2, rows, D] and (max, sum) [ranges, 2, rows, 2] floats, one header per range; none for one
+// range. Nothing in it outlives a call.
+struct TreeWs {
+  size_t ml, headers, total;
+};
+TreeWs tree_ws(const TreePlan& p, int D) {
+  TreeWs w{};
+  if (p.ranges <= 1) return w;
+  const size_t slots = size_t(p.ranges) * 2 * p.rows;
+  w.ml = align256(slots * D * sizeof(float));
+  w.headers = align256(w.ml + slots * 2 * sizeof(float));
+  w.total = w.headers + size_t(p.ranges) * sizeof(int4);
+  return w;
+}
+
 // KV groups per prefill scheduling band: as many as have their prompt's K and V (T x D x 2 x
 // 2 bytes each, bf16) within 64 MB, half of the L2, and divide Hkv; at least one.
 int prefill_kv_band(int T, int Hkv, int D) {
@@ -1498,6 +1547,188 @@ int rra_shared_prefix_step(const void* q, const void* k_new, const void* v_new, 
   return shared_prefix_launch(q_out, k_pool, v_pool, prefix_blocks, prefix_len, block_table, max_blocks_per_seq,
                               nullptr, positions, block_size, num_blocks, out, B, gamma, Hq, Hkv, D, scale, num_splits,
                               prefix_splits, workspace, ws_bytes, err_flag, stream, false);
+}
+
+// What the tree calls check alike: the cache's layout and the plan.
+static int tree_checks(int B, int N, int Hq, int Hkv, int D, const int32_t* block_table, int max_blocks_per_seq, int block_size,
+                       int num_blocks, int max_len, int num_splits, TreePlan* p) {
+  int64_t capacity = max_len;
+  if (block_table != nullptr) {
+    if (block_size <= 0 || max_blocks_per_seq < 1 || num_blocks < 1) return RRA_EINVAL;
+    if (int64_t(num_blocks) * (block_size / 8) > INT32_MAX) return RRA_ERANGE;  // groups of 8 rows, a TMA coordinate
+    capacity = int64_t(max_blocks_per_seq) * block_size;
+  } else if (max_len < 1) {
+    return RRA_EINVAL;
+  }
+  return make_plan_tree(B, N, Hq, Hkv, D, capacity, block_table != nullptr ? block_size : 0, num_splits, p);
+}
+
+// Whether two arrays share memory.
+static bool meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+static bool tree_pointers(std::initializer_list<const void*> tensors) {
+  for (const void* x : tensors)
+    if (x == nullptr || !aligned16(x)) return false;
+  return true;
+}
+
+static int tree_append_launch(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                              const int32_t* parents, const int32_t* tree_lens, void* q_out, void* k_cache, void* v_cache,
+                              const int32_t* block_table, int max_blocks_per_seq, int block_size, int num_blocks, int max_len,
+                              int B, int N, int Hq, int Hkv, int D, double rope_base, int rope_style, int32_t* err_flag,
+                              void* stream) {
+  rra::TreeAppendArgs a{};
+  a.q = q;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.positions = positions;
+  a.parents = parents;
+  a.lens = tree_lens;
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_table = block_table;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.log2_bs = block_table != nullptr ? ilog2(block_size) : 0;
+  a.num_blocks = num_blocks;
+  a.capacity = block_table != nullptr ? max_blocks_per_seq * block_size : max_len;
+  a.B = B;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.rope_style = rope_style;
+  a.err = err_flag;
+  rra::fill_rope_phi(a.rope_phi, D, rope_base);
+  const cudaError_t e = rra::launch_tree_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RRA_OK : cuda_fail(e, "tree append launch");
+}
+
+int rra_tree_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions, const int32_t* parents,
+                    const int32_t* tree_lens, void* q_out, void* k_cache, void* v_cache, const int32_t* block_table,
+                    int max_blocks_per_seq, int block_size, int num_blocks, int max_len, int B, int N, int Hq, int Hkv,
+                    int D, double rope_base, int rope_style, int32_t* err_flag, void* stream) {
+  TreePlan p;
+  int st = tree_checks(B, N, Hq, Hkv, D, block_table, max_blocks_per_seq, block_size, num_blocks, max_len, 1, &p);
+  if (st != RRA_OK) return st;
+  if (!(rope_base > 1.0) || !std::isfinite(rope_base) || (rope_style != 0 && rope_style != 1)) return RRA_EINVAL;
+  if (B == 0) return RRA_OK;
+  if (!parents) return RRA_EINVAL;
+  const size_t kv = size_t(B) * N * Hkv * D * 2, rows = size_t(B) * N * Hq * D * 2;
+  if (!tree_pointers({q, k_new, v_new, q_out, k_cache, v_cache}) || !positions) return RRA_EINVAL;
+  if (meet(q_out, rows, k_new, kv) || meet(q_out, rows, v_new, kv) || (q_out != q && meet(q_out, rows, q, rows)))
+    return RRA_EINVAL;
+  return tree_append_launch(q, k_new, v_new, positions, parents, tree_lens, q_out, k_cache, v_cache, block_table,
+                            max_blocks_per_seq, block_size, num_blocks, max_len, B, N, Hq, Hkv, D, rope_base, rope_style,
+                            err_flag, stream);
+}
+
+// after_append: behind the append of the same call. check_only: what would be refused.
+static int tree_attn_launch(const void* q_rot, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            int max_blocks_per_seq, const int32_t* positions, const int32_t* parents,
+                            const int32_t* tree_lens, int block_size, int num_blocks, int max_len, void* out, int B, int N,
+                            int Hq, int Hkv, int D, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                            int32_t* err_flag, void* stream, bool after_append, bool check_only) {
+  TreePlan p;
+  int st = tree_checks(B, N, Hq, Hkv, D, block_table, max_blocks_per_seq, block_size, num_blocks, max_len, num_splits, &p);
+  if (st != RRA_OK) return st;
+  if (!std::isfinite(scale)) return RRA_EINVAL;
+  if (B == 0) return RRA_OK;
+  if (!tree_pointers({q_rot, k_cache, v_cache, out}) || !positions || !parents) return RRA_EINVAL;
+  const size_t rows = size_t(B) * N * Hq * D * 2;
+  if (meet(out, rows, q_rot, rows)) return RRA_EINVAL;
+  const TreeWs w = tree_ws(p, D);
+  if (w.total > 0 && (workspace == nullptr || ws_bytes < w.total || !aligned16(workspace))) return RRA_EWORKSPACE;
+  if (check_only) return RRA_OK;
+  CUtensorMap km{}, vm{};
+  const int tile = rra::tree_tile(D, p.nq);
+  if (block_table != nullptr) {
+    st = encode_group_map(&km, k_cache, num_blocks, block_size, Hkv, D, std::min(block_size, tile));
+    if (st == RRA_OK) st = encode_group_map(&vm, v_cache, num_blocks, block_size, Hkv, D, std::min(block_size, tile));
+  } else {
+    st = encode_contig_map(&km, k_cache, B, Hkv, max_len, D, tile, RRA_BF16);
+    if (st == RRA_OK) st = encode_contig_map(&vm, v_cache, B, Hkv, max_len, D, tile, RRA_BF16);
+  }
+  if (st != RRA_OK) return st;
+  rra::TreeArgs a{};
+  a.q = q_rot;
+  a.positions = positions;
+  a.parents = parents;
+  a.lens = tree_lens;
+  a.block_table = block_table;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.log2_bs = block_table != nullptr ? ilog2(block_size) : 0;
+  a.num_blocks = num_blocks;
+  a.capacity = static_cast<int>(p.capacity);
+  a.out = out;
+  a.B = B;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.n_rep = Hq / Hkv;
+  a.rows = p.rows;
+  a.nq = p.nq;
+  a.row_ctas = p.row_ctas;
+  a.ranges = p.ranges;
+  a.min_tiles = p.min_tiles;
+  if (p.ranges > 1) {
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    a.ws_o = reinterpret_cast<float*>(base);
+    a.ws_ml = reinterpret_cast<float*>(base + w.ml);
+    a.headers = reinterpret_cast<int4*>(base + w.headers);
+    a.headers_by_unit = int64_t(B) * Hkv <= p.ranges ? 1 : 0;
+  }
+  const float s = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
+  a.scale_log2 = s * 1.4426950408889634f;
+  a.after_append = after_append ? 1 : 0;
+  a.err = err_flag;
+  return finish_decode(rra::launch_tree_attn(a, km, vm, static_cast<cudaStream_t>(stream)));
+}
+
+int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int block_size, int num_splits, int* splits,
+                  size_t* workspace_bytes) {
+  TreePlan p;
+  const int st = make_plan_tree(B, N, Hq, Hkv, D, max_tokens, block_size, num_splits, &p);
+  if (st != RRA_OK) return st;
+  if (splits != nullptr) *splits = p.ranges;
+  if (workspace_bytes != nullptr) *workspace_bytes = tree_ws(p, D).total;
+  return RRA_OK;
+}
+
+int rra_tree_attn(const void* q_rot, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                  int max_blocks_per_seq, const int32_t* positions, const int32_t* parents, const int32_t* tree_lens,
+                  int block_size, int num_blocks, int max_len, void* out, int B, int N, int Hq, int Hkv, int D,
+                  float scale, int num_splits, void* workspace, size_t ws_bytes, int32_t* err_flag, void* stream) {
+  return tree_attn_launch(q_rot, k_cache, v_cache, block_table, max_blocks_per_seq, positions, parents, tree_lens,
+                          block_size, num_blocks, max_len, out, B, N, Hq, Hkv, D, scale, num_splits, workspace, ws_bytes,
+                          err_flag, stream, false, false);
+}
+
+int rra_tree_step(const void* q, const void* k_new, const void* v_new, const int32_t* positions, const int32_t* parents,
+                  const int32_t* tree_lens, void* q_out, void* k_cache, void* v_cache, const int32_t* block_table,
+                  int max_blocks_per_seq, int block_size, int num_blocks, int max_len, void* out, int B, int N, int Hq,
+                  int Hkv, int D, double rope_base, int rope_style, float scale, int num_splits, void* workspace,
+                  size_t ws_bytes, int32_t* err_flag, void* stream) {
+  // every check of both parts first, so that nothing is enqueued when one would refuse
+  int st = tree_attn_launch(q_out, k_cache, v_cache, block_table, max_blocks_per_seq, positions, parents, tree_lens,
+                            block_size, num_blocks, max_len, out, B, N, Hq, Hkv, D, scale, num_splits, workspace, ws_bytes,
+                            err_flag, stream, true, true);
+  if (st != RRA_OK) return st;
+  // (the attention may write rows of `out` while the append still reads its inputs)
+  const size_t kv = size_t(B) * N * Hkv * D * 2, rows = size_t(B) * N * Hq * D * 2;
+  if (B > 0 && (meet(out, rows, q, rows) || meet(out, rows, k_new, kv) || meet(out, rows, v_new, kv) || q_out == q))
+    return RRA_EINVAL;
+  st = rra_tree_append(q, k_new, v_new, positions, parents, tree_lens, q_out, k_cache, v_cache, block_table,
+                       max_blocks_per_seq, block_size, num_blocks, max_len, B, N, Hq, Hkv, D, rope_base, rope_style,
+                       err_flag, stream);
+  if (st != RRA_OK || B == 0) return st;
+  return tree_attn_launch(q_out, k_cache, v_cache, block_table, max_blocks_per_seq, positions, parents, tree_lens, block_size,
+                          num_blocks, max_len, out, B, N, Hq, Hkv, D, scale, num_splits, workspace, ws_bytes, err_flag,
+                          stream, true, false);
 }
 
 }  // extern "C"

@@ -213,6 +213,45 @@ struct SharedMaps {
   CUtensorMap k_prefix, v_prefix, k_own, v_own;
 };
 cudaError_t launch_shared_prefix(const DecodeArgs& a, const SharedMaps& maps, cudaStream_t stream);
+// Attention of a tree of drafted tokens (tree.cuh): rows of a row tile; keys of a tile for NQ row tiles per CTA; most nodes.
+constexpr int kTreeRows = 128;
+constexpr int kTreeMaxNodes = 128;
+__host__ __device__ constexpr int tree_tile(int D, int NQ) { return NQ == 2 || D == 64 ? 128 : 64; }
+struct TreeArgs {
+  const void* q;                // q_rot [B, N, Hq, D]
+  const int32_t* positions;     // [B] cached tokens before the tree
+  const int32_t* parents;       // [B, N]
+  const int32_t* lens;          // [B] nodes, or nullptr (N)
+  const int32_t* block_table;   // [B, max_blocks_per_seq] (paged only)
+  int max_blocks_per_seq, log2_bs, num_blocks;
+  int capacity;                 // tokens a sequence can hold
+  void* out;                    // [B, N, Hq, D]
+  int B, N, Hq, Hkv, D, n_rep;
+  int rows;                     // N * n_rep
+  int nq, row_ctas;             // row tiles per CTA, CTAs for the rows of a KV head
+  int ranges, min_tiles;        // runs of key tiles, the least tiles of one
+  float* ws_o;                  // [ranges, 2, rows, D] unnormalised partial outputs (ranges > 1)
+  float* ws_ml;                 // [ranges, 2, rows, 2] (running max in log2 units, running sum)
+  int4* headers;                // what tree_merge_kernel joins: (partials, first range, sequence, KV head), 0 partials: nothing
+  int headers_by_unit;          // one per (sequence, KV head), otherwise one per range
+  float scale_log2;
+  int after_append;             // the kernel before this one is the append of the same call
+  int32_t* err;
+};
+cudaError_t launch_tree_attn(const TreeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+struct TreeAppendArgs {
+  const void *q, *k_new, *v_new;  // [B, N, H, D]
+  const int32_t *positions, *parents, *lens;
+  void *q_out, *k_cache, *v_cache;
+  const int32_t* block_table;
+  int max_blocks_per_seq, log2_bs, num_blocks;
+  int capacity;                 // contiguous: max_len
+  int B, N, Hq, Hkv, D;
+  int rope_style;
+  int32_t* err;
+  uint32_t rope_phi[kMaxDecodeHeadDim / 2][3];
+};
+cudaError_t launch_tree_append(const TreeAppendArgs& a, cudaStream_t stream);
 // Prefill: causal attention of the T = a.gamma prompt tokens of each sequence (a.positions: the
 // first one's position); 64 query rows (a.hpc heads x 64 / a.hpc tokens) per CTA.
 cudaError_t launch_prefill(const DecodeArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, bool paged,

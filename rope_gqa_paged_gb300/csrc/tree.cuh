@@ -1,0 +1,766 @@
+// Attention of a tree of drafted tokens over each sequence's cache, on the fifth-generation tensor cores.
+//
+// Sequence b has p cached tokens and a tree of n nodes in cache slots p .. p + n - 1 (their keys rotated for position
+// p + depth). Query row (node j, head i of a KV head's group) attends [0, p), its ancestors and itself: one
+// softmax over p + depth + 1 tokens,
+//   out = sum_t e^(s_t - m) V_t / sum_t e^(s_t - m),   s_t = scale q.K_t,   m = max s_t.
+// For one KV head these are n x n_rep rows over the same p + n keys, so the rows are M of the MMAs and every K and V
+// byte that comes from HBM serves all of them (a tree of 16 nodes with 4 heads per group: 64 flops per byte;
+// 256 rows need as many clocks of the tensor cores as HBM needs for their keys). The mask is in the last tiles
+// only: bit words of the row's ancestors, shifted to the tile.
+//
+// Work: the key tiles of all (sequence, KV head) units, in one line, cut into `ranges` runs of equal length; the
+// CTAs of a range (one per kRows x NQ rows: they share its keys through L2) go through its units or parts of
+// units. So the load is even whatever the sequences' lengths are, which the host does not know: every CTA adds up the
+// lengths for itself. A unit that lies wholly in one range is written to the output; the parts of a cut one leave
+// (o, m, l) for tree_merge_kernel. Those are the first and the last unit of a range at most.
+//
+// In a CTA the roles run through the same list of units: a producer warp (K and V tiles by TMA into a ring that goes
+// on over unit borders), an MMA lane and a softmax warpgroup for each row tile. For row tile k and key tile j
+//   S_k = Q_k K_j^T   D / 16 MMAs (M 128, N kTile, K 16) into Tensor Memory
+//   softmax           one row per thread; running max, moved only when it grows by more than 2^8
+//   O_k += P V_j      kTile / 16 MMAs, P (bf16) the A operand from Tensor Memory over the S columns
+// as in shared_prefix.cuh, whose notes on issue order and on waits hold here too. At the end of a unit the next one's
+// Q goes in before O is read, so that its first S runs meanwhile; its first P.V waits for the softmax of its first
+// tile, which comes after that reading.
+// P is rounded to bf16 (half a step, 2^-8 of each weight); in sequences of fewer than kShortRow cached tokens, where
+// such errors do not average out, its remainders go through a second P.V (2^-16). Maxima, sums and O are float32.
+#pragma once
+
+#include "shared_prefix.cuh"
+
+namespace rra {
+namespace tree {
+
+using spx::add2;
+using spx::elect_one;
+using spx::ex2;
+using spx::fma2;
+using spx::hi2;
+using spx::kRescaleLog2;
+using spx::kShortRow;
+using spx::ld_cols;
+using spx::lo2;
+using spx::max3;
+using spx::pack2;
+using spx::scale_cols8;
+using spx::st_cols;
+using spx::tma_g2s_5d;
+using spx::warp_wait;
+
+constexpr int kRows = kTreeRows;
+
+template <int D, int NQ, bool PAGED>
+struct Cfg {
+  static constexpr int kTile = tree_tile(D, NQ);             // keys per tile
+  static constexpr int kParts = kTile == 128 ? 4 : 2;        // of a P tile, each handed to the MMAs as soon as it is there
+  static constexpr int kHalves = D / 64;
+  // paged: 8-row groups with their 64-dim halves side by side; contiguous: whole halves
+  static constexpr int kGroupBytes = PAGED ? 1024 * kHalves : 1024;
+  static constexpr int kHalfBytes = PAGED ? 1024 : kTile * 128;
+  static constexpr int kTileBytes = kTile * 128 * kHalves;
+  static constexpr int kQHalfBytes = kRows * 128;            // NQ 2: Q tiles, K-major, 64-dim halves
+  static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
+  static constexpr int kRing = NQ == 2 && D == 128 ? 4 : 6;  // slots: K_0, V_0, K_1, V_1, ...
+  static constexpr int kWarps = 4 * NQ;                      // softmax warps
+  static constexpr int kStagePitch = 80;                     // 64 bytes of a row and 16: eight rows in other banks
+  static constexpr int kStageBytes = 32 * kStagePitch;       // per softmax warp: rows on their way out
+  // Tensor Memory columns
+  static constexpr uint32_t kColO = 0;                       // O_k: D columns each
+  static constexpr uint32_t kColS = NQ * D;                  // S_k: kTile columns each, P over their first half
+  static constexpr uint32_t kColQ = kColS + NQ * kTile;      // NQ 1: Q as bf16 pairs, D / 2 columns
+  static constexpr uint32_t kTmemCols = NQ == 2 ? 512 : 256;
+  // shared memory
+  static constexpr int kOffRing = kQBytes;
+  static constexpr int kOffStage = kOffRing + kRing * kTileBytes;
+  static constexpr int kOffBar = kOffStage + kWarps * kStageBytes;
+  // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ][kParts], o_done
+  static constexpr int kNumBars = 1 + 2 * kRing + NQ + NQ * kParts + 1;
+  static constexpr int kOffStart = kOffBar + kNumBars * 8;   // Start
+  static constexpr int kOffTmemSlot = kOffStart + 144;
+  static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
+  static constexpr int kThreads = 32 * kWarps + 64;          // + producer warp + MMA warp
+  static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
+  static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kRows, kTile, false);  // Q (K-major) . K^T (K-major)
+  static constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kRows, D, true);      // P (K-major) . V (MN-major)
+  static_assert((NQ == 2 ? kColQ : kColQ + D / 2) <= kTmemCols, "Tensor Memory columns");
+  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of the SM");
+  static_assert(kThreads <= 32 * 32, "the scan's warps");
+};
+
+// Sequence b: cached tokens, nodes, key tiles. Refused: no tiles, and nothing of it is written.
+struct Seq {
+  int p, n, tiles;
+  bool refused;
+};
+__device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool flag = false) {
+  Seq s;
+  s.p = __ldcg(a.positions + b);
+  s.n = a.lens != nullptr ? __ldcg(a.lens + b) : a.N;
+  if (s.n < 0 || s.n > a.N) {
+    if (flag) flag_error(a.err, RRA_ERR_SEQ_LEN);
+    s.n = min(max(s.n, 0), a.N);
+  }
+  s.refused = s.n > 0 && (s.p < 0 || s.p > a.capacity - s.n);
+  if (flag && s.refused) flag_error(a.err, RRA_ERR_POSITION);
+  s.tiles = s.refused || s.n == 0 ? 0 : (s.p + s.n - 1) / tile + 1;
+  return s;
+}
+
+// Where a range starts: tiles [t0, t1) of all, from tile `off` of sequence b's Hkv x tiles on.
+struct Start {
+  int64_t t0, t1, total;
+  int b, ranges;
+  int64_t off;
+  int64_t sums[12];
+};
+// t-th border of `ranges` equal runs of `total` tiles
+__device__ __forceinline__ int64_t border(int64_t total, int ranges, int64_t r) { return total * r / ranges; }
+
+// Adds up the sequences' tiles and finds the start of range r (all threads of the CTA; r past the ranges in use:
+// t0 = t1). Ranges of at least min_tiles tiles, so some of a.ranges may stay unused.
+template <int THREADS>
+__device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) {
+  const int per = (a.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(sequence(a, b, tile, flag).tiles) * a.Hkv;
+  int64_t incl = mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) s->sums[warp] = incl;
+  if (threadIdx.x == 0) s->t0 = s->t1 = 0;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += s->sums[w];
+    total += s->sums[w];
+  }
+  const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
+  const int ranges = static_cast<int>(min(static_cast<int64_t>(a.ranges), max(most, int64_t(1))));
+  if (r < ranges) {
+    const int64_t t0 = border(total, ranges, r), t1 = border(total, ranges, r + 1);
+    if (t0 < t1 && before <= t0 && t0 < before + mine) {  // one thread
+      int b = b0;
+      for (;; ++b) {
+        const int64_t u = static_cast<int64_t>(sequence(a, b, tile).tiles) * a.Hkv;
+        if (t0 < before + u) break;
+        before += u;
+      }
+      s->t0 = t0;
+      s->t1 = t1;
+      s->total = total;
+      s->ranges = ranges;
+      s->b = b;
+      s->off = t0 - before;
+    }
+  }
+  __syncthreads();
+}
+
+// A range's units one after the other: key tiles [j0, j1) of KV head g of sequence b.
+struct Units {
+  int b, g, j0, j1;
+  Seq seq;
+  int64_t off, left;
+  __device__ __forceinline__ Units(const TreeArgs& a, const Start& s, int tile)
+      : b(s.b), g(0), j0(0), j1(0), seq{0, 0, 0, false}, off(s.off), left(s.t1 - s.t0) {
+    if (left > 0) seq = sequence(a, b, tile);
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, int tile, int first_row) {
+    while (left > 0) {
+      while (off >= static_cast<int64_t>(seq.tiles) * a.Hkv) {
+        off = 0;
+        seq = sequence(a, ++b, tile);
+      }
+      g = static_cast<int>(off / seq.tiles);
+      j0 = static_cast<int>(off - static_cast<int64_t>(g) * seq.tiles);
+      j1 = static_cast<int>(min(static_cast<int64_t>(seq.tiles), j0 + left));
+      off += j1 - j0;
+      left -= j1 - j0;
+      if (seq.n * a.n_rep > first_row) return true;  // (a smaller tree leaves this CTA's rows empty)
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == seq.tiles; }
+};
+
+template <int D, int NQ, bool PAGED>
+__global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>::kCtasPerSm)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                     const TreeArgs a) {
+  using C = Cfg<D, NQ, PAGED>;
+  constexpr int kTile = C::kTile, kRing = C::kRing, kParts = C::kParts;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+  const int range = blockIdx.x / a.row_ctas, first_row = (blockIdx.x - range * a.row_ctas) * NQ * kRows;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  constexpr int kProducerWarp = C::kWarps, kMmaWarp = C::kWarps + 1;
+
+  uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* ring_full = q_ready + 1;
+  uint64_t* ring_empty = ring_full + kRing;
+  uint64_t* s_full = ring_empty + kRing;
+  uint64_t* p_full = s_full + NQ;
+  uint64_t* o_done = p_full + NQ * kParts;
+  Start* start = reinterpret_cast<Start*>(smem + C::kOffStart);
+  static_assert(sizeof(Start) <= 144, "Start");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_ready, C::kWarps);  // one arrival per softmax warp
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ring_full[s], 1);
+      mbar_init(&ring_empty[s], NQ);  // every row tile gives a slot back
+    }
+    for (int k = 0; k < NQ; ++k) mbar_init(&s_full[k], 1);
+    for (int k = 0; k < NQ * kParts; ++k) mbar_init(&p_full[k], 4);
+    mbar_init(o_done, 1);
+    fence_barrier_init();
+  }
+  // Behind the append of the same call (after_append) everything that it does not write is complete already: it lets
+  // this kernel start only when its own wait is over. Queries and the tree's keys wait for it further down.
+  if (!a.after_append) pdl_wait();
+  locate<C::kThreads>(a, kTile, range, blockIdx.x == 0, start);
+
+  // rows of nodes that a tree does not have are zero
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = sequence(a, b, kTile);
+    if (s.tiles == 0 && a.headers_by_unit)
+      for (int g = threadIdx.x; g < a.Hkv; g += C::kThreads) a.headers[b * a.Hkv + g] = make_int4(0, 0, 0, 0);
+    if (s.refused || s.n == a.N) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(b) * a.N + s.n) * a.Hq * D);
+    const size_t vecs = static_cast<size_t>(a.N - s.n) * a.Hq * (D / 8);
+    for (size_t i = threadIdx.x; i < vecs; i += C::kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (start->t0 >= start->t1) {  // (the same for every thread)
+    if (threadIdx.x == 0 && first_row == 0 && a.headers != nullptr && !a.headers_by_unit) a.headers[range] = make_int4(0, 0, 0, 0);
+    pdl_wait();
+    return;
+  }
+  // Tensor Memory when every kernel that may hold some is complete, and the next kernel only when all CTAs have theirs.
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, C::kTmemCols);
+    tc::tmem_relinquish();
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  pdl_launch_dependents();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // ring position r: K of the CTA's tile r / 2 (r even) or its V (r odd)
+  auto slot_of = [](uint32_t r) { return r % kRing; };
+  auto phase_of = [](uint32_t r) { return (r / kRing) & 1u; };
+  Units u(a, *start, kTile);
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&k_map);
+      prefetch_tensormap(&v_map);
+    }
+    const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
+    const int box = PAGED ? min(bs, kTile) : kTile;  // rows per TMA box, as the tensor maps were encoded
+    bool ok = true, waited = !a.after_append;
+    uint32_t issued = 0;
+    while (ok && u.next(a, kTile, first_row)) {
+      const int L = u.seq.p + u.seq.n;
+      const int32_t* row = a.block_table + static_cast<size_t>(u.b) * a.max_blocks_per_seq;
+      // block where this lane's box of tile j starts (the id loads a tile ahead of its use)
+      auto block_of = [&](int j) {
+        const int t = j * kTile + lane * box;
+        return PAGED && j < u.j1 && lane < kTile / box && t < L ? __ldcg(row + (t >> log2_bs)) : 0;
+      };
+      int next = block_of(u.j0);
+      for (int j = u.j0; ok && j < u.j1; ++j) {
+        const int tile0 = j * kTile, nbox = PAGED ? (min(kTile, L - tile0) + box - 1) / box : 1;
+        int id = next;
+        next = block_of(j + 1);
+        if (PAGED && (id < 0 || id >= a.num_blocks)) {
+          flag_error(a.err, RRA_ERR_BLOCK_ID);
+          id = 0;
+        }
+        if (!waited && tile0 + kTile > u.seq.p) {  // the tree's keys and values
+          pdl_wait();
+          waited = true;
+        }
+        const int rows8 = PAGED ? (id << (log2_bs - 3)) + (((tile0 + lane * box) & (bs - 1)) >> 3) : 0;
+        for (int kv = 0; kv < 2; ++kv, ++issued) {
+          const uint32_t s = slot_of(issued);
+          int good = 1;
+          if (lane == 0) {
+            if (issued >= kRing && !mbar_wait(&ring_empty[s], phase_of(issued) ^ 1u))
+              good = 0;
+            else
+              mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
+          }
+          if (!__shfl_sync(0xffffffffu, good, 0)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + C::kOffRing + s * C::kTileBytes;
+          const CUtensorMap* map = kv ? &v_map : &k_map;
+          if constexpr (PAGED) {
+            if (lane < nbox)  // one copy per lane (at most 16)
+              tma_g2s_5d(dst + lane * (box >> 3) * C::kGroupBytes, map, 0, 0, 0, rows8, u.g, &ring_full[s]);
+          } else if (lane < C::kHalves) {
+            tma_g2s_3d(dst + lane * C::kHalfBytes, map, 64 * lane, tile0, u.b * a.Hkv + u.g, &ring_full[s]);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
+      // no copy may still be landing when the CTA exits
+      for (uint32_t r = issued > kRing ? issued - kRing : 0; r < issued; ++r) mbar_wait(&ring_full[slot_of(r)], phase_of(r));
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issue (one lane)
+    if (elect_one()) {
+      const uint32_t base = smem_addr(smem);
+      bool ok = true;
+      uint32_t c = 0, units = 0;  // the CTA's tiles and units so far
+      while (ok && u.next(a, kTile, first_row)) {
+        const bool short_seq = u.seq.p < kShortRow;
+        ok = mbar_wait(q_ready, units & 1u);
+        tc::fence_after_sync();
+        auto issue_s = [&](int k, uint32_t t) -> bool {
+          const uint32_t s = slot_of(2 * t);
+          if (k == 0) {
+            if (!mbar_wait(&ring_full[s], phase_of(2 * t))) return false;
+            tc::fence_after_sync();
+          }
+          const uint32_t k_base = base + C::kOffRing + s * C::kTileBytes, s_col = tmem + C::kColS + kTile * k;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * C::kHalfBytes + (kk & 3) * 32, 1024, C::kGroupBytes);
+            if constexpr (NQ == 2)
+              tc::mma_bf16_ss(s_col, tc::sw128_desc(base + (k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32,
+                                                    1024, 1024),
+                              kd, C::kIdescS, kk > 0 ? 1u : 0u);
+            else
+              tc::mma_bf16_ts(s_col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          tc::commit(&s_full[k]);
+          return true;
+        };
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) ok = ok && issue_s(k, c);
+        for (int j = u.j0; ok && j < u.j1; ++j, ++c) {
+          const uint32_t s = slot_of(2 * c + 1);
+          const uint32_t v_base = base + C::kOffRing + s * C::kTileBytes;
+          ok = mbar_wait(&ring_full[s], phase_of(2 * c + 1));
+#pragma unroll
+          for (int k = 0; k < NQ; ++k) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk) {
+              if (kk % (kTile / 16 / kParts) == 0) {
+                ok = ok && mbar_wait(&p_full[k * kParts + kk / (kTile / 16 / kParts)], c & 1u);
+                if (!ok) break;
+                tc::fence_after_sync();
+              }
+              tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + 8 * kk,
+                              tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, C::kHalfBytes, C::kGroupBytes), C::kIdescPV,
+                              (j > u.j0 || kk > 0) ? 1u : 0u);
+            }
+            if (ok && short_seq) {  // the remainders of P
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + kTile / 2 + 8 * kk,
+                                tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, C::kHalfBytes, C::kGroupBytes),
+                                C::kIdescPV, 1u);
+            }
+            if (ok && j + 1 < u.j1) ok = issue_s(k, c + 1);
+          }
+        }
+        tc::commit(o_done);  // every MMA issued above has completed once this arrives
+        ++units;
+      }
+      if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
+      if (units > 0) mbar_wait(o_done, (units - 1) & 1u);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax: thread = query row
+    const int k = warp >> 2;                               // row tile of this warpgroup
+    const int r = static_cast<int>(threadIdx.x) & 127;     // row = TMEM lane
+    const int row = first_row + k * kRows + r;             // node row / n_rep, head row % n_rep of the group
+    const int j_node = row / a.n_rep, i_head = row - j_node * a.n_rep;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t o_col = tmem + lane_base + C::kColO + D * k;
+    uint8_t* stage = smem + C::kOffStage + warp * C::kStageBytes;
+    const float sl = a.scale_log2;
+    if (a.after_append) pdl_wait();  // the queries
+
+    auto load_q = [&]() {  // the unit's query row
+      const bool real = row < u.seq.n * a.n_rep;
+      const size_t q_row = (static_cast<size_t>(u.b) * a.N + j_node) * a.Hq + u.g * a.n_rep + i_head;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q_row * D);
+      uint4 qv[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) qv[c] = real ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (NQ == 2) {  // into the Q tile (K-major, 128-byte swizzle)
+        uint8_t* dst = smem + k * C::kHalves * C::kQHalfBytes + r * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kQHalfBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
+        tc::fence_smem_to_async();
+      } else {  // into Tensor Memory: dims (2c, 2c + 1) in column kColQ + c
+        uint32_t qw[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          qw[4 * c] = qv[c].x;
+          qw[4 * c + 1] = qv[c].y;
+          qw[4 * c + 2] = qv[c].z;
+          qw[4 * c + 3] = qv[c].w;
+        }
+        st_cols<D / 2>(tmem + lane_base + C::kColQ, qw);
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready);
+    };
+
+    uint32_t c = 0, units = 0;  // the CTA's tiles and units so far
+    bool ok = true, more = u.next(a, kTile, first_row);
+    if (more) load_q();
+    while (ok && more) {
+      const int p = u.seq.p, L = p + u.seq.n;
+      const bool real = row < u.seq.n * a.n_rep, short_seq = p < kShortRow;
+      const bool warp_real = __any_sync(0xffffffffu, real);
+      const size_t out_row = (static_cast<size_t>(u.b) * a.N + j_node) * a.Hq + u.g * a.n_rep + i_head;
+      // the row's node and its ancestors, one bit each
+      uint32_t sees[kTreeMaxNodes / 32] = {};
+      if (warp_real && u.j1 * kTile > p) {
+        int up[kTreeMaxNodes / 32];  // parents of nodes lane, lane + 32, ...
+#pragma unroll
+        for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
+          const int n = 32 * w + lane;
+          up[w] = n < u.seq.n ? __ldcg(a.parents + static_cast<size_t>(u.b) * a.N + n) : -1;
+          if (up[w] < -1 || up[w] >= n) {
+            flag_error(a.err, RRA_ERR_TREE);
+            up[w] = -1;
+          }
+        }
+        int n = real ? j_node : -1;
+        while (__any_sync(0xffffffffu, n >= 0)) {  // (parents come before their children)
+          int above = -1;
+#pragma unroll
+          for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
+            const int x = __shfl_sync(0xffffffffu, up[w], n & 31);
+            if ((n >> 5) == w) {
+              above = x;
+              sees[w] |= 1u << (n & 31);
+            }
+          }
+          n = above;
+        }
+      }
+      auto seen_from = [&](int first) -> uint32_t {  // of the 32 tokens from token p + first on
+        if (first <= -32) return 0xffffffffu;
+        uint32_t lo = 0, hi = 0;
+#pragma unroll
+        for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
+          lo = w == (first >> 5) ? sees[w] : lo;
+          hi = w == (first >> 5) + 1 ? sees[w] : hi;
+        }
+        if (first < 0) lo = 0xffffffffu;  // (first >> 5 is -1 there)
+        return __funnelshift_r(lo, hi, first & 31);
+      };
+      float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
+      for (int j = u.j0; j < u.j1; ++j, ++c) {
+        if (!warp_wait(&s_full[k], c & 1u)) {  // S_k is there, and every MMA issued before it is complete
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        if (r == 0) {
+          mbar_arrive(&ring_empty[slot_of(2 * c)]);
+          if (j > u.j0) mbar_arrive(&ring_empty[slot_of(2 * c - 1)]);
+        }
+        if (L - j * kTile < kTile) {
+          // rows past the last token: their V is whatever the slot held; zeros keep 0 * V at 0 (both row
+          // tiles' threads write them, each before its own P.V)
+          if (!warp_wait(&ring_full[slot_of(2 * c + 1)], phase_of(2 * c + 1))) {
+            ok = false;
+            break;
+          }
+          if (r >= L - j * kTile && r < kTile) {
+            uint8_t* vrow = smem + C::kOffRing + slot_of(2 * c + 1) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(vrow + h * C::kHalfBytes + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          tc::fence_smem_to_async();
+        }
+        if (warp_real) {
+          const uint32_t s_col = tmem + lane_base + C::kColS + kTile * k;
+          uint32_t sv[kTile];
+          ld_cols<kTile>(s_col, sv);
+          if ((j + 1) * kTile > p) {  // the tree begins in this tile, or before it
+#pragma unroll
+            for (int w = 0; w < kTile / 32; ++w) {
+              const uint32_t see = seen_from(j * kTile + 32 * w - p);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sv[32 * w + i] = (see >> i) & 1u ? sv[32 * w + i] : __float_as_uint(-INFINITY);
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mx[x] = fmaxf(__uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]));
+#pragma unroll
+          for (int x = 8; x < kTile; x += 2)
+            mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
+          const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float m_new = fmaxf(m_use, rmax * sl);
+          const bool rescale = m_new > m_use + kRescaleLog2;  // also the first finite max
+          float alpha = 1.f;
+          if (rescale) {
+            alpha = ex2(m_use - m_new);
+            m_use = m_new;
+          }
+          if (j > u.j0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
+#pragma unroll 1
+            for (int x = 0; x < D / 8; ++x) scale_cols8(o_col + 8 * x, alpha);  // (few registers: S is held)
+          }
+          const float mref = m_use == -INFINITY ? 0.f : m_use;
+          const uint64_t sl2 = pack2(sl, sl), mref2 = pack2(-mref, -mref);
+          uint64_t ls[2] = {0, 0};
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) {
+            constexpr int kWords = kTile / 2 / kParts;
+            uint32_t pw[kWords];
+            if (short_seq) {
+              uint32_t lw[kWords];
+#pragma unroll
+              for (int x = 0; x < kWords; ++x) {
+                const int cc = h * kWords + x;
+                const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
+                const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
+                ls[x & 1] = add2(ls[x & 1], pack2(e0, e1));
+                split_bf16x2(e0, e1, pw[x], lw[x]);
+              }
+              st_cols<kWords>(s_col + kTile / 2 + h * kWords, lw);
+            } else {
+#pragma unroll
+              for (int x = 0; x < kWords; ++x) {
+                const int cc = h * kWords + x;
+                const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
+                const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
+                ls[x & 1] = add2(ls[x & 1], pack2(e0, e1));
+                pw[x] = pack_bf16x2(e0, e1);
+              }
+            }
+            st_cols<kWords>(s_col + h * kWords, pw);
+            tc::tmem_wait_st();
+            if (h + 1 < kParts) {
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[k * kParts + h]);
+            }
+          }
+          const uint64_t lsum = add2(ls[0], ls[1]);
+          l = l * alpha + (lo2(lsum) + hi2(lsum));
+        } else if (kParts > 1) {
+          __syncwarp();
+          if (lane == 0)
+            for (int h = 0; h + 1 < kParts; ++h) mbar_arrive(&p_full[k * kParts + h]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[k * kParts + kParts - 1]);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- the unit's rows, the next one's Q before them
+      const bool whole = u.whole();
+      const int slot = u.j0 > 0 ? 0 : 1;
+      const int live = u.seq.n * a.n_rep;
+      if (threadIdx.x == 0 && first_row == 0 && a.headers != nullptr) {
+        // a unit that starts here and goes on in later ranges is merged for this range's header
+        int4 h = make_int4(0, 0, 0, 0);
+        if (u.j0 == 0 && !whole) {
+          const int64_t end = start->t1 + (u.seq.tiles - u.j1);  // the unit's end among all tiles
+          int last = range + 1;
+          while (border(start->total, start->ranges, last + 1) < end) ++last;
+          h = make_int4(last - range + 1, range, u.b, u.g);
+        }
+        if (a.headers_by_unit) {
+          if (u.j0 == 0) a.headers[u.b * a.Hkv + u.g] = h;
+        } else if (u.left == 0) {
+          a.headers[range] = h;
+        }
+      }
+      more = u.next(a, kTile, first_row);
+      if (more) load_q();
+      if (!warp_wait(o_done, units & 1u)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      if (r == 0) mbar_arrive(&ring_empty[slot_of(2 * c - 1)]);
+      ++units;
+      if (warp_real) {
+        const int rows_here = min(32, live - (first_row + k * kRows + 32 * (warp & 3)));  // of this warp
+        if (whole) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const uint32_t out_lo = static_cast<uint32_t>(out_row), out_hi = static_cast<uint32_t>(out_row >> 32);
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t v[32];
+            tc::tmem_ld32(o_col + 32 * x, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = pack_bf16x2(__uint_as_float(v[8 * y + 2 * z]) * inv, __uint_as_float(v[8 * y + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(stage + lane * C::kStagePitch + 16 * y) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // 64 bytes of 8 rows at a time
+              const int rr = 8 * y + (lane >> 2);
+              const size_t to = __shfl_sync(0xffffffffu, out_lo, rr) |
+                                (static_cast<size_t>(__shfl_sync(0xffffffffu, out_hi, rr)) << 32);
+              const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * C::kStagePitch + 16 * (lane & 3));
+              if (rr < rows_here)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to * D + 32 * x + 8 * (lane & 3)) = val;
+            }
+            __syncwarp();
+          }
+        } else {
+          const size_t part = (static_cast<size_t>(range) * 2 + slot) * a.rows + row - lane;  // of lane 0's row
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t v[32];
+            tc::tmem_ld32(o_col + 32 * x, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<uint4*>(stage + lane * C::kStagePitch + 16 * y) =
+                    make_uint4(v[16 * h + 4 * y], v[16 * h + 4 * y + 1], v[16 * h + 4 * y + 2], v[16 * h + 4 * y + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {  // 64 bytes of 8 rows at a time
+                const int rr = 8 * y + (lane >> 2);
+                const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * C::kStagePitch + 16 * (lane & 3));
+                if (rr < rows_here) *reinterpret_cast<uint4*>(a.ws_o + (part + rr) * D + 32 * x + 16 * h + 4 * (lane & 3)) = val;
+              }
+              __syncwarp();
+            }
+          }
+          if (real) *reinterpret_cast<float2*>(a.ws_ml + 2 * (part + lane)) = make_float2(m_use, l);
+        }
+      }
+      tc::fence_before_sync();  // (O is read before the next unit's first P.V, which waits for its first P)
+    }
+    if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Output rows of the units that several ranges share, from their partials: one warp per row. A range writes the
+// unit that it starts with into its slot 0 and the one that it ends with into slot 1, so a unit's partials are slot 1 of
+// its first range and slot 0 of the following ones.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a) {
+  constexpr int E = D / 32;  // dims per lane
+  constexpr int kBatch = 4;  // partials loaded at a time
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 h = __ldcg(a.headers + blockIdx.x);
+  const int n = h.x, first = h.y, b = h.z, g = h.w;
+  // (what a range whose waits ran out has not written may be anything)
+  if (n < 2 || first < 0 || first >= a.ranges || n > a.ranges - first || b < 0 || b >= a.B || g < 0 || g >= a.Hkv) return;
+  const Seq s = sequence(a, b, 1);
+  if (row >= s.n * a.n_rep) return;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
+  auto slot = [&](int i) { return static_cast<size_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
+  float M = -INFINITY, l = 0.f;
+  float acc[E] = {};
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    const float2 x = s0 + lane < n ? __ldcg(ml + slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
+    float m = x.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = fmaxf(m, M);
+    const float mref = m == -INFINITY ? 0.f : m;
+    const float w = ex2(x.x - mref), keep = ex2(M - mref);
+    float ls = w * x.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    l = l * keep + ls;
+    M = m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+    for (int i = s0; i < min(n, s0 + 32); i += kBatch) {
+      float v[kBatch][E];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i + k < n) {
+          const float* o = a.ws_o + slot(i + k) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(o));
+            v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(o));
+            v[k][0] = t.x, v[k][1] = t.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float ws = __shfl_sync(0xffffffffu, w, (i + k - s0) & 31);  // (0 from n on)
+        if (i + k < n) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, v[k][e], acc[e]);
+        }
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int j = row / a.n_rep, i = row - j * a.n_rep;
+  const size_t out_row = (static_cast<size_t>(b) * a.N + j) * a.Hq + g * a.n_rep + i;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+template <int D, int NQ, bool PAGED>
+cudaError_t launch_attn(const TreeArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  using C = Cfg<D, NQ, PAGED>;
+  static int done[64] = {0};
+  auto kern = tree_attn_kernel<D, NQ, PAGED>;
+  cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(a.ranges) * a.row_ctas), dim3(C::kThreads), C::kSmemBytes, st, km, vm, a);
+  if (e != cudaSuccess || a.ranges == 1) return e;
+  const int headers = a.headers_by_unit ? a.B * a.Hkv : a.ranges;
+  return launch_pdl(tree_merge_kernel<D>, dim3(headers, (a.rows + kMergeWarps - 1) / kMergeWarps), dim3(32 * kMergeWarps), 0,
+                    st, a);
+}
+
+}  // namespace tree
+}  // namespace rra

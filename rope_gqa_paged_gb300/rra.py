@@ -18,7 +18,7 @@ from . import _build
 
 RRA_F32, RRA_BF16 = 0, 1
 RRA_ERR_POSITION, RRA_ERR_BLOCK_ID, RRA_ERR_SEQ_LEN, RRA_ERR_TIMEOUT, RRA_ERR_WORKSPACE = 1, 2, 4, 8, 16
-RRA_ERR_TOKEN, RRA_ERR_PROBS = 32, 64
+RRA_ERR_TOKEN, RRA_ERR_PROBS, RRA_ERR_TREE = 32, 64, 128
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -83,6 +83,12 @@ _SIGNATURES = {
     "rra_accept_draft": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
     "rra_shared_prefix_plan": (_c_int, [_c_int] * 10 + [_vp, _vp, _vp]),
+    "rra_tree_append": (_c_int, [_vp] * 10 + [_c_int] * 9 + [_c_f64, _c_int, _vp, _vp]),
+    "rra_tree_attn": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int,
+                               _c_int, _c_int, _c_int, _c_f32, _c_int, _vp, _c_size, _vp, _vp]),
+    "rra_tree_step": (_c_int, [_vp] * 10 + [_c_int] * 4 + [_vp] + [_c_int] * 5 + [_c_f64, _c_int, _c_f32, _c_int, _vp,
+                                                                                _c_size, _vp, _vp]),
+    "rra_tree_plan": (_c_int, [_c_int] * 5 + [_c_i64, _c_int, _c_int, _vp, _vp]),
 }
 
 
@@ -611,3 +617,83 @@ def rra_prefill_step(q, k_new, v_new, positions, q_out, k_cache, v_cache, out, b
                                 _ptr(v_cache), _ptr(block_table), mbps, bs, nblk, max_len, _ptr(out), B, T, Hq, Hkv, D,
                                 float(rope_base), int(rope_style), float(scale), _ptr(err_flag), _stream(stream, q))
     _check("rra_prefill_step", st)
+
+
+# --------------------------------------------------------------------------- trees of drafted tokens
+def _tree_layout(q, k_cache, v_cache, positions, parents, block_table, tree_lens, out):
+    """(B, N, Hq, D, block-table columns, block_size, num_blocks, max_len, Hkv) of a tree call. The C calls take no
+    element types, so they are checked here, with the shapes."""
+    if q.dim() != 4:
+        raise ValueError("q: [B, N, Hq, D]")
+    B, N, Hq, D = q.shape
+    if not (q.dtype == k_cache.dtype == v_cache.dtype == out.dtype == _BF16):
+        raise TypeError("tree attention takes bf16 queries, caches and outputs")
+    if out.shape != q.shape or k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
+        raise ValueError("out: the shape of q; k_cache, v_cache: [B, Hkv, max_len, D], or [num_blocks, block_size, Hkv, D]")
+    if block_table is None and k_cache.shape[0] != B:
+        raise ValueError("k_cache, v_cache: a row per sequence")
+    if block_table is not None and (block_table.dtype != _I32 or block_table.dim() != 2 or block_table.shape[0] != B):
+        raise ValueError("block_table: int32 [B, max_blocks_per_seq]")
+    for t, shape, what in ((positions, (B,), "positions"), (parents, (B, N), "parents"), (tree_lens, (B,), "tree_lens")):
+        if t is not None and (t.dtype != _I32 or t.shape != shape):
+            raise ValueError(f"{what}: an int32 tensor of shape {shape}")
+    return (B, N, Hq, D) + _cache_layout(k_cache, block_table)
+
+
+def rra_tree_plan(B: int, N: int, Hq: int, Hkv: int, D: int, max_tokens: int, block_size: int,
+                  num_splits: int = 0) -> tuple:
+    """(runs the batch's keys are cut into at most, workspace bytes) of the tree attention."""
+    splits, ws = ctypes.c_int(), ctypes.c_size_t()
+    _check("rra_tree_plan", lib().rra_tree_plan(B, N, Hq, Hkv, D, max_tokens, block_size, num_splits,
+                                                ctypes.byref(splits), ctypes.byref(ws)))
+    return splits.value, ws.value
+
+
+def rra_tree_append(q, k_new, v_new, positions, parents, q_out, k_cache, v_cache, block_table=None, tree_lens=None,
+                    rope_base: float = 10000.0, rope_style: int = 0, err_flag=None, stream=None) -> None:
+    """RoPE on q / k_new [B, N, H, D] (node j at positions[b] + its depth) and append of the nodes (node j in slot
+    positions[b] + j). parents [B, N]: the node that node j follows, -1: the last cached token."""
+    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q, k_cache, v_cache, positions, parents, block_table,
+                                                             tree_lens, q_out)
+    _tree_nodes(q, k_new, v_new, Hkv)
+    st = lib().rra_tree_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(parents), _ptr(tree_lens),
+                               _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, bs, nblk, max_len, B,
+                               N, Hq, Hkv, D, rope_base, rope_style, _ptr(err_flag), _stream(stream, q))
+    _check("rra_tree_append", st)
+
+
+def _tree_nodes(q, k_new, v_new, Hkv: int) -> None:
+    if not k_new.dtype == v_new.dtype == _BF16:
+        raise TypeError("tree attention takes bf16 nodes")
+    shape = (q.shape[0], q.shape[1], Hkv, q.shape[3])
+    if k_new.shape != shape or v_new.shape != shape:
+        raise ValueError("k_new and v_new: [B, N, Hkv, D]")
+
+
+def rra_tree_attn(q_rot, k_cache, v_cache, positions, parents, out, block_table=None, tree_lens=None,
+                  scale: float = 0.0, num_splits: int = 0, workspace=None, err_flag=None, stream=None) -> None:
+    """out[b, j] = attention of q_rot[b, j] over tokens [0, positions[b]), node j's ancestors and node j itself
+    (bf16 caches that hold the nodes already)."""
+    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q_rot, k_cache, v_cache, positions, parents, block_table,
+                                                             tree_lens, out)
+    st = lib().rra_tree_attn(_ptr(q_rot), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, _ptr(positions),
+                             _ptr(parents), _ptr(tree_lens), bs, nblk, max_len, _ptr(out), B, N, Hq, Hkv, D, scale,
+                             num_splits, _ptr(workspace), workspace.nbytes if workspace is not None else 0,
+                             _ptr(err_flag), _stream(stream, q_rot))
+    _check("rra_tree_attn", st)
+
+
+def rra_tree_step(q, k_new, v_new, positions, parents, q_out, k_cache, v_cache, out, block_table=None, tree_lens=None,
+                  rope_base: float = 10000.0, rope_style: int = 0, scale: float = 0.0, num_splits: int = 0,
+                  workspace=None, err_flag=None, stream=None) -> None:
+    """The whole step on a tree of drafted tokens: RoPE + append of its nodes, then their attention."""
+    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q, k_cache, v_cache, positions, parents, block_table,
+                                                             tree_lens, out)
+    _tree_nodes(q, k_new, v_new, Hkv)
+    if q_out.shape != q.shape or q_out.dtype != _BF16:
+        raise ValueError("q_out: bf16, the shape of q")
+    st = lib().rra_tree_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(parents), _ptr(tree_lens),
+                             _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, bs, nblk, max_len,
+                             _ptr(out), B, N, Hq, Hkv, D, rope_base, rope_style, scale, num_splits, _ptr(workspace),
+                             workspace.nbytes if workspace is not None else 0, _ptr(err_flag), _stream(stream, q))
+    _check("rra_tree_step", st)

@@ -83,18 +83,24 @@ class DecodeStep:
         ``before()`` / ``after()`` record work around every repetition into the same graph,
         e.g. the copy of the step's inputs from pinned host memory and of its output back.
         """
+        def step():
+            self(q, k_new, v_new, positions, seq_lens)
+
+        return self._capture(step, q.device, repeat, between, before, after)
+
+    def _capture(self, step, device, repeat, between, before, after):
         def one():
             if before is not None:
                 before()
-            self(q, k_new, v_new, positions, seq_lens)
+            step()
             if after is not None:
                 after()
 
-        side = torch.cuda.Stream(device=q.device)
-        side.wait_stream(torch.cuda.current_stream(q.device))
+        side = torch.cuda.Stream(device=device)
+        side.wait_stream(torch.cuda.current_stream(device))
         with torch.cuda.stream(side):
             one()
-        torch.cuda.current_stream(q.device).wait_stream(side)
+        torch.cuda.current_stream(device).wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             for i in range(repeat):
@@ -282,6 +288,66 @@ class SharedPrefixStep(VerifyStep):
             return self.fused(q, k_new, v_new, positions, stream)
         self.rope_append(q, k_new, v_new, positions, stream)
         return self.attend(seq_lens, stream)
+
+
+class TreeStep(DecodeStep):
+    """The step on a tree of drafted tokens: ``nodes`` nodes per sequence, each attending the cached tokens, its
+    ancestors and itself.
+
+    q / k_new / v_new are [B, nodes, H, D]; ``positions[b]`` is the number of cached tokens, ``parents`` [B, nodes]
+    the node that each node follows (an earlier one; -1: the last cached token), and ``tree_lens`` [B] the
+    nodes of each sequence where they are not all of them (0: a padding row). Node j goes into slot positions[b] + j
+    and is rotated for position positions[b] + its depth. The output is [B, nodes, Hq, D], zero past a sequence's
+    nodes. Caches as for VerifyStep (bf16). ``rra_tree_keep`` then moves the accepted path together.
+    """
+
+    def __init__(self, batch: int, nodes: int, n_q_heads: int, n_kv_heads: int, head_dim: int, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, block_table: Optional[torch.Tensor] = None, num_splits: int = 0,
+                 rope_base: float = 10000.0, rope_style: int = 0, scale: float = 0.0):
+        self.B, self.nodes, self.Hq, self.Hkv, self.D = batch, nodes, n_q_heads, n_kv_heads, head_dim
+        self.k_cache, self.v_cache, self.block_table = k_cache, v_cache, block_table
+        self.rope_base, self.rope_style, self.scale = rope_base, rope_style, scale
+        self.dtype, dev = k_cache.dtype, k_cache.device
+        if block_table is not None:
+            bs = k_cache.shape[1]
+            max_tokens = block_table.shape[1] * bs
+        else:
+            bs, max_tokens = 0, k_cache.shape[2]
+        rra.use_device_of(k_cache)  # the plan depends on the device's SM count
+        self.num_splits = num_splits
+        self.splits, ws = rra.rra_tree_plan(batch, nodes, n_q_heads, n_kv_heads, head_dim, max_tokens, bs, num_splits)
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
+        self.q_rot = torch.empty(batch, nodes, n_q_heads, head_dim, dtype=self.dtype, device=dev)
+        self.out = torch.empty(batch, nodes, n_q_heads, head_dim, dtype=self.dtype, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.graph = None
+
+    def rope_append(self, q, k_new, v_new, positions, parents, tree_lens=None, stream=None) -> None:
+        rra.rra_tree_append(q, k_new, v_new, positions, parents, self.q_rot, self.k_cache, self.v_cache,
+                            self.block_table, tree_lens, self.rope_base, self.rope_style, self.err, stream)
+
+    def attend(self, positions, parents, tree_lens=None, stream=None) -> torch.Tensor:
+        """Attention of the already-appended nodes."""
+        rra.rra_tree_attn(self.q_rot, self.k_cache, self.v_cache, positions, parents, self.out, self.block_table,
+                          tree_lens, self.scale, self.num_splits, self.workspace, self.err, stream)
+        return self.out
+
+    def fused(self, q, k_new, v_new, positions, parents, tree_lens=None, stream=None) -> torch.Tensor:
+        rra.rra_tree_step(q, k_new, v_new, positions, parents, self.q_rot, self.k_cache, self.v_cache, self.out,
+                          self.block_table, tree_lens, self.rope_base, self.rope_style, self.scale, self.num_splits,
+                          self.workspace, self.err, stream)
+        return self.out
+
+    def __call__(self, q, k_new, v_new, positions, parents, tree_lens=None, stream=None) -> torch.Tensor:
+        return self.fused(q, k_new, v_new, positions, parents, tree_lens, stream)
+
+    def capture(self, q, k_new, v_new, positions, parents, tree_lens=None, repeat: int = 1, between=None, before=None,
+                after=None):
+        """``DecodeStep.capture`` for a tree: the graph is bound to these input tensors, parents and lengths too."""
+        def step():
+            self.fused(q, k_new, v_new, positions, parents, tree_lens)
+
+        return self._capture(step, q.device, repeat, between, before, after)
 
 
 class PrefillStep(VerifyStep):
