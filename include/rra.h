@@ -498,6 +498,52 @@ RRA_API int rra_tree_step(const void* q, const void* k_new, const void* v_new, c
 RRA_API int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int block_size, int num_splits,
                           int* splits, size_t* workspace_bytes);
 
+/* The path of the tree that the target keeps, and its tokens moved together in the caches.
+ *
+ * choices[b, j] is the token that the target chose after node j (the most likely one, or one drawn from its distribution: then
+ * the kept tokens follow that distribution). The path starts at node 0 (the last token that is not cached yet, always kept)
+ * and goes on from node x to its lowest child whose draft token is choices[b, x], as long as there is one. With m nodes kept:
+ *   tokens_out     int32 [B, N]: the m chosen tokens after them (those of the kept children, and one more), then -1
+ *   n_kept         int32 [B]: m (0 for a padding row)
+ *   nodes_out      int32 [B, N]: the kept nodes in order, then -1
+ *   positions_out  int32 [B]: positions[b] + m, the cached tokens of the next step, whose node 0 is the last of tokens_out
+ * and in every layer's cache the keys and values of the i-th kept node move from slot p_b + node to p_b + i (where they are
+ * rotated for already). Other slots keep what they hold.
+ *
+ *   draft_tokens, parents  int32 [B, N]; choices int32 [B, N], consecutive ones choice_stride elements apart (so that one column of
+ *                 rra_token_logprobs' top_tokens will do). A choice below 0 matches no child.
+ *   k_caches, v_caches  HOST arrays of n_layers (0..128) device pointers: caches of element type dt (bf16 or fp32), all laid
+ *                 out alike (paged pools of any power of two, or contiguous) under one block table
+ * tree_lens, positions, parents and their error bits as in rra_tree_append; a sequence with RRA_ERR_POSITION has its path
+ * written, positions_out = positions and nothing moved; a row whose slot has a block id outside the pool does not
+ * move (RRA_ERR_BLOCK_ID). No output may lie over another one or over an input (RRA_EINVAL). N is 1..128. */
+RRA_API int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents, const int32_t* choices,
+                          int64_t choice_stride, const int32_t* tree_lens, const int32_t* positions,
+                          void* const* k_caches, void* const* v_caches, int n_layers, const int32_t* block_table,
+                          int max_blocks_per_seq, int block_size, int num_blocks, int max_len, int32_t* tokens_out,
+                          int32_t* n_kept, int32_t* nodes_out, int32_t* positions_out, int B, int N, int Hkv, int D,
+                          rra_dtype dt, int32_t* err_flag, void* stream);
+
+/* --- Log probabilities of tokens ---
+ *
+ * For every row of logits x (V values): log p(v) = x_v - ln sum e^x of given tokens, the entropy -sum p ln p (natural
+ * logarithms) and the top_k most likely tokens in order, of equal logits the lower index first.
+ *
+ *   logits        dt (bf16 or fp32) [B, N, V]: V consecutive values per row, rows `stride_t` and sequences `stride_b` elements
+ *                 apart (>= 0, any alignment of the element type). -inf: a token that is ruled out (log probability
+ *                 -inf, nothing added to the entropy). A row with a NaN or +inf, or with nothing but -inf, has no distribution:
+ *                 RRA_ERR_PROBS, its results NaN and its top tokens -1.
+ *   tokens        int32 [B, N, T], T 0..32 (NULL for 0); -1: no token, log probability 0; other values outside [0, V):
+ *                 RRA_ERR_TOKEN and NaN
+ *   logprobs      float32 [B, N, T]
+ *   entropy       float32 [B, N], may be NULL
+ *   top_logprobs, top_tokens  float32 and int32 [B, N, top_k], top_k 0..32 and at most V (NULL for 0)
+ * Sums are float32 over parts of a row of a few hundred to a few thousand values, joined in a fixed order. V is at most 2^30. No
+ * output may lie over another one or over the tokens (RRA_EINVAL), nor over the logits. */
+RRA_API int rra_token_logprobs(const void* logits, int64_t stride_b, int64_t stride_t, const int32_t* tokens, int T,
+                               float* logprobs, float* entropy, int top_k, float* top_logprobs, int32_t* top_tokens,
+                               int B, int N, int V, rra_dtype dt, int32_t* err_flag, void* stream);
+
 /* Bytes of a K+V cache: 2 * n_layers * n_kv_heads * head_dim * seq_len * batch * dtype_bytes
  * ([Opt-2026] §四 memory formula; [KVC-GQA-RoPE] §5.3). Host only; returns 0 when an
  * argument is negative or the product overflows 64 bits. */

@@ -89,6 +89,10 @@ _SIGNATURES = {
     "rra_tree_step": (_c_int, [_vp] * 10 + [_c_int] * 4 + [_vp] + [_c_int] * 5 + [_c_f64, _c_int, _c_f32, _c_int, _vp,
                                                                                 _c_size, _vp, _vp]),
     "rra_tree_plan": (_c_int, [_c_int] * 5 + [_c_i64, _c_int, _c_int, _vp, _vp]),
+    "rra_tree_keep": (_c_int, [_vp, _vp, _vp, _c_i64] + [_vp] * 4 + [_c_int, _vp] + [_c_int] * 4 + [_vp] * 4 +
+                      [_c_int] * 5 + [_vp, _vp]),
+    "rra_token_logprobs": (_c_int, [_vp, _c_i64, _c_i64, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                    _c_int, _vp, _vp]),
 }
 
 
@@ -697,3 +701,107 @@ def rra_tree_step(q, k_new, v_new, positions, parents, q_out, k_cache, v_cache, 
                              _ptr(out), B, N, Hq, Hkv, D, rope_base, rope_style, scale, num_splits, _ptr(workspace),
                              workspace.nbytes if workspace is not None else 0, _ptr(err_flag), _stream(stream, q))
     _check("rra_tree_step", st)
+
+
+def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches, block_table=None, tree_lens=None,
+                  tokens_out=None, n_kept=None, nodes_out=None, positions_out=None, err_flag=None, stream=None) -> tuple:
+    """(tokens [B, N], kept [B], nodes [B, N], next positions [B]): the path of drafted nodes that the target's
+    ``choices`` [B, N] follow from node 0, then -1; its keys and values move together in the caches.
+
+    k_caches / v_caches: the caches of every layer (lists of tensors alike, or one tensor each), bf16 or fp32,
+    contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
+    Outputs are made where they are not given.
+    """
+    ids = draft_tokens.shape
+    B, N = ids
+    k_caches = [k_caches] if isinstance(k_caches, torch.Tensor) else k_caches
+    v_caches = [v_caches] if isinstance(v_caches, torch.Tensor) else v_caches
+    layers = len(k_caches)
+    if layers == 0 or len(v_caches) != layers:
+        raise ValueError("k_caches, v_caches: the caches of each layer")
+    k0 = k_caches[0]
+    shape, dtype, device = k0.shape, k0.dtype, draft_tokens.device
+    code = _dtype_code(k0)
+    pointers = (_vp * layers)(), (_vp * layers)()
+    for at, caches in zip(pointers, (k_caches, v_caches)):
+        for i, c in enumerate(caches):
+            if c.shape != shape or c.dtype != dtype or not c.is_contiguous() or c.device != device:
+                raise ValueError("the layers' caches: contiguous tensors alike, on the tokens' device")
+            at[i] = c.data_ptr()
+    if len(shape) != 4 or (block_table is None and shape[0] != B):
+        raise ValueError("caches: [B, Hkv, max_len, D], or [num_blocks, block_size, Hkv, D] with a block table")
+    if block_table is not None and (block_table.dtype != _I32 or block_table.dim() != 2 or block_table.shape[0] != B):
+        raise ValueError("block_table: int32 [B, max_blocks_per_seq]")
+    mbps, bs, nblk, max_len, Hkv = _cache_layout(k0, block_table)
+    if choices.dtype != _I32 or choices.shape != ids or not choices.is_cuda:
+        raise ValueError("choices: an int32 CUDA tensor of draft_tokens' shape")
+    step = choices.stride(1) if N > 1 else max(1, choices.stride(0))
+    if B > 1 and choices.stride(0) != N * step:
+        choices, step = choices.contiguous(), 1
+    row = (B,)
+
+    def output(t, shape, what):
+        if t is None:
+            t = torch.empty(shape, dtype=_I32, device=device)
+            return t, t.data_ptr()
+        return t, _i32(t, shape, what)
+
+    tokens_out, tokens_ptr = output(tokens_out, ids, "tokens_out")
+    n_kept, kept_ptr = output(n_kept, row, "n_kept")
+    nodes_out, nodes_ptr = output(nodes_out, ids, "nodes_out")
+    positions_out, next_ptr = output(positions_out, row, "positions_out")
+    st = lib().rra_tree_keep(_i32(draft_tokens, ids, "draft_tokens"), _i32(parents, ids, "parents"), choices.data_ptr(), step,
+                             _i32(tree_lens, row, "tree_lens") if tree_lens is not None else None,
+                             _i32(positions, row, "positions"), pointers[0], pointers[1], layers, _ptr(block_table), mbps,
+                             bs, nblk, max_len, tokens_ptr, kept_ptr, nodes_ptr, next_ptr, B, N, Hkv, shape[3], code,
+                             _ptr(err_flag), _stream(stream, draft_tokens))
+    _check("rra_tree_keep", st)
+    return tokens_out, n_kept, nodes_out, positions_out
+
+
+# --------------------------------------------------------------------------- log probabilities of tokens
+def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=None, top_logprobs=None,
+                       top_tokens=None, err_flag=None, stream=None) -> tuple:
+    """(log probabilities of ``tokens``, entropies, log probabilities of the top_k most likely tokens, these tokens)
+    of logits [..., V] (bf16 or fp32, one or two dimensions of rows, a unit last stride).
+
+    ``tokens``: int32, one per row ([...]) or several ([..., T]); -1: no token, 0. The results are float32 and
+    int32 tensors of the shapes [...] or [..., T], [...], [..., top_k] and [..., top_k], made where they are not given; without
+    ``tokens`` the first is None, without ``top_k`` the last two are.
+    """
+    rows, V = logits.shape[:-1], logits.shape[-1]
+    if len(rows) == 1:
+        (B,), N, sb, st_ = rows, 1, logits.stride(0), 0
+    elif len(rows) == 2:
+        (B, N), sb, st_ = rows, logits.stride(0), logits.stride(1)
+    else:
+        raise ValueError("logits: [rows, V] or [B, N, V]")
+    code = _dtype_code(logits)
+    if not logits.is_cuda or (logits.stride(-1) != 1 and V > 1):
+        raise ValueError("logits: a CUDA tensor with a unit last stride")
+    T, device = 0, logits.device
+    if tokens is not None:
+        if tokens.shape[:len(rows)] != rows or tokens.dim() > len(rows) + 1:
+            raise ValueError("tokens: [...] or [..., T] for logits [..., V]")
+        T = tokens.shape[-1] if tokens.dim() > len(rows) else 1
+
+    def output(t, shape, dtype, what):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=device)
+            return t, t.data_ptr()
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{what}: a {dtype} tensor of shape {tuple(shape)}")
+        return t, _ptr(t)
+
+    lp_ptr = top_lp_ptr = top_ptr = None
+    if tokens is not None:
+        logprobs, lp_ptr = output(logprobs, tokens.shape, _F32, "logprobs")
+    entropy, h_ptr = output(entropy, rows, _F32, "entropy")
+    if top_k > 0:
+        top_logprobs, top_lp_ptr = output(top_logprobs, rows + (top_k,), _F32, "top_logprobs")
+        top_tokens, top_ptr = output(top_tokens, rows + (top_k,), _I32, "top_tokens")
+    st = lib().rra_token_logprobs(logits.data_ptr(), sb, st_,
+                                  _i32(tokens, tokens.shape, "tokens") if tokens is not None else None, T, lp_ptr, h_ptr,
+                                  top_k, top_lp_ptr, top_ptr, B, N, V, code, _ptr(err_flag), _stream(stream, logits))
+    _check("rra_token_logprobs", st)
+    return logprobs, entropy, top_logprobs, top_tokens

@@ -138,3 +138,71 @@ def test_binding_refusals(rra):
             step(**kw)
     with pytest.raises(ValueError):  # (a CPU tensor)
         step()
+
+
+KEEP_AT = {n: (i + 1) << 30 for i, n in
+           enumerate("tokens parents choices lens positions table tokens_out kept nodes_out next".split())}
+
+
+def _keep(rra, layers=2, caches=None, **kw):
+    a = {**KEEP_AT, **SIZES, "stride": 1, "B": 4, "N": 16, "Hkv": 8, "D": 128, "dt": 1, **kw}
+    arrays = [(ctypes.c_void_p * max(layers, 1))(*(caches or [1 << 40] * layers)) for _ in range(2)]
+    return rra.lib().rra_tree_keep(a["tokens"], a["parents"], a["choices"], a["stride"], a["lens"], a["positions"], arrays[0],
+                                   arrays[1], layers, a["table"], a["mbps"], a["bs"], a["nblk"], a["max_len"],
+                                   a["tokens_out"], a["kept"], a["nodes_out"], a["next"], a["B"], a["N"], a["Hkv"], a["D"],
+                                   a["dt"], None, None)
+
+
+@host_only
+def test_keep_refusals(rra):
+    n = 4 * 16 * 4
+    for kw, st in ((dict(N=0), RRA_EINVAL), (dict(N=129), RRA_EUNSUPPORTED), (dict(D=32), RRA_EUNSUPPORTED),
+                   (dict(dt=2), RRA_EUNSUPPORTED), (dict(layers=129), RRA_EUNSUPPORTED), (dict(layers=-1), RRA_EINVAL),
+                   (dict(bs=24), RRA_EUNSUPPORTED), (dict(bs=0), RRA_EINVAL), (dict(nblk=0), RRA_EINVAL), (dict(B=-1), RRA_EINVAL),
+                   (dict(B=65536), RRA_ERANGE), (dict(table=None, max_len=0), RRA_EINVAL), (dict(mbps=1 << 30), RRA_ERANGE),
+                   (dict(stride=-1), RRA_EINVAL), (dict(tokens=None), RRA_EINVAL), (dict(choices=None), RRA_EINVAL),
+                   (dict(positions=None), RRA_EINVAL), (dict(kept=None), RRA_EINVAL), (dict(nodes_out=None), RRA_EINVAL),
+                   (dict(caches=[1 << 40, None]), RRA_EINVAL), (dict(caches=[1 << 40, (1 << 40) + 8]), RRA_EINVAL),
+                   (dict(next=KEEP_AT["positions"]), RRA_EINVAL), (dict(tokens_out=KEEP_AT["tokens"]), RRA_EINVAL),
+                   (dict(tokens_out=KEEP_AT["choices"] + 5 * n, stride=7), RRA_EINVAL),
+                   (dict(nodes_out=KEEP_AT["tokens_out"] + n - 4), RRA_EINVAL), (dict(kept=KEEP_AT["lens"]), RRA_EINVAL)):
+        assert _keep(rra, **kw) == st, kw
+    assert _keep(rra, B=0) == RRA_OK
+
+
+LP_AT = {n: (i + 1) << 40 for i, n in enumerate("logits tokens logprobs entropy top_lp top".split())}
+
+
+def _logprobs(rra, **kw):
+    a = {**LP_AT, "sb": 16000, "st": 1000, "T": 2, "k": 5, "B": 4, "N": 16, "V": 1000, "dt": 1, **kw}
+    return rra.lib().rra_token_logprobs(*[a[k] for k in "logits sb st tokens T logprobs entropy k top_lp top B N V dt".split()],
+                                        None, None)
+
+
+@host_only
+def test_logprobs_refusals(rra):
+    rows = 4 * 16 * 4
+    for kw, st in ((dict(dt=3), RRA_EUNSUPPORTED), (dict(T=33), RRA_EUNSUPPORTED), (dict(k=33), RRA_EUNSUPPORTED),
+                   (dict(k=4, V=3), RRA_EINVAL), (dict(k=-1), RRA_EINVAL), (dict(T=-1), RRA_EINVAL), (dict(V=0), RRA_EINVAL),
+                   (dict(V=(1 << 30) + 1), RRA_ERANGE), (dict(B=-1), RRA_EINVAL), (dict(N=0), RRA_EINVAL),
+                   (dict(B=1 << 20, N=1 << 12), RRA_ERANGE), (dict(logits=None), RRA_EINVAL), (dict(tokens=None), RRA_EINVAL),
+                   (dict(logprobs=None), RRA_EINVAL), (dict(top=None), RRA_EINVAL), (dict(top_lp=None), RRA_EINVAL),
+                   (dict(logits=LP_AT["logits"] + 1), RRA_EINVAL), (dict(logits=LP_AT["logits"] + 2, dt=0), RRA_EINVAL),
+                   (dict(sb=-1), RRA_EINVAL), (dict(st=-5), RRA_EINVAL), (dict(entropy=LP_AT["tokens"] + 4), RRA_EINVAL),
+                   (dict(top=LP_AT["top_lp"] + 5 * rows - 4), RRA_EINVAL), (dict(logprobs=LP_AT["entropy"]), RRA_EINVAL)):
+        assert _logprobs(rra, **kw) == st, kw
+    assert _logprobs(rra, B=0) == RRA_OK
+
+
+def test_binding_refusals_of_the_others(rra):
+    x, tok = torch.zeros(4, 100), torch.zeros(4, 2, dtype=torch.int32)
+    for kw in (dict(logits=x), dict(logits=x[0]), dict(logits=x[None, None]), dict(logits=x.half())):
+        with pytest.raises((ValueError, TypeError)):
+            rra.rra_token_logprobs(**{"tokens": tok, **kw})
+    ids, pos, k = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 8, 64)
+    for kw in (dict(k_caches=[]), dict(v_caches=[k, k]), dict(k_caches=[k[:1]]), dict(choices=ids.long()),
+               dict(v_caches=[k.bfloat16()]), dict(block_table=ids.long()), dict()):
+        a = dict(draft_tokens=ids, parents=ids, choices=ids, positions=pos, k_caches=[k], v_caches=[k])
+        a.update(kw)
+        with pytest.raises(ValueError):
+            rra.rra_tree_keep(**a)
