@@ -21,6 +21,7 @@
 // bf16 first, then quantised with its KV head's scale into the cache slot; with a window the
 // bf16 values also go to slot pos % window of the sequence's ring.
 #include <cmath>
+#include <cstring>
 
 #include "rra_device.cuh"
 #include "rra_internal.h"
@@ -443,7 +444,7 @@ cudaError_t launch_rope_append_q8(const RopeArgs& a, cudaStream_t stream) {
 // theta_i / 2pi for i < D/2, theta_i = base^(-2i/D) in float64, as a 96-bit binary fraction
 // (least significant 32-bit word first), exact up to truncation (< 2^-96): theta = m 2^(e-53) with
 // an integer m < 2^53, times floor(2^127 / pi) (2^128 / 2pi, a 128-bit integer), shifted down.
-void fill_rope_phi(uint32_t (*phi)[3], int D, double base) {
+static void make_rope_phi(uint32_t (*phi)[3], int D, double base) {
   // floor(2^127 / pi), computed at 400-bit precision
   constexpr uint64_t kHi = 0x28be60db9391054aULL, kLo = 0x7f09d5f47d4d3770ULL;
   using u128 = unsigned __int128;
@@ -471,6 +472,23 @@ void fill_rope_phi(uint32_t (*phi)[3], int D, double base) {
     phi[i][1] = static_cast<uint32_t>(out[0] >> 32);
     phi[i][2] = static_cast<uint32_t>(out[1]);
   }
+}
+
+// The last table is kept per thread: a model's calls ask for the same one every time (64 pow calls and wide products, 2.5 us
+// of a call on the host).
+void fill_rope_phi(uint32_t (*phi)[3], int D, double base) {
+  static thread_local struct {
+    int D = 0;
+    double base = 0.0;
+    uint32_t phi[kMaxHeadDim / 2][3];
+  } last;
+  if (D > kMaxHeadDim) return make_rope_phi(phi, D, base);
+  if (last.D != D || !(last.base == base)) {
+    make_rope_phi(last.phi, D, base);
+    last.D = D;
+    last.base = base;
+  }
+  std::memcpy(phi, last.phi, sizeof(last.phi[0]) * (D / 2));
 }
 
 namespace {

@@ -3,6 +3,7 @@
 // Nothing here allocates device memory; every buffer belongs to the caller.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -420,7 +421,7 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
   const int tile = rra::tree_tile(D, p->nq);
   const int64_t tiles = int64_t(B) * Hkv * ((max_tokens + tile - 1) / tile);
-  if (tiles > (int64_t(1) << 40)) return RRA_ERANGE;
+  if (tiles > INT32_MAX) return RRA_ERANGE;
   if (requested > 0) {
     p->ranges = std::min(requested, rra::kMaxSplits);
   } else {
@@ -428,7 +429,7 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
     p->ranges = std::max(1, (p->nq == 2 ? 1 : 2) * sms / p->row_ctas);
     p->min_tiles = 256 / tile;
   }
-  p->ranges = static_cast<int>(std::min<int64_t>(p->ranges, std::max<int64_t>(1, (tiles + p->min_tiles - 1) / p->min_tiles)));
+  p->ranges = static_cast<int>(std::min<int64_t>(p->ranges, std::max<int64_t>({1, (tiles + p->min_tiles - 1) / p->min_tiles, int64_t(B) * Hkv})));
   return RRA_OK;
 }
 

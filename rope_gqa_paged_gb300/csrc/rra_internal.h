@@ -232,7 +232,7 @@ struct TreeArgs {
   int ranges, min_tiles;        // runs of key tiles, the least tiles of one
   float* ws_o;                  // [ranges, 2, rows, D] unnormalised partial outputs (ranges > 1)
   float* ws_ml;                 // [ranges, 2, rows, 2] (running max in log2 units, running sum)
-  int4* headers;                // what tree_merge_kernel joins: (partials, first range, sequence, KV head), 0 partials: nothing
+  int4* headers;                // what tree_merge_kernel joins: (partials, first range, unit, live rows), 0 partials: nothing
   int headers_by_unit;          // one per (sequence, KV head), otherwise one per range
   float scale_log2;
   int after_append;             // the kernel before this one is the append of the same call

@@ -33,7 +33,11 @@ constexpr int kMaxCluster = 16;
 constexpr int kMaxTop = 32;
 constexpr int kMaxTokens = 32;   // given tokens per row: a lane each
 constexpr int kBatch = 4;        // vectors in flight per thread
-constexpr int kMaxFound = 1024;  // values that reach T; more go the long way
+constexpr int kStageBytes = kThreads * kBatch * 16;
+constexpr int kRing = 2;         // batches of all threads on their way
+constexpr int kEntries = 16;     // batch maxima that a thread keeps, as bf16 (rounded up)
+constexpr int kMaxFound = 1024;  // values of a row that reach the bound; more of a CTA go the long way
+constexpr int kMaxKeys = 512;    // of a CTA that reach the bound there; more go the longest way
 
 struct LogprobArgs {
   const void* logits;            // [B, N, V] with these strides (elements)
@@ -54,6 +58,79 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x on the special-function 
   return y;
 }
 
+// Two float32 operations in one instruction, on pairs (lo, hi).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(lo)) | (static_cast<uint64_t>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ float lo2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi2(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t c) {
+  uint64_t z;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(x), "l"(y), "l"(c));
+  return z;
+}
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t z;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+  return z;
+}
+
+// What a type's vectors are worked on with: their maximum, and their values no lower than a bound.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);  // -inf
+  }
+  static __device__ __forceinline__ float max_of(const uint4& w, float m) {
+    return max_nan(max_nan(max_nan(m, __uint_as_float(w.x)), max_nan(__uint_as_float(w.y), __uint_as_float(w.z))),
+                   __uint_as_float(w.w));
+  }
+  static constexpr int kPairs = 2;
+  static __device__ __forceinline__ void clamped(const uint4& w, float bound, uint64_t (&x)[2]) {
+    x[0] = pack2(max_nan(__uint_as_float(w.x), bound), max_nan(__uint_as_float(w.y), bound));
+    x[1] = pack2(max_nan(__uint_as_float(w.z), bound), max_nan(__uint_as_float(w.w), bound));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
+  static __device__ __forceinline__ float max_of(const uint4& w, float m) {
+    const uint32_t x = max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w));
+    return max_nan(m, max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
+  }
+  static constexpr int kPairs = 4;
+  static __device__ __forceinline__ void clamped(const uint4& w, float bound, uint64_t (&x)[4]) {
+    const __nv_bfloat16 b = __float2bfloat16_rd(bound);
+    const uint32_t bb = static_cast<uint32_t>(__bfloat16_as_ushort(b)) * 0x10001u;
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = max_nan_bf16x2(v[i], bb);
+      x[i] = pack2(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
+    }
+  }
+};
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFar = -1000.f;  // a power of two that is 0, and no infinity to multiply 0 with
@@ -71,14 +148,6 @@ struct Stats {
     const float d = (x - (m == -INFINITY ? 0.f : m)) * kLog2e, e = ex2(d);
     s += e;
     u = fmaf(fmaxf(d, kFar), e, u);
-  }
-  __device__ __forceinline__ void join(const Stats& o) {
-    const float to = fmaxf(m, o.m);
-    Stats b = o;
-    move_to(to);
-    b.move_to(to);
-    s += b.s;
-    u += b.u;
   }
 };
 
@@ -114,81 +183,264 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t ran
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
   return addr;
 }
-__device__ __forceinline__ Key ld_cluster_key(uint32_t addr) {
-  Key v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, Key v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The warp's statistics together, the same in every lane (the sums are over pairs, so their order does not show).
+__device__ __forceinline__ Stats join_warp(Stats s) {
+  const uint32_t m = __reduce_max_sync(0xffffffffu, ordered(s.m));  // (a NaN counts as the largest)
+  s.move_to(__uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    s.s += __shfl_xor_sync(0xffffffffu, s.s, d);
+    s.u += __shfl_xor_sync(0xffffffffu, s.u, d);
+  }
+  return s;
 }
 
 struct Shared {
-  Stats warp_stats[kWarps], stats;
-  Key held[kWarps * kMaxTop];     // the largest keys of each warp's threads
-  Key found[kMaxFound];
-  Key top[kMaxTop];               // this CTA's, sorted; 0 past the end
-  Key all[kMaxCluster * kMaxTop];
+  Stats stats[kMaxCluster * kWarps];              // of every CTA's warps (in the first CTA)
+  alignas(16) uint32_t groups[kThreads / 4];      // the largest values of groups of four threads
+  uint32_t bound;
+  Key top[kMaxTop];                               // this CTA's, sorted; 0 past the end
   Key best[kWarps];
-  int count;
+  uint64_t full[kRing], empty[kRing];
+  int counts[kMaxCluster];                        // keys that the CTAs found (in the first CTA)
+  int count, kept;
 };
 
-// A thread's part of the row: vectors v0 + threadIdx.x, + kThreads, ... below v1, whose first element is
-// head + E v, and at most one element in front of or behind the vectors.
+// Dynamic shared memory: the ring of vectors on their way in, the batch maxima, the keys found here and in all CTAs.
+constexpr int kOffMaxima = kRing * kStageBytes;
+constexpr int kOffFound = kOffMaxima + kEntries * kThreads * 2;
+constexpr int kOffAll = kOffFound + kMaxKeys * 8;  // (in the first CTA: kMaxFound / C places for each CTA)
+constexpr int kSmemBytes = kOffAll + kMaxFound * 8;
+static_assert(kCtasPerSm * (kSmemBytes + sizeof(Shared) + 1024) <= 228 * 1024, "shared memory of the SM");
+static_assert(kMaxFound >= kMaxCluster * kMaxTop, "every CTA's k largest fit");
+
+// A thread's part of the row: vectors v0 + thread, + kThreads, ... below v1, whose first element is head + E v, and at
+// most one element in front of or behind the vectors. kBatch of its vectors are a batch; `per_entry` batches share an
+// entry of the maxima. `in`: the vectors from v0 on, in shared memory where they all are still there.
 template <typename T>
 struct Part {
+  static constexpr int E = Elem<T>::kPerChunk;
   const T* row;
+  const uint4* in;
   int head, v0, v1, single;       // single: its index, -1: none
+  int per_entry;
   template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {  // f(value, index), indexes ascending but for the single one
-    constexpr int E = Elem<T>::kPerChunk;
-    const uint4* vec = reinterpret_cast<const uint4*>(row + head);
-    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads) {
-      float x[E];
-      Elem<T>::unpack(vec[v], x);
+  __device__ __forceinline__ void vector(int v, const uint4& w, F&& f) const {  // f(value, index)
+    float x[E];
+    Elem<T>::unpack(w, x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f(x[e], head + E * v + e);
-    }
-    if (single >= 0) f(Elem<T>::load(row + single), single);
+    for (int e = 0; e < E; ++e) f(x[e], head + E * v + e);
   }
+  // f of the values of entry e's vectors of this thread, but for vectors that hold nothing as large as `bound`.
+  template <typename F>
+  __device__ __forceinline__ void entry(int e, float bound, F&& f) const {
+    constexpr int kLoads = 2 * kBatch;
+    const int first = v0 + e * per_entry * kBatch * kThreads + static_cast<int>(threadIdx.x);
+    const int end = min(v1, first + per_entry * kBatch * kThreads);
+    for (int v = first; v < end; v += kLoads * kThreads) {
+      uint4 w[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) w[i] = v + i * kThreads < end ? in[v + i * kThreads - v0] : Vec<T>::none();
+      uint32_t hits = 0;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) hits |= !(Vec<T>::max_of(w[i], -INFINITY) < bound) && v + i * kThreads < end ? 1u << i : 0u;
+      for (; hits != 0; hits &= hits - 1) {
+        const int at = v + (__ffs(hits) - 1) * kThreads;
+        vector(at, in[at - v0], f);  // (read again: picked out of registers it takes more of them than there are)
+      }
+    }
+  }
+  __device__ __forceinline__ float single_value() const { return Elem<T>::load(row + single); }
 };
+
+// The barrier of the warps that read (the one that feeds the ring leaves by itself).
+__device__ __forceinline__ void sync_readers() { named_barrier_sync(1, kThreads); }
 
 // The CTA's k largest keys by taking the largest below the last one, k times.
 template <typename T>
-__device__ __noinline__ void top_slowly(const Part<T>& part, int k, Shared& sh) {
+__device__ __noinline__ void top_slowly(const Part<T> part, int k, Shared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Key last = ~Key(0);
   for (int r = 0; r < k; ++r) {
     Key mine = 0;
-    part.each([&](float x, int i) {
+    auto look = [&](float x, int i) {
       const Key key = make_key(x, i);
       if (key < last && key > mine) mine = key;
-    });
+    };
+    for (int e = 0; e < kEntries; ++e) part.entry(e, -INFINITY, look);
+    if (part.single >= 0) look(part.single_value(), part.single);
     mine = warp_max(mine);
     if (lane == 0) sh.best[warp] = mine;
-    __syncthreads();
+    sync_readers();
     last = 0;
     for (int w = 0; w < kWarps; ++w) last = max(last, sh.best[w]);
     if (threadIdx.x == 0) sh.top[r] = last;
-    __syncthreads();
+    sync_readers();
   }
 }
 
+// A bound that at least k of the values that the threads hold (0: none) reach, 0 if there are not k: the k-th largest
+// of the maxima of groups of four threads. (The k-th largest of all is no smaller; of values in no order about
+// 64 (1/64 + 1/63 + ... , k terms) reach it: 24 for k = 20.) Every thread ranks one maximum against a quarter of the
+// others.
+constexpr int kGroups = kThreads / 4;
+__device__ __forceinline__ uint32_t common_bound(uint32_t x, int k, Shared& sh) {
+  const int t = threadIdx.x;
+  x = max(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  x = max(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  if (t % 4 == 0) sh.groups[t / 4] = x;
+  sync_readers();
+  int larger = 0, as_large = 0;
+#pragma unroll
+  for (int j = 0; j < kGroups / 4; j += 4) {
+    const uint4 y = *reinterpret_cast<const uint4*>(&sh.groups[t % 4 * (kGroups / 4) + j]);
+    larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+    as_large += (y.x >= x) + (y.y >= x) + (y.z >= x) + (y.w >= x);
+  }
+  int both = larger | as_large << 16;
+  both += __shfl_xor_sync(0xffffffffu, both, 1);
+  both += __shfl_xor_sync(0xffffffffu, both, 2);
+  if ((both & 0xffff) < k && both >> 16 >= k) sh.bound = x;  // (equal ones write the same)
+  sync_readers();
+  return sh.bound;
+}
+
+// This CTA's k largest keys, sorted into sh.top, where too many values reach a bound on the value alone: equal ones (ruled out
+// tokens, a row of one value), or an order that puts large ones with few threads. First by a bound on keys, which
+// differ by their index.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(const LogprobArgs a) {
+__device__ __noinline__ void top_of_many(const Part<T> part, const __nv_bfloat16* maxima, float largest, bool some, int k, Key* found, Shared& sh) {
+  const int per_warp = min(kMaxTop, 2 * ((k + kWarps - 1) / kWarps));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
+  Key mine = 0;  // the thread's largest
+  for (int e = 0; some && e < kEntries; ++e) {
+    if (part.v0 + e * part.per_entry * kBatch * kThreads + t >= part.v1) break;
+    if (static_cast<uint32_t>(mine >> 32) == ordered(largest)) break;  // (the first entry that has it holds its lowest index)
+    if (ordered(__bfloat162float(maxima[e * kThreads + t])) >= ordered(largest))
+      part.entry(e, largest, [&](float x, int index) { mine = max(mine, make_key(x, index)); });
+  }
+  if (part.single >= 0) mine = max(mine, make_key(part.single_value(), part.single));
+  Key left = mine;
+  Key* held = found;  // the largest keys of each warp's threads
+  static_assert(kMaxKeys >= kWarps * kMaxTop, "they fit");
+  sync_readers();
+  for (int i = 0; i < per_warp; ++i) {
+    const Key top = warp_max(left);
+    if (lane == 0) held[warp * per_warp + i] = top;
+    if (left == top) left = 0;  // (keys differ, but for 0)
+  }
+  if (t == 0) sh.count = 0;
+  sync_readers();
+  Key bound = 0;
+  for (int i = lane; i < kWarps * per_warp; i += 32) {
+    int larger = 0;
+    for (int j = 0; j < kWarps * per_warp; ++j) larger += held[j] > held[i];
+    if (larger == k - 1) bound = held[i];
+  }
+  bound = warp_max(bound);
+  sync_readers();
+  auto put = [&](float x, int i) {
+    const Key key = make_key(x, i);
+    if (key >= bound) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kMaxKeys) found[at] = key;
+    }
+  };
+  if (mine != 0 && mine >= bound) {
+    for (int e = 0; some && e < kEntries && part.v0 + e * part.per_entry * kBatch * kThreads + t < part.v1; ++e)
+      if (ordered(__bfloat162float(maxima[e * kThreads + t])) >= static_cast<uint32_t>(bound >> 32)) part.entry(e, key_value(bound), put);
+    if (part.single >= 0) put(part.single_value(), part.single);
+  }
+  if (t < k) sh.top[t] = 0;
+  sync_readers();
+  const int n = sh.count;
+  if (n > kMaxKeys) {
+    top_slowly(part, k, sh);
+  } else {
+    for (int i = t; i < n; i += kThreads) {
+      const Key key = found[i];
+      int larger = 0;
+      for (int j = 0; j < n; ++j) larger += found[j] > key;
+      if (larger < k) sh.top[larger] = key;
+    }
+  }
+  sync_readers();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kernel(const LogprobArgs a) {
   constexpr int E = Elem<T>::kPerChunk;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
+  __nv_bfloat16* maxima = reinterpret_cast<__nv_bfloat16*>(smem + kOffMaxima);  // [kEntries][kThreads]
+  Key* found = reinterpret_cast<Key*>(smem + kOffFound);
+  Key* all = reinterpret_cast<Key*>(smem + kOffAll);
   const int64_t r = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;  // row b N + t
   if (r >= a.rows) return;  // (the whole cluster)
   const int C = gridDim.x, rank = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kWarps);
+    }
+    sh.count = sh.kept = 0;
+    sh.bound = 0;
+    fence_barrier_init();
+  }
+  cluster_arrive();  // (waited for before the first CTA's memory is written to)
   pdl_wait();
   pdl_launch_dependents();
   const int64_t b = r / a.N;
   const T* row = static_cast<const T*>(a.logits) + b * a.sb + (r - b * a.N) * a.st;
   const int V = a.V, k = a.top_k;
+
+  Part<T> part;
+  part.row = row;
+  part.head = min(V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
+  const uint4* vec = reinterpret_cast<const uint4*>(row + part.head);
+  const int vecs = (V - part.head) / E, tail = V - part.head - vecs * E;
+  const int per = (vecs + C - 1) / C;
+  part.v0 = min(rank * per, vecs);
+  part.v1 = min(part.v0 + per, vecs);
+  const int batches = (part.v1 - part.v0 + kBatch * kThreads - 1) / (kBatch * kThreads);
+  part.per_entry = (batches + kEntries - 1) / kEntries;
+  part.single = -1;
+  part.in = batches <= kRing ? reinterpret_cast<const uint4*>(smem) : vec + part.v0;
+  const bool ringed = batches > 1;  // (one batch is loaded as it is: the ring's barriers would only delay it)
+  __syncthreads();
+  if (warp == kWarps) {  // the warp that feeds the ring: one copy per batch
+    if (ringed && lane == 0) {
+      int n = 0;
+      for (; n < batches; ++n) {
+        const int s = n % kRing;
+        if (n >= kRing && !mbar_wait(&sh.empty[s], ((n / kRing) & 1) ^ 1)) {
+          flag_error(a.err, RRA_ERR_TIMEOUT);
+          break;
+        }
+        const int v = part.v0 + n * kBatch * kThreads;
+        const uint32_t bytes = 16u * static_cast<uint32_t>(min(kBatch * kThreads, part.v1 - v));
+        mbar_arrive_expect_tx(&sh.full[s], bytes);
+        bulk_g2s(smem + s * kStageBytes, vec + v, bytes, &sh.full[s]);
+      }
+      for (int i = max(n - kRing, 0); i < n; ++i) mbar_wait(&sh.full[i % kRing], (i / kRing) & 1);  // none still on its way
+    }
+    __syncwarp();
+    cluster_wait();
+    return;  // (barriers count the threads that are left)
+  }
+
+  const int t = threadIdx.x;
   // the given tokens' logits
   int token = -1;
   float x_token = 0.f;
@@ -197,175 +449,193 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_logprobs_kernel(co
     token = a.tokens[r * a.T + lane];
     if (token >= 0 && token < V) x_token = Elem<T>::load(row + token);
   }
+  part.single = rank != 0 ? -1 : t < part.head ? t : t >= E && t - E < tail ? V - tail + t - E : -1;
 
   // ---- (m, S, U), one pass
-  Part<T> part;
-  part.row = row;
-  part.head = static_cast<int>(min(static_cast<uint32_t>(V), static_cast<uint32_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<uint32_t>(sizeof(T))));
-  const int vecs = (V - part.head) / E, tail = V - part.head - vecs * E;
-  const int per = (vecs + C - 1) / C;
-  part.v0 = min(rank * per, vecs);
-  part.v1 = min(part.v0 + per, vecs);
-  const int t = threadIdx.x;
-  part.single = rank != 0 ? -1 : t < part.head ? t : t >= E && t - E < tail ? V - tail + t - E : -1;
   Stats st{-INFINITY, 0.f, 0.f};
-  int best = -1;  // first vector of the batch that raised the maximum last
-  const uint4* vec = reinterpret_cast<const uint4*>(row + part.head);
-  for (int v = part.v0 + t; v < part.v1; v += kBatch * kThreads) {
-    uint4 w[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (v + i * kThreads < part.v1) w[i] = vec[v + i * kThreads];
-    float x[kBatch][E];
+  int entry = t, in_entry = 0;
+  auto batch = [&](const uint4 (&w)[kBatch]) {
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (v + i * kThreads < part.v1) {
-        Elem<T>::unpack(w[i], x[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = -INFINITY;
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) mx = fmaxf(mx, x[i][e]);
-    }
-    if (mx > st.m || best < 0) {
-      st.move_to(fmaxf(mx, st.m));
-      best = v;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e) st.add(x[i][e]);
-  }
-  Key mine = 0;  // the thread's largest
-  if (k > 0 && best >= 0) {
-    for (int i = 0; i < kBatch; ++i) {
-      const int v = best + i * kThreads;
-      if (v < part.v1) {
-        float x[E];
-        Elem<T>::unpack(vec[v], x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) mine = max(mine, make_key(x[e], part.head + E * v + e));
+    for (int i = 0; i < kBatch; ++i) mx = Vec<T>::max_of(w[i], mx);
+    if (k > 0) {
+      maxima[entry] = __float2bfloat16_ru(in_entry == 0 ? mx : max_nan(mx, __bfloat162float(maxima[entry])));
+      if (++in_entry == part.per_entry) {
+        in_entry = 0;
+        entry += kThreads;
       }
     }
-  }
-  if (part.single >= 0) {
-    const float x = Elem<T>::load(row + part.single);
-    if (x > st.m) st.move_to(x);
-    st.add(x);
-    mine = max(mine, make_key(x, part.single));
-  }
+    if (!(mx <= st.m)) st.move_to(mx);  // (a NaN too: it makes m and the sums NaN)
+    // A logit far below m adds 0 to both sums, wherever it is: held at a bound, so that -inf is no infinity to
+    // multiply 0 with. (e^-150 is 0 in float32; |m| / 16 so that the bound is another number than m.)
+    const float m0 = st.m == -INFINITY ? 0.f : st.m, bound = m0 - fmaf(fabsf(m0), 0x1p-4f, 150.f);
+    if (bound > -1e38f) {
+      const uint64_t minus_m = pack2(-m0, -m0), log2e = pack2(kLog2e, kLog2e);
+      uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    Stats o;
-    o.m = __shfl_xor_sync(0xffffffffu, st.m, d);
-    o.s = __shfl_xor_sync(0xffffffffu, st.s, d);
-    o.u = __shfl_xor_sync(0xffffffffu, st.u, d);
-    st.join(o);
-  }
-  if (lane == 0) sh.warp_stats[warp] = st;
-
-  // ---- this CTA's k largest
-  if (k > 0) {
-    const int per_warp = min(kMaxTop, 2 * ((k + kWarps - 1) / kWarps));
-    Key left = mine;
-    for (int i = 0; i < per_warp; ++i) {
-      const Key top = warp_max(left);
-      if (lane == 0) sh.held[warp * per_warp + i] = top;
-      if (left == top) left = 0;  // (keys differ, but for 0)
-    }
-    if (t == 0) sh.count = 0;
-    __syncthreads();
-    // T: the k-th largest of what the warps hold (0 where the CTA has fewer values)
-    const int held = kWarps * per_warp;
-    Key T_key = 0;
-    for (int i = lane; i < held; i += 32) {
-      const Key key = sh.held[i];
-      int larger = 0;
-      for (int j = 0; j < held; ++j) larger += sh.held[j] > key;
-      if (larger == k - 1) T_key = key;
-    }
-    T_key = warp_max(T_key);
-    if (mine >= T_key && mine != 0)
-      part.each([&](float x, int i) {
-        const Key key = make_key(x, i);
-        if (key >= T_key) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kMaxFound) sh.found[at] = key;
+      for (int i = 0; i < kBatch; ++i) {
+        uint64_t x[Vec<T>::kPairs];
+        Vec<T>::clamped(w[i], bound, x);
+#pragma unroll
+        for (int p = 0; p < Vec<T>::kPairs; ++p) {
+          const uint64_t d = mul2(add2(x[p], minus_m), log2e), e = pack2(ex2(lo2(d)), ex2(hi2(d)));
+          s2[p & 1] = add2(s2[p & 1], e);
+          u2[p & 1] = fma2(d, e, u2[p & 1]);
         }
-      });
-    for (int i = t; i < k; i += kThreads) sh.top[i] = 0;
-    __syncthreads();
-    const int found = sh.count;
-    if (found > kMaxFound) {
-      top_slowly(part, k, sh);
-    } else {
-      for (int i = t; i < found; i += kThreads) {
-        const Key key = sh.found[i];
-        int larger = 0;
-        for (int j = 0; j < found; ++j) larger += sh.found[j] > key;
-        if (larger < k) sh.top[larger] = key;
+      }
+      const uint64_t s = add2(s2[0], s2[1]), u = add2(u2[0], u2[1]);
+      st.s += lo2(s) + hi2(s);
+      st.u += lo2(u) + hi2(u);
+    } else {  // (nothing but values near the type's lowest so far)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float x[E];
+        Elem<T>::unpack(w[i], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) st.add(x[e]);
       }
     }
+  };
+  const bool some = part.v0 + t < part.v1;
+  if (ringed) {
+    int n = 0;
+    for (; n < batches; ++n) {
+      const int s = n % kRing, v = part.v0 + n * kBatch * kThreads + t;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[s], (n / kRing) & 1))) break;
+      const uint4* in = reinterpret_cast<const uint4*>(smem + s * kStageBytes) + t;
+      uint4 w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) w[i] = v + i * kThreads < part.v1 ? in[i * kThreads] : Vec<T>::none();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[s]);
+      batch(w);
+    }
+    if (n < batches) flag_error(a.err, RRA_ERR_TIMEOUT);
+  } else if (some) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) w[i] = part.v0 + t + i * kThreads < part.v1 ? vec[part.v0 + t + i * kThreads] : Vec<T>::none();
+    if (k > 0) {  // (for a second look)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) reinterpret_cast<uint4*>(smem)[t + i * kThreads] = w[i];
+    }
+    batch(w);
   }
-  __syncthreads();
+  const float largest = st.m;  // of the vectors
+  uint32_t mine = some ? ordered(largest) : 0u;
+  if (part.single >= 0) {
+    const float x = part.single_value();
+    if (!(x <= st.m)) st.move_to(x);
+    st.add(x);
+    mine = max(mine, ordered(x));
+  }
+  st = join_warp(st);
+  cluster_wait();
+  if (lane == 0) {
+    const uint32_t to = cluster_addr(&sh.stats[rank * kWarps + warp], 0);
+    st_cluster(to, st.m);
+    st_cluster(to + 4, st.s);
+    st_cluster(to + 8, st.u);
+  }
+
+  // ---- this CTA's k largest, and what else reaches a bound below them: to the first CTA, which has places for them
+  const int places = kMaxFound / C;  // (at least kMaxTop)
+  if (k > 0) {
+    const uint32_t bound = common_bound(mine, k, sh);
+    const float bound_x = bound != 0 ? key_value(static_cast<Key>(bound) << 32) : -INFINITY;
+    const uint32_t to = cluster_addr(all + rank * places, 0);
+    auto put = [&](float x, int i) {
+      if (x >= bound_x) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < places) st_cluster(to + 8 * at, make_key(x, i));
+      }
+    };
+    if (some && largest >= bound_x)  // the thread's batches that reach the bound
+      for (int e = 0; e < kEntries && part.v0 + e * part.per_entry * kBatch * kThreads + t < part.v1; ++e)
+        if (__bfloat162float(maxima[e * kThreads + t]) >= bound_x) part.entry(e, bound_x, put);
+    if (part.single >= 0) put(part.single_value(), part.single);
+    sync_readers();
+    int n = sh.count;
+    if (n > places) {
+      sync_readers();
+      top_of_many(part, maxima, largest, some, k, found, sh);
+      if (t < k) st_cluster(to + 8 * t, sh.top[t]);
+      n = k;
+    }
+    if (t == 0) st_cluster(cluster_addr(&sh.counts[rank], 0), n);
+  }
+  if (C > 1) {
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
+  } else {
+    sync_readers();
+  }
+
+  // ---- the row's statistics, by every warp; the results
+  Stats s{-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kMaxCluster * kWarps / 32; ++i) {
+    if (32 * i + lane < C * kWarps) {
+      Stats o = sh.stats[32 * i + lane];
+      const float m = max_nan(s.m, o.m);
+      s.move_to(m);
+      o.move_to(m);
+      s.s += o.s;
+      s.u += o.u;
+    }
+  }
+  s = join_warp(s);
+  const bool good = s.s > 0.f && s.s < INFINITY;  // (NaN: no)
+  const float nan = __int_as_float(0x7fc00000), log_s = good ? logf(s.s) : nan;
   if (t == 0) {
-    Stats s = sh.warp_stats[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) s.join(sh.warp_stats[w]);
-    sh.stats = s;
+    if (!good) flag_error(a.err, RRA_ERR_PROBS);
+    if (a.entropy != nullptr) a.entropy[r] = good ? fmaxf(log_s - kLn2 * (s.u / s.s), 0.f) : nan;
   }
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-  if (rank == 0) {
-    // ---- the row's statistics, by every warp; the results
-    Stats s{-INFINITY, 0.f, 0.f};
-    if (lane < C) {
-      const uint32_t at = cluster_addr(&sh.stats, lane);
-      s.m = ld_cluster_f32(at);
-      s.s = ld_cluster_f32(at + 4);
-      s.u = ld_cluster_f32(at + 8);
+  if (asks) {
+    float lp = 0.f;  // (-1: no token)
+    if (token < -1 || token >= V) {
+      flag_error(a.err, RRA_ERR_TOKEN);
+      lp = nan;
+    } else if (token >= 0) {
+      lp = (x_token - s.m) - log_s;
     }
-    for (int i = t; i < C * k; i += kThreads) sh.all[i] = ld_cluster_key(cluster_addr(&sh.top[i % k], i / k));
+    a.logprobs[r * a.T + lane] = lp;
+  }
+  if (k == 0) return;
+  if (!good) {
+    if (t < k) {
+      a.top_tokens[r * k + t] = -1;
+      a.top_logprobs[r * k + t] = nan;
+    }
+    return;
+  }
+  Key* kept = reinterpret_cast<Key*>(smem);  // (the ring is done)
+  static_assert(kRing * kStageBytes >= kMaxFound * 8, "they fit");
+  // the k largest of all keys: those that reach a bound made in the same way, sorted by counting
+  Key mine_of[kMaxFound / kThreads];
+  uint32_t best = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      Stats o;
-      o.m = __shfl_xor_sync(0xffffffffu, s.m, d);
-      o.s = __shfl_xor_sync(0xffffffffu, s.s, d);
-      o.u = __shfl_xor_sync(0xffffffffu, s.u, d);
-      s.join(o);
-    }
-    __syncthreads();
-    const bool good = s.s > 0.f && s.s < INFINITY;  // (NaN: no)
-    const float nan = __int_as_float(0x7fc00000), log_s = good ? logf(s.s) : nan;
-    if (t == 0) {
-      if (!good) flag_error(a.err, RRA_ERR_PROBS);
-      if (a.entropy != nullptr) a.entropy[r] = good ? fmaxf(log_s - kLn2 * (s.u / s.s), 0.f) : nan;
-    }
-    if (asks) {
-      float lp = 0.f;  // (-1: no token)
-      if (token < -1 || token >= V) {
-        flag_error(a.err, RRA_ERR_TOKEN);
-        lp = nan;
-      } else if (token >= 0) {
-        lp = (x_token - s.m) - log_s;
-      }
-      a.logprobs[r * a.T + lane] = lp;
-    }
-    for (int i = t; i < C * k; i += kThreads) {
-      const Key key = sh.all[i];
-      int larger = 0;
-      for (int j = 0; j < C * k; ++j) larger += sh.all[j] > key;
-      if (key != 0 && larger < k) {
-        a.top_tokens[r * k + larger] = good ? key_index(key) : -1;
-        a.top_logprobs[r * k + larger] = good ? (key_value(key) - s.m) - log_s : nan;
-      }
+  for (int i = 0; i < kMaxFound / kThreads; ++i) {
+    const int at = t + i * kThreads, c = at / places;
+    mine_of[i] = c < C && at - c * places < sh.counts[c] ? all[at] : 0;
+    best = max(best, static_cast<uint32_t>(mine_of[i] >> 32));
+  }
+  const uint32_t bound = C > 1 ? common_bound(best, k, sh) : 0;
+#pragma unroll
+  for (int i = 0; i < kMaxFound / kThreads; ++i)
+    if (mine_of[i] != 0 && static_cast<uint32_t>(mine_of[i] >> 32) >= bound) kept[atomicAdd(&sh.kept, 1)] = mine_of[i];
+  sync_readers();
+  const int n = sh.kept;
+  for (int i = t; i < n; i += kThreads) {
+    const Key key = kept[i];
+    int larger = 0;
+    for (int j = 0; j < n; ++j) larger += kept[j] > key;
+    if (larger < k) {
+      a.top_tokens[r * k + larger] = key_index(key);
+      a.top_logprobs[r * k + larger] = (key_value(key) - s.m) - log_s;
     }
   }
-  cluster_arrive();  // no CTA's lists go away while another may still read them
-  cluster_wait();
 }
 
 template <typename T>
@@ -377,13 +647,15 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int clusters, cudaStream_t str
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !done[dev]) {  // clusters of 16 CTAs are opt-in
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = 1;
   }
   cudaLaunchConfig_t cfg{};
   const unsigned y = static_cast<unsigned>(std::min<int64_t>(a.rows, 65535));
   cfg.gridDim = dim3(clusters, y, static_cast<unsigned>((a.rows + y - 1) / y));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads + 32);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

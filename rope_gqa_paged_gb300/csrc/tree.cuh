@@ -61,7 +61,7 @@ struct Cfg {
   static constexpr int kTileBytes = kTile * 128 * kHalves;
   static constexpr int kQHalfBytes = kRows * 128;            // NQ 2: Q tiles, K-major, 64-dim halves
   static constexpr int kQBytes = NQ == 2 ? NQ * kHalves * kQHalfBytes : 0;
-  static constexpr int kRing = NQ == 2 && D == 128 ? 4 : 6;  // slots: K_0, V_0, K_1, V_1, ...
+  static constexpr int kRing = NQ == 2 && D == 128 ? 4 : 5;  // slots: K_0, V_0, K_1, V_1, ...
   static constexpr int kWarps = 4 * NQ;                      // softmax warps
   static constexpr int kStagePitch = 80;                     // 64 bytes of a row and 16: eight rows in other banks
   static constexpr int kStageBytes = 32 * kStagePitch;       // per softmax warp: rows on their way out
@@ -73,13 +73,17 @@ struct Cfg {
   // shared memory
   static constexpr int kOffRing = kQBytes;
   static constexpr int kOffStage = kOffRing + kRing * kTileBytes;
-  static constexpr int kOffBar = kOffStage + kWarps * kStageBytes;
+  static constexpr int kOffSees = kOffStage + kWarps * kStageBytes;  // 128 bits per row: the nodes that it attends
+  static constexpr int kOffBar = kOffSees + NQ * kRows * kTreeMaxNodes / 8;
   // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ][kParts], o_done
   static constexpr int kNumBars = 1 + 2 * kRing + NQ + NQ * kParts + 1;
   static constexpr int kOffStart = kOffBar + kNumBars * 8;   // Start
-  static constexpr int kOffTmemSlot = kOffStart + 144;
+  static constexpr int kOffUnits = kOffStart + 144;          // Units, one per softmax warp
+  static constexpr int kOffTmemSlot = kOffUnits + kWarps * 48;
   static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
-  static constexpr int kThreads = 32 * kWarps + 64;          // + producer warp + MMA warp
+  // + producer warp + MMA warp; NQ 2: and two idle ones, so that a whole warpgroup gives registers to the softmax
+  static constexpr int kThreads = 32 * kWarps + (NQ == 2 ? 128 : 64);
+  static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's
   static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
   static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kRows, kTile, false);  // Q (K-major) . K^T (K-major)
   static constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kRows, D, true);      // P (K-major) . V (MN-major)
@@ -107,55 +111,75 @@ __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool
   return s;
 }
 
+// The key tiles of all units in one line, cut into `ranges` runs whose lengths differ by one at most.
+struct Cut {
+  int each, more;  // the first `more` runs have each + 1 tiles
+  __device__ __forceinline__ int border(int r) const { return each * r + min(r, more); }
+  __device__ __forceinline__ int range_of(int t) const {
+    const int split = more * (each + 1);
+    return t < split ? t / (each + 1) : more + (t - split) / max(each, 1);
+  }
+};
+
 // Where a range starts: tiles [t0, t1) of all, from tile `off` of sequence b's Hkv x tiles on.
 struct Start {
-  int64_t t0, t1, total;
-  int b, ranges;
-  int64_t off;
-  int64_t sums[12];
+  int t0, t1, b, off;
+  Cut cut;
+  Seq seq;        // of sequence b
+  int sums[2][12];
 };
-// t-th border of `ranges` equal runs of `total` tiles
-__device__ __forceinline__ int64_t border(int64_t total, int ranges, int64_t r) { return total * r / ranges; }
 
-// Adds up the sequences' tiles and finds the start of range r (all threads of the CTA; r past the ranges in use:
-// t0 = t1). Ranges of at least min_tiles tiles, so some of a.ranges may stay unused.
+// Adds up the sequences' tiles and finds the start of range r (all threads of the CTA; r past the ranges in use: t0 = t1).
+// Ranges of at least min_tiles tiles, unless there are more units than such ranges: so some of a.ranges may stay unused.
 template <int THREADS>
 __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) {
   const int per = (a.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(sequence(a, b, tile, flag).tiles) * a.Hkv;
-  int64_t incl = mine;
+  Seq seq{0, 0, 0, false};
+  int mine = 0, seqs = 0;
+  for (int b = b0; b < b1; ++b) {
+    seq = sequence(a, b, tile, flag);
+    mine += seq.tiles * a.Hkv;
+    seqs += seq.tiles > 0;
+  }
+  int incl = mine;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    const int y = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += y;
   }
-  if (lane == 31) s->sums[warp] = incl;
+  seqs = __reduce_add_sync(0xffffffffu, seqs);
+  if (lane == 31) {
+    s->sums[0][warp] = incl;
+    s->sums[1][warp] = seqs;
+  }
   if (threadIdx.x == 0) s->t0 = s->t1 = 0;
   __syncthreads();
-  int64_t before = incl - mine, total = 0;
+  int before = incl - mine, total = 0, units = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += s->sums[w];
-    total += s->sums[w];
+    if (w < warp) before += s->sums[0][w];
+    total += s->sums[0][w];
+    units += s->sums[1][w] * a.Hkv;
   }
-  const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
-  const int ranges = static_cast<int>(min(static_cast<int64_t>(a.ranges), max(most, int64_t(1))));
+  const int ranges = min(a.ranges, max((total + a.min_tiles - 1) / a.min_tiles, max(units, 1)));
   if (r < ranges) {
-    const int64_t t0 = border(total, ranges, r), t1 = border(total, ranges, r + 1);
+    const Cut cut{total / ranges, total % ranges};
+    const int t0 = cut.border(r), t1 = cut.border(r + 1);
     if (t0 < t1 && before <= t0 && t0 < before + mine) {  // one thread
       int b = b0;
-      for (;; ++b) {
-        const int64_t u = static_cast<int64_t>(sequence(a, b, tile).tiles) * a.Hkv;
-        if (t0 < before + u) break;
-        before += u;
+      if (per > 1) {
+        for (;; ++b) {
+          seq = sequence(a, b, tile);
+          if (t0 < before + seq.tiles * a.Hkv) break;
+          before += seq.tiles * a.Hkv;
+        }
       }
       s->t0 = t0;
       s->t1 = t1;
-      s->total = total;
-      s->ranges = ranges;
+      s->cut = cut;
       s->b = b;
+      s->seq = seq;
       s->off = t0 - before;
     }
   }
@@ -164,22 +188,18 @@ __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) 
 
 // A range's units one after the other: key tiles [j0, j1) of KV head g of sequence b.
 struct Units {
-  int b, g, j0, j1;
+  int b, g, j0, j1, off, left;
   Seq seq;
-  int64_t off, left;
-  __device__ __forceinline__ Units(const TreeArgs& a, const Start& s, int tile)
-      : b(s.b), g(0), j0(0), j1(0), seq{0, 0, 0, false}, off(s.off), left(s.t1 - s.t0) {
-    if (left > 0) seq = sequence(a, b, tile);
-  }
+  __device__ __forceinline__ Units(const Start& s) : b(s.b), g(0), j0(0), j1(0), off(s.off), left(s.t1 - s.t0), seq(s.seq) {}
   __device__ __forceinline__ bool next(const TreeArgs& a, int tile, int first_row) {
     while (left > 0) {
-      while (off >= static_cast<int64_t>(seq.tiles) * a.Hkv) {
+      while (off >= seq.tiles * a.Hkv) {
         off = 0;
         seq = sequence(a, ++b, tile);
       }
-      g = static_cast<int>(off / seq.tiles);
-      j0 = static_cast<int>(off - static_cast<int64_t>(g) * seq.tiles);
-      j1 = static_cast<int>(min(static_cast<int64_t>(seq.tiles), j0 + left));
+      g = off / seq.tiles;
+      j0 = off - g * seq.tiles;
+      j1 = min(seq.tiles, j0 + left);
       off += j1 - j0;
       left -= j1 - j0;
       if (seq.n * a.n_rep > first_row) return true;  // (a smaller tree leaves this CTA's rows empty)
@@ -188,6 +208,20 @@ struct Units {
   }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == seq.tiles; }
 };
+
+// Rows of nodes that a tree does not have are zero, and a sequence without any has nothing to merge; by a warp or a CTA, for
+// every gridDim.x-th sequence.
+__device__ __forceinline__ void pad_rows(const TreeArgs& a, int D, int thread, int threads) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = sequence(a, b, 1);
+    if (s.tiles == 0 && a.headers_by_unit)
+      for (int g = thread; g < a.Hkv; g += threads) a.headers[b * a.Hkv + g] = make_int4(0, 0, 0, 0);
+    if (s.refused || s.n == a.N) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(b) * a.N + s.n) * a.Hq * D);
+    const size_t vecs = static_cast<size_t>(a.N - s.n) * a.Hq * (D / 8);
+    for (size_t i = thread; i < vecs; i += threads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
 
 template <int D, int NQ, bool PAGED>
 __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>::kCtasPerSm)
@@ -209,7 +243,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   uint64_t* p_full = s_full + NQ;
   uint64_t* o_done = p_full + NQ * kParts;
   Start* start = reinterpret_cast<Start*>(smem + C::kOffStart);
-  static_assert(sizeof(Start) <= 144, "Start");
+  static_assert(sizeof(Start) <= 144 && sizeof(Units) <= 48 && sizeof(Units) % 4 == 0 && C::kOffSees % 16 == 0 && kTreeMaxNodes == 128, "layout");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
 
   if (threadIdx.x == 0) {
@@ -228,18 +262,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   if (!a.after_append) pdl_wait();
   locate<C::kThreads>(a, kTile, range, blockIdx.x == 0, start);
 
-  // rows of nodes that a tree does not have are zero
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Seq s = sequence(a, b, kTile);
-    if (s.tiles == 0 && a.headers_by_unit)
-      for (int g = threadIdx.x; g < a.Hkv; g += C::kThreads) a.headers[b * a.Hkv + g] = make_int4(0, 0, 0, 0);
-    if (s.refused || s.n == a.N) continue;
-    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (static_cast<size_t>(b) * a.N + s.n) * a.Hq * D);
-    const size_t vecs = static_cast<size_t>(a.N - s.n) * a.Hq * (D / 8);
-    for (size_t i = threadIdx.x; i < vecs; i += C::kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
   if (start->t0 >= start->t1) {  // (the same for every thread)
     if (threadIdx.x == 0 && first_row == 0 && a.headers != nullptr && !a.headers_by_unit) a.headers[range] = make_int4(0, 0, 0, 0);
+    pad_rows(a, D, threadIdx.x, C::kThreads);
     pdl_wait();
     return;
   }
@@ -256,9 +281,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   // ring position r: K of the CTA's tile r / 2 (r even) or its V (r odd)
   auto slot_of = [](uint32_t r) { return r % kRing; };
   auto phase_of = [](uint32_t r) { return (r / kRing) & 1u; };
-  Units u(a, *start, kTile);
 
-  if (warp == kProducerWarp) {
+  if (warp >= C::kWarps) {
+   if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+   Units u(*start);
+   if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
       prefetch_tensormap(&k_map);
@@ -270,6 +297,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     uint32_t issued = 0;
     while (ok && u.next(a, kTile, first_row)) {
       const int L = u.seq.p + u.seq.n;
+      if (first_row == 0 && lane == 0 && a.headers != nullptr) {
+        // a unit that starts here and goes on in later ranges is merged for this range's header
+        int4 h = make_int4(0, 0, 0, 0);
+        if (u.j0 == 0 && !u.whole()) {
+          const int end = start->t1 + (u.seq.tiles - u.j1);  // the unit's end among all tiles
+          h = make_int4(start->cut.range_of(end - 1) - range + 1, range, u.b * a.Hkv + u.g, u.seq.n * a.n_rep);
+        }
+        if (a.headers_by_unit) {
+          if (u.j0 == 0) a.headers[u.b * a.Hkv + u.g] = h;
+        } else if (u.left == 0) {
+          a.headers[range] = h;
+        }
+      }
       const int32_t* row = a.block_table + static_cast<size_t>(u.b) * a.max_blocks_per_seq;
       // block where this lane's box of tile j starts (the id loads a tile ahead of its use)
       auto block_of = [&](int j) {
@@ -315,15 +355,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
         }
       }
     }
+    pad_rows(a, D, lane, 32);
     if (lane == 0) {
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       // no copy may still be landing when the CTA exits
       for (uint32_t r = issued > kRing ? issued - kRing : 0; r < issued; ++r) mbar_wait(&ring_full[slot_of(r)], phase_of(r));
     }
-  } else if (warp == kMmaWarp) {
+   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
     if (elect_one()) {
+      // Descriptors by additions to one per operand (addresses count 16 bytes in their low bits): worked out one by one
+      // and kept, they take more registers than this warp has.
+      auto opaque = [](uint64_t d) {
+        asm volatile("" : "+l"(d));
+        return d;
+      };
       const uint32_t base = smem_addr(smem);
+      const uint64_t q_desc = tc::sw128_desc(base, 1024, 1024);
       bool ok = true;
       uint32_t c = 0, units = 0;  // the CTA's tiles and units so far
       while (ok && u.next(a, kTile, first_row)) {
@@ -336,16 +384,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
             if (!mbar_wait(&ring_full[s], phase_of(2 * t))) return false;
             tc::fence_after_sync();
           }
-          const uint32_t k_base = base + C::kOffRing + s * C::kTileBytes, s_col = tmem + C::kColS + kTile * k;
+          const uint32_t s_col = tmem + C::kColS + kTile * k;
+          const uint64_t kd = opaque(tc::sw128_desc(base + C::kOffRing + s * C::kTileBytes, 1024, C::kGroupBytes));
+          const uint64_t qd = opaque(q_desc);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t kd = tc::sw128_desc(k_base + (kk >> 2) * C::kHalfBytes + (kk & 3) * 32, 1024, C::kGroupBytes);
+            const uint64_t kd_kk = kd + ((kk >> 2) * C::kHalfBytes + (kk & 3) * 32) / 16;
             if constexpr (NQ == 2)
-              tc::mma_bf16_ss(s_col, tc::sw128_desc(base + (k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32,
-                                                    1024, 1024),
-                              kd, C::kIdescS, kk > 0 ? 1u : 0u);
+              tc::mma_bf16_ss(s_col, qd + ((k * C::kHalves + (kk >> 2)) * C::kQHalfBytes + (kk & 3) * 32) / 16, kd_kk,
+                              C::kIdescS, kk > 0 ? 1u : 0u);
             else
-              tc::mma_bf16_ts(s_col, tmem + C::kColQ + 8 * kk, kd, C::kIdescS, kk > 0 ? 1u : 0u);
+              tc::mma_bf16_ts(s_col, tmem + C::kColQ + 8 * kk, kd_kk, C::kIdescS, kk > 0 ? 1u : 0u);
           }
           tc::commit(&s_full[k]);
           return true;
@@ -354,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
         for (int k = 0; k < NQ; ++k) ok = ok && issue_s(k, c);
         for (int j = u.j0; ok && j < u.j1; ++j, ++c) {
           const uint32_t s = slot_of(2 * c + 1);
-          const uint32_t v_base = base + C::kOffRing + s * C::kTileBytes;
+          const uint64_t vd = opaque(tc::sw128_desc(base + C::kOffRing + s * C::kTileBytes, C::kHalfBytes, C::kGroupBytes));
           ok = mbar_wait(&ring_full[s], phase_of(2 * c + 1));
 #pragma unroll
           for (int k = 0; k < NQ; ++k) {
@@ -366,15 +415,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
                 tc::fence_after_sync();
               }
               tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + 8 * kk,
-                              tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, C::kHalfBytes, C::kGroupBytes), C::kIdescPV,
-                              (j > u.j0 || kk > 0) ? 1u : 0u);
+                              vd + kk * 2 * C::kGroupBytes / 16, C::kIdescPV, (j > u.j0 || kk > 0) ? 1u : 0u);
             }
             if (ok && short_seq) {  // the remainders of P
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
                 tc::mma_bf16_ts(tmem + C::kColO + D * k, tmem + C::kColS + kTile * k + kTile / 2 + 8 * kk,
-                                tc::sw128_desc(v_base + kk * 2 * C::kGroupBytes, C::kHalfBytes, C::kGroupBytes),
-                                C::kIdescPV, 1u);
+                                vd + kk * 2 * C::kGroupBytes / 16, C::kIdescPV, 1u);
             }
             if (ok && j + 1 < u.j1) ok = issue_s(k, c + 1);
           }
@@ -385,21 +432,36 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       if (units > 0) mbar_wait(o_done, (units - 1) & 1u);
     }
+   }
   } else {
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------------ softmax: thread = query row
     const int k = warp >> 2;                               // row tile of this warpgroup
     const int r = static_cast<int>(threadIdx.x) & 127;     // row = TMEM lane
     const int row = first_row + k * kRows + r;             // node row / n_rep, head row % n_rep of the group
-    const int j_node = row / a.n_rep, i_head = row - j_node * a.n_rep;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t o_col = tmem + lane_base + C::kColO + D * k;
     uint8_t* stage = smem + C::kOffStage + warp * C::kStageBytes;
     const float sl = a.scale_log2;
+    uint4* sees = reinterpret_cast<uint4*>(smem + C::kOffSees);
+    // The warp's place in the list of units, in shared memory: S takes the registers.
+    Units& u = *reinterpret_cast<Units*>(smem + C::kOffUnits + 48 * warp);
+    auto advance = [&]() -> bool {
+      __syncwarp();
+      const int more = __shfl_sync(0xffffffffu, lane == 0 && u.next(a, kTile, first_row) ? 1 : 0, 0);
+      __syncwarp();
+      return more != 0;
+    };
+    if (lane == 0) u = Units(*start);
     if (a.after_append) pdl_wait();  // the queries
 
+    auto out_row_of = [&](int b, int g) {
+      const int j = row / a.n_rep;
+      return (static_cast<size_t>(b) * a.N + j) * a.Hq + g * a.n_rep + (row - j * a.n_rep);
+    };
     auto load_q = [&]() {  // the unit's query row
       const bool real = row < u.seq.n * a.n_rep;
-      const size_t q_row = (static_cast<size_t>(u.b) * a.N + j_node) * a.Hq + u.g * a.n_rep + i_head;
+      const size_t q_row = out_row_of(u.b, u.g);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q_row * D);
       uint4 qv[D / 8];
 #pragma unroll
@@ -428,16 +490,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     };
 
     uint32_t c = 0, units = 0;  // the CTA's tiles and units so far
-    bool ok = true, more = u.next(a, kTile, first_row);
+    bool ok = true, more = advance();
     if (more) load_q();
     while (ok && more) {
-      const int p = u.seq.p, L = p + u.seq.n;
-      const bool real = row < u.seq.n * a.n_rep, short_seq = p < kShortRow;
-      const bool warp_real = __any_sync(0xffffffffu, real);
-      const size_t out_row = (static_cast<size_t>(u.b) * a.N + j_node) * a.Hq + u.g * a.n_rep + i_head;
-      // the row's node and its ancestors, one bit each
-      uint32_t sees[kTreeMaxNodes / 32] = {};
-      if (warp_real && u.j1 * kTile > p) {
+      const int p = u.seq.p, j0 = u.j0, j1 = u.j1;
+      const bool short_seq = p < kShortRow;
+      const bool warp_real = first_row + k * kRows + (r & ~31) < u.seq.n * a.n_rep;  // any row of this warp
+      // the row's node and its ancestors, one bit each (kept in shared memory: every register counts below)
+      if (warp_real && j1 * kTile > p) {
+        uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
         int up[kTreeMaxNodes / 32];  // parents of nodes lane, lane + 32, ...
 #pragma unroll
         for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
@@ -448,33 +509,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
             up[w] = -1;
           }
         }
-        int n = real ? j_node : -1;
+        int n = row < u.seq.n * a.n_rep ? row / a.n_rep : -1;
         while (__any_sync(0xffffffffu, n >= 0)) {  // (parents come before their children)
-          int above = -1;
-#pragma unroll
-          for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
-            const int x = __shfl_sync(0xffffffffu, up[w], n & 31);
-            if ((n >> 5) == w) {
-              above = x;
-              sees[w] |= 1u << (n & 31);
-            }
-          }
-          n = above;
+          const uint32_t bit = n >= 0 ? 1u << (n & 31) : 0u;
+          const int x0 = __shfl_sync(0xffffffffu, up[0], n & 31), x1 = __shfl_sync(0xffffffffu, up[1], n & 31);
+          const int x2 = __shfl_sync(0xffffffffu, up[2], n & 31), x3 = __shfl_sync(0xffffffffu, up[3], n & 31);
+          const int w = n >> 5;  // (-1: none)
+          s0 |= w == 0 ? bit : 0u;
+          s1 |= w == 1 ? bit : 0u;
+          s2 |= w == 2 ? bit : 0u;
+          s3 |= w == 3 ? bit : 0u;
+          n = w < 0 ? -1 : w == 0 ? x0 : w == 1 ? x1 : w == 2 ? x2 : x3;
         }
+        sees[threadIdx.x] = make_uint4(s0, s1, s2, s3);
       }
-      auto seen_from = [&](int first) -> uint32_t {  // of the 32 tokens from token p + first on
-        if (first <= -32) return 0xffffffffu;
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
-          lo = w == (first >> 5) ? sees[w] : lo;
-          hi = w == (first >> 5) + 1 ? sees[w] : hi;
-        }
-        if (first < 0) lo = 0xffffffffu;  // (first >> 5 is -1 there)
-        return __funnelshift_r(lo, hi, first & 31);
-      };
       float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
-      for (int j = u.j0; j < u.j1; ++j, ++c) {
+      for (int j = j0; j < j1; ++j, ++c) {
         if (!warp_wait(&s_full[k], c & 1u)) {  // S_k is there, and every MMA issued before it is complete
           ok = false;
           break;
@@ -482,16 +532,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
         tc::fence_after_sync();
         if (r == 0) {
           mbar_arrive(&ring_empty[slot_of(2 * c)]);
-          if (j > u.j0) mbar_arrive(&ring_empty[slot_of(2 * c - 1)]);
+          if (j > j0) mbar_arrive(&ring_empty[slot_of(2 * c - 1)]);
         }
-        if (L - j * kTile < kTile) {
+        if (j + 1 == j1 && p + u.seq.n - j * kTile < kTile) {
           // rows past the last token: their V is whatever the slot held; zeros keep 0 * V at 0 (both row
           // tiles' threads write them, each before its own P.V)
           if (!warp_wait(&ring_full[slot_of(2 * c + 1)], phase_of(2 * c + 1))) {
             ok = false;
             break;
           }
-          if (r >= L - j * kTile && r < kTile) {
+          if (r >= p + u.seq.n - j * kTile && r < kTile) {
             uint8_t* vrow = smem + C::kOffRing + slot_of(2 * c + 1) * C::kTileBytes + (r >> 3) * C::kGroupBytes + (r & 7) * 128;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
@@ -505,9 +555,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
           uint32_t sv[kTile];
           ld_cols<kTile>(s_col, sv);
           if ((j + 1) * kTile > p) {  // the tree begins in this tile, or before it
+            const uint4 s = sees[threadIdx.x];
 #pragma unroll
             for (int w = 0; w < kTile / 32; ++w) {
-              const uint32_t see = seen_from(j * kTile + 32 * w - p);
+              const int first = j * kTile + 32 * w - p, at = first >> 5;  // node of the word's first token
+              uint32_t see = 0xffffffffu;
+              if (first > -32) {
+                const uint32_t lo = at < 0 ? 0xffffffffu : at == 0 ? s.x : at == 1 ? s.y : at == 2 ? s.z : at == 3 ? s.w : 0u;
+                const uint32_t hi = at == -1 ? s.x : at == 0 ? s.y : at == 1 ? s.z : at == 2 ? s.w : 0u;
+                see = __funnelshift_r(lo, hi, first & 31);
+              }
 #pragma unroll
               for (int i = 0; i < 32; ++i) sv[32 * w + i] = (see >> i) & 1u ? sv[32 * w + i] : __float_as_uint(-INFINITY);
             }
@@ -526,7 +583,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
             alpha = ex2(m_use - m_new);
             m_use = m_new;
           }
-          if (j > u.j0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
+          if (j > j0 && __any_sync(0xffffffffu, rescale)) {  // O rows whose max moved (alpha = 1 elsewhere)
 #pragma unroll 1
             for (int x = 0; x < D / 8; ++x) scale_cols8(o_col + 8 * x, alpha);  // (few registers: S is held)
           }
@@ -537,28 +594,25 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
           for (int h = 0; h < kParts; ++h) {
             constexpr int kWords = kTile / 2 / kParts;
             uint32_t pw[kWords];
-            if (short_seq) {
-              uint32_t lw[kWords];
 #pragma unroll
-              for (int x = 0; x < kWords; ++x) {
-                const int cc = h * kWords + x;
-                const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
-                const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
-                ls[x & 1] = add2(ls[x & 1], pack2(e0, e1));
-                split_bf16x2(e0, e1, pw[x], lw[x]);
-              }
-              st_cols<kWords>(s_col + kTile / 2 + h * kWords, lw);
-            } else {
-#pragma unroll
-              for (int x = 0; x < kWords; ++x) {
-                const int cc = h * kWords + x;
-                const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
-                const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
-                ls[x & 1] = add2(ls[x & 1], pack2(e0, e1));
-                pw[x] = pack_bf16x2(e0, e1);
-              }
+            for (int x = 0; x < kWords; ++x) {
+              const int cc = h * kWords + x;
+              const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
+              const float e0 = ex2(lo2(y)), e1 = ex2(hi2(y));
+              ls[x & 1] = add2(ls[x & 1], pack2(e0, e1));
+              pw[x] = pack_bf16x2(e0, e1);
             }
             st_cols<kWords>(s_col + h * kWords, pw);
+            if (short_seq) {  // the remainders (worked out again: there is no room to keep them beside S)
+#pragma unroll
+              for (int x = 0; x < kWords; ++x) {
+                const int cc = h * kWords + x;
+                const uint64_t y = fma2(pack2(__uint_as_float(sv[2 * cc]), __uint_as_float(sv[2 * cc + 1])), sl2, mref2);
+                uint32_t hi;
+                split_bf16x2(ex2(lo2(y)), ex2(hi2(y)), hi, pw[x]);
+              }
+              st_cols<kWords>(s_col + kTile / 2 + h * kWords, pw);
+            }
             tc::tmem_wait_st();
             if (h + 1 < kParts) {
               tc::fence_before_sync();
@@ -580,24 +634,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's rows, the next one's Q before them
       const bool whole = u.whole();
-      const int slot = u.j0 > 0 ? 0 : 1;
+      const int slot = j0 > 0 ? 0 : 1, unit_b = u.b, unit_g = u.g;
       const int live = u.seq.n * a.n_rep;
-      if (threadIdx.x == 0 && first_row == 0 && a.headers != nullptr) {
-        // a unit that starts here and goes on in later ranges is merged for this range's header
-        int4 h = make_int4(0, 0, 0, 0);
-        if (u.j0 == 0 && !whole) {
-          const int64_t end = start->t1 + (u.seq.tiles - u.j1);  // the unit's end among all tiles
-          int last = range + 1;
-          while (border(start->total, start->ranges, last + 1) < end) ++last;
-          h = make_int4(last - range + 1, range, u.b, u.g);
-        }
-        if (a.headers_by_unit) {
-          if (u.j0 == 0) a.headers[u.b * a.Hkv + u.g] = h;
-        } else if (u.left == 0) {
-          a.headers[range] = h;
-        }
-      }
-      more = u.next(a, kTile, first_row);
+      more = advance();
       if (more) load_q();
       if (!warp_wait(o_done, units & 1u)) {
         ok = false;
@@ -610,6 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
         const int rows_here = min(32, live - (first_row + k * kRows + 32 * (warp & 3)));  // of this warp
         if (whole) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
+          const size_t out_row = out_row_of(unit_b, unit_g);
           const uint32_t out_lo = static_cast<uint32_t>(out_row), out_hi = static_cast<uint32_t>(out_row >> 32);
 #pragma unroll 1
           for (int x = 0; x < D / 32; ++x) {
@@ -659,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
               __syncwarp();
             }
           }
-          if (real) *reinterpret_cast<float2*>(a.ws_ml + 2 * (part + lane)) = make_float2(m_use, l);
+          if (lane < rows_here) *reinterpret_cast<float2*>(a.ws_ml + 2 * (part + lane)) = make_float2(m_use, l);
         }
       }
       tc::fence_before_sync();  // (O is read before the next unit's first P.V, which waits for its first P)
@@ -674,78 +714,113 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   }
 }
 
-// Output rows of the units that several ranges share, from their partials: one warp per row. A range writes the
-// unit that it starts with into its slot 0 and the one that it ends with into slot 1, so a unit's partials are slot 1 of
-// its first range and slot 0 of the following ones.
+// Output rows of the units that several ranges share, from their partials. A range writes the unit that it starts
+// with into its slot 0 and the one that it ends with into slot 1, so a unit's partials are slot 1 of its first range and
+// slot 0 of the following ones.
+// Bound: latency (header, then maxima and partials together, then the rows) and L2's bandwidth. ROWS rows per warp at a
+// time, so that a warp has 8 loads in flight: of one row where a unit has many partials, of four rows where it
+// has two or three.
 constexpr int kMergeWarps = 8;
 
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a) {
-  constexpr int E = D / 32;  // dims per lane
-  constexpr int kBatch = 4;  // partials loaded at a time
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  constexpr int E = D / 32;           // dims per lane
+  constexpr int kBatch = 8 / ROWS;    // partials of a row loaded at a time, the first before the maxima are known
+  constexpr int kGroup = 32 / ROWS;   // partials whose (max, sum) a warp looks at together
+  const int lane = threadIdx.x & 31, mine = lane / kGroup, at = lane % kGroup;  // this lane's row of (max, sum), its partial
+  const int row0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * ROWS;
   pdl_wait();
   pdl_launch_dependents();
   const int4 h = __ldcg(a.headers + blockIdx.x);
-  const int n = h.x, first = h.y, b = h.z, g = h.w;
+  const int n = h.x, first = h.y, b = h.z / a.Hkv, g = h.z - b * a.Hkv, rows = min(h.w, a.rows);
   // (what a range whose waits ran out has not written may be anything)
-  if (n < 2 || first < 0 || first >= a.ranges || n > a.ranges - first || b < 0 || b >= a.B || g < 0 || g >= a.Hkv) return;
-  const Seq s = sequence(a, b, 1);
-  if (row >= s.n * a.n_rep) return;
+  if (n < 2 || first < 0 || first >= a.ranges || n > a.ranges - first || b < 0 || b >= a.B || g < 0 || row0 >= rows) return;
   const float2* ml = reinterpret_cast<const float2*>(a.ws_ml);
-  auto slot = [&](int i) { return static_cast<size_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
-  float M = -INFINITY, l = 0.f;
-  float acc[E] = {};
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    const float2 x = s0 + lane < n ? __ldcg(ml + slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
+  auto slot = [&](int i, int row) { return static_cast<size_t>(2 * (first + i) + (i == 0 ? 1 : 0)) * a.rows + row; };
+  float next[kBatch][ROWS][E];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        if (s + k < n && row0 + q < rows) {
+          const float* o = a.ws_o + slot(s + k, row0 + q) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(o));
+            next[k][q][0] = t.x, next[k][q][1] = t.y, next[k][q][2] = t.z, next[k][q][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(o));
+            next[k][q][0] = t.x, next[k][q][1] = t.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) next[k][q][e] = 0.f;
+        }
+      }
+  };
+  load(0);
+  float M = -INFINITY, l = 0.f;  // of row `mine`
+  float acc[ROWS][E] = {};
+  for (int s0 = 0; s0 < n; s0 += kGroup) {
+    const float2 x = s0 + at < n && row0 + mine < rows ? __ldcg(ml + slot(s0 + at, row0 + mine)) : make_float2(-INFINITY, 0.f);
     float m = x.x;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = kGroup / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     m = fmaxf(m, M);
     const float mref = m == -INFINITY ? 0.f : m;
     const float w = ex2(x.x - mref), keep = ex2(M - mref);
     float ls = w * x.y;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    for (int d = kGroup / 2; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
     l = l * keep + ls;
     M = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= keep;
-    for (int i = s0; i < min(n, s0 + 32); i += kBatch) {
-      float v[kBatch][E];
+    for (int q = 0; q < ROWS; ++q) {
+      const float f = __shfl_sync(0xffffffffu, keep, q * kGroup);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (i + k < n) {
-          const float* o = a.ws_o + slot(i + k) * D + lane * E;
-          if constexpr (E == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(o));
-            v[k][0] = t.x, v[k][1] = t.y, v[k][2] = t.z, v[k][3] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(o));
-            v[k][0] = t.x, v[k][1] = t.y;
-          }
-        } else {
+      for (int e = 0; e < E; ++e) acc[q][e] *= f;
+    }
+    for (int i = s0; i < min(n, s0 + kGroup); i += kBatch) {
+      float v[kBatch][ROWS][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[k][q][e] = next[k][q][e];
+      load(i + kBatch);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          const float ws = __shfl_sync(0xffffffffu, w, q * kGroup + i - s0 + k);  // (0 from n on)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[q][e] = fmaf(ws, v[k][q][e], acc[q][e]);
         }
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float ws = __shfl_sync(0xffffffffu, w, (i + k - s0) & 31);  // (0 from n on)
-        if (i + k < n) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, v[k][e], acc[e]);
-        }
-      }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int j = row / a.n_rep, i = row - j * a.n_rep;
-  const size_t out_row = (static_cast<size_t>(b) * a.N + j) * a.Hq + g * a.n_rep + i;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  for (int q = 0; q < ROWS; ++q) {
+    const float sum = __shfl_sync(0xffffffffu, l, q * kGroup), inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (row0 + q >= rows) continue;
+    const int j = (row0 + q) / a.n_rep, i = row0 + q - j * a.n_rep;
+    const size_t out_row = (static_cast<size_t>(b) * a.N + j) * a.Hq + g * a.n_rep + i;
+    uint32_t out[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[q][e] * inv, acc[q][e + 1] * inv);
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D + lane * E);
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
+    else
+      *to = out[0];
+  }
+}
+
+template <int D, int ROWS>
+cudaError_t launch_merge(const TreeArgs& a, cudaStream_t st) {
+  const int headers = a.headers_by_unit ? a.B * a.Hkv : a.ranges;
+  return launch_pdl(tree_merge_kernel<D, ROWS>, dim3(headers, (a.rows + kMergeWarps * ROWS - 1) / (kMergeWarps * ROWS)),
+                    dim3(32 * kMergeWarps), 0, st, a);
 }
 
 template <int D, int NQ, bool PAGED>
@@ -757,9 +832,8 @@ cudaError_t launch_attn(const TreeArgs& a, const CUtensorMap& km, const CUtensor
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(static_cast<unsigned>(a.ranges) * a.row_ctas), dim3(C::kThreads), C::kSmemBytes, st, km, vm, a);
   if (e != cudaSuccess || a.ranges == 1) return e;
-  const int headers = a.headers_by_unit ? a.B * a.Hkv : a.ranges;
-  return launch_pdl(tree_merge_kernel<D>, dim3(headers, (a.rows + kMergeWarps - 1) / kMergeWarps), dim3(32 * kMergeWarps), 0,
-                    st, a);
+  // partials of a cut unit: about ranges / units, two or three where there are more units
+  return a.headers_by_unit && a.ranges >= 4 * a.B * a.Hkv ? launch_merge<D, 1>(a, st) : launch_merge<D, 4>(a, st);
 }
 
 }  // namespace tree

@@ -624,24 +624,35 @@ def rra_prefill_step(q, k_new, v_new, positions, q_out, k_cache, v_cache, out, b
 
 
 # --------------------------------------------------------------------------- trees of drafted tokens
-def _tree_layout(q, k_cache, v_cache, positions, parents, block_table, tree_lens, out):
-    """(B, N, Hq, D, block-table columns, block_size, num_blocks, max_len, Hkv) of a tree call. The C calls take no
-    element types, so they are checked here, with the shapes."""
-    if q.dim() != 4:
+def _tree_call(q, k_cache, v_cache, positions, parents, block_table, tree_lens, out, k_new=None, v_new=None):
+    """The shapes and pointers that the tree calls have in common, checked: (B, N, Hq, Hkv, D, cache layout, pointers of
+    positions, parents, tree_lens, block_table, k_cache, v_cache). The C calls take no element types."""
+    shape, cache = q.shape, k_cache.shape
+    if len(shape) != 4:
         raise ValueError("q: [B, N, Hq, D]")
-    B, N, Hq, D = q.shape
+    B, N, Hq, D = shape
     if not (q.dtype == k_cache.dtype == v_cache.dtype == out.dtype == _BF16):
         raise TypeError("tree attention takes bf16 queries, caches and outputs")
-    if out.shape != q.shape or k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != D:
+    if out.shape != shape or len(cache) != 4 or v_cache.shape != cache or cache[3] != D:
         raise ValueError("out: the shape of q; k_cache, v_cache: [B, Hkv, max_len, D], or [num_blocks, block_size, Hkv, D]")
-    if block_table is None and k_cache.shape[0] != B:
-        raise ValueError("k_cache, v_cache: a row per sequence")
-    if block_table is not None and (block_table.dtype != _I32 or block_table.dim() != 2 or block_table.shape[0] != B):
-        raise ValueError("block_table: int32 [B, max_blocks_per_seq]")
-    for t, shape, what in ((positions, (B,), "positions"), (parents, (B, N), "parents"), (tree_lens, (B,), "tree_lens")):
-        if t is not None and (t.dtype != _I32 or t.shape != shape):
-            raise ValueError(f"{what}: an int32 tensor of shape {shape}")
-    return (B, N, Hq, D) + _cache_layout(k_cache, block_table)
+    if block_table is None:
+        if cache[0] != B:
+            raise ValueError("k_cache, v_cache: a row per sequence")
+        Hkv, layout = cache[1], (0, 0, 0, cache[2])
+    else:
+        columns = block_table.shape
+        if block_table.dtype != _I32 or len(columns) != 2 or columns[0] != B:
+            raise ValueError("block_table: int32 [B, max_blocks_per_seq]")
+        Hkv, layout = cache[2], (columns[1], cache[1], cache[0], 0)
+    if k_new is not None:
+        if not k_new.dtype == v_new.dtype == _BF16:
+            raise TypeError("tree attention takes bf16 nodes")
+        if not k_new.shape == v_new.shape == (B, N, Hkv, D):
+            raise ValueError("k_new and v_new: [B, N, Hkv, D]")
+    row = (B,)
+    return (B, N, Hq, Hkv, D, layout, _i32(positions, row, "positions"), _i32(parents, (B, N), "parents"),
+            _i32(tree_lens, row, "tree_lens") if tree_lens is not None else None, _ptr(block_table), _ptr(k_cache),
+            _ptr(v_cache))
 
 
 def rra_tree_plan(B: int, N: int, Hq: int, Hkv: int, D: int, max_tokens: int, block_size: int,
@@ -657,32 +668,21 @@ def rra_tree_append(q, k_new, v_new, positions, parents, q_out, k_cache, v_cache
                     rope_base: float = 10000.0, rope_style: int = 0, err_flag=None, stream=None) -> None:
     """RoPE on q / k_new [B, N, H, D] (node j at positions[b] + its depth) and append of the nodes (node j in slot
     positions[b] + j). parents [B, N]: the node that node j follows, -1: the last cached token."""
-    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q, k_cache, v_cache, positions, parents, block_table,
-                                                             tree_lens, q_out)
-    _tree_nodes(q, k_new, v_new, Hkv)
-    st = lib().rra_tree_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(parents), _ptr(tree_lens),
-                               _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, bs, nblk, max_len, B,
-                               N, Hq, Hkv, D, rope_base, rope_style, _ptr(err_flag), _stream(stream, q))
+    B, N, Hq, Hkv, D, layout, pos, par, lens, table, k, v = _tree_call(q, k_cache, v_cache, positions, parents,
+                                                                       block_table, tree_lens, q_out, k_new, v_new)
+    st = lib().rra_tree_append(_ptr(q), _ptr(k_new), _ptr(v_new), pos, par, lens, _ptr(q_out), k, v, table, *layout, B, N,
+                               Hq, Hkv, D, rope_base, rope_style, _ptr(err_flag), _stream(stream, q))
     _check("rra_tree_append", st)
-
-
-def _tree_nodes(q, k_new, v_new, Hkv: int) -> None:
-    if not k_new.dtype == v_new.dtype == _BF16:
-        raise TypeError("tree attention takes bf16 nodes")
-    shape = (q.shape[0], q.shape[1], Hkv, q.shape[3])
-    if k_new.shape != shape or v_new.shape != shape:
-        raise ValueError("k_new and v_new: [B, N, Hkv, D]")
 
 
 def rra_tree_attn(q_rot, k_cache, v_cache, positions, parents, out, block_table=None, tree_lens=None,
                   scale: float = 0.0, num_splits: int = 0, workspace=None, err_flag=None, stream=None) -> None:
     """out[b, j] = attention of q_rot[b, j] over tokens [0, positions[b]), node j's ancestors and node j itself
     (bf16 caches that hold the nodes already)."""
-    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q_rot, k_cache, v_cache, positions, parents, block_table,
-                                                             tree_lens, out)
-    st = lib().rra_tree_attn(_ptr(q_rot), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, _ptr(positions),
-                             _ptr(parents), _ptr(tree_lens), bs, nblk, max_len, _ptr(out), B, N, Hq, Hkv, D, scale,
-                             num_splits, _ptr(workspace), workspace.nbytes if workspace is not None else 0,
+    B, N, Hq, Hkv, D, layout, pos, par, lens, table, k, v = _tree_call(q_rot, k_cache, v_cache, positions, parents,
+                                                                       block_table, tree_lens, out)
+    st = lib().rra_tree_attn(_ptr(q_rot), k, v, table, layout[0], pos, par, lens, *layout[1:], _ptr(out), B, N, Hq, Hkv,
+                             D, scale, num_splits, _ptr(workspace), workspace.nbytes if workspace is not None else 0,
                              _ptr(err_flag), _stream(stream, q_rot))
     _check("rra_tree_attn", st)
 
@@ -691,16 +691,23 @@ def rra_tree_step(q, k_new, v_new, positions, parents, q_out, k_cache, v_cache, 
                   rope_base: float = 10000.0, rope_style: int = 0, scale: float = 0.0, num_splits: int = 0,
                   workspace=None, err_flag=None, stream=None) -> None:
     """The whole step on a tree of drafted tokens: RoPE + append of its nodes, then their attention."""
-    B, N, Hq, D, mbps, bs, nblk, max_len, Hkv = _tree_layout(q, k_cache, v_cache, positions, parents, block_table,
-                                                             tree_lens, out)
-    _tree_nodes(q, k_new, v_new, Hkv)
-    if q_out.shape != q.shape or q_out.dtype != _BF16:
+    B, N, Hq, Hkv, D, layout, pos, par, lens, table, k, v = _tree_call(q, k_cache, v_cache, positions, parents,
+                                                                       block_table, tree_lens, out, k_new, v_new)
+    if q_out.dtype != _BF16 or q_out.shape != q.shape:
         raise ValueError("q_out: bf16, the shape of q")
-    st = lib().rra_tree_step(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(positions), _ptr(parents), _ptr(tree_lens),
-                             _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), mbps, bs, nblk, max_len,
+    st = lib().rra_tree_step(_ptr(q), _ptr(k_new), _ptr(v_new), pos, par, lens, _ptr(q_out), k, v, table, *layout,
                              _ptr(out), B, N, Hq, Hkv, D, rope_base, rope_style, scale, num_splits, _ptr(workspace),
                              workspace.nbytes if workspace is not None else 0, _ptr(err_flag), _stream(stream, q))
-    _check("rra_tree_step", st)
+    if st != 0:
+        raise RraError("rra_tree_step", st)
+
+
+def _cache_pointers(caches, shape, dtype, device: int):
+    """The device pointers of a list of caches alike, as a C array."""
+    for c in caches:
+        if c.shape != shape or c.dtype != dtype or c.get_device() != device or not c.is_contiguous():
+            raise ValueError("the layers' caches: contiguous tensors alike, on the tokens' device")
+    return (_vp * len(caches))(*[c.data_ptr() for c in caches])
 
 
 def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches, block_table=None, tree_lens=None,
@@ -713,53 +720,62 @@ def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches,
     Outputs are made where they are not given.
     """
     ids = draft_tokens.shape
+    if len(ids) != 2:
+        raise ValueError("draft_tokens: [B, N]")
     B, N = ids
-    k_caches = [k_caches] if isinstance(k_caches, torch.Tensor) else k_caches
-    v_caches = [v_caches] if isinstance(v_caches, torch.Tensor) else v_caches
+    if isinstance(k_caches, torch.Tensor):
+        k_caches = (k_caches,)
+    if isinstance(v_caches, torch.Tensor):
+        v_caches = (v_caches,)
     layers = len(k_caches)
     if layers == 0 or len(v_caches) != layers:
         raise ValueError("k_caches, v_caches: the caches of each layer")
     k0 = k_caches[0]
-    shape, dtype, device = k0.shape, k0.dtype, draft_tokens.device
-    code = _dtype_code(k0)
-    pointers = (_vp * layers)(), (_vp * layers)()
-    for at, caches in zip(pointers, (k_caches, v_caches)):
-        for i, c in enumerate(caches):
-            if c.shape != shape or c.dtype != dtype or not c.is_contiguous() or c.device != device:
-                raise ValueError("the layers' caches: contiguous tensors alike, on the tokens' device")
-            at[i] = c.data_ptr()
-    if len(shape) != 4 or (block_table is None and shape[0] != B):
+    cache = k0.shape
+    code, device = _dtype_code(k0), draft_tokens.get_device()
+    k_ptrs = _cache_pointers(k_caches, cache, k0.dtype, device)
+    v_ptrs = _cache_pointers(v_caches, cache, k0.dtype, device)
+    if len(cache) != 4 or (block_table is None and cache[0] != B):
         raise ValueError("caches: [B, Hkv, max_len, D], or [num_blocks, block_size, Hkv, D] with a block table")
     if block_table is not None and (block_table.dtype != _I32 or block_table.dim() != 2 or block_table.shape[0] != B):
         raise ValueError("block_table: int32 [B, max_blocks_per_seq]")
     mbps, bs, nblk, max_len, Hkv = _cache_layout(k0, block_table)
     if choices.dtype != _I32 or choices.shape != ids or not choices.is_cuda:
         raise ValueError("choices: an int32 CUDA tensor of draft_tokens' shape")
-    step = choices.stride(1) if N > 1 else max(1, choices.stride(0))
-    if B > 1 and choices.stride(0) != N * step:
+    row_step, step = choices.stride()
+    if N == 1:
+        step = max(1, row_step)
+    if B > 1 and row_step != N * step:
         choices, step = choices.contiguous(), 1
     row = (B,)
-
-    def output(t, shape, what):
-        if t is None:
-            t = torch.empty(shape, dtype=_I32, device=device)
-            return t, t.data_ptr()
-        return t, _i32(t, shape, what)
-
-    tokens_out, tokens_ptr = output(tokens_out, ids, "tokens_out")
-    n_kept, kept_ptr = output(n_kept, row, "n_kept")
-    nodes_out, nodes_ptr = output(nodes_out, ids, "nodes_out")
-    positions_out, next_ptr = output(positions_out, row, "positions_out")
-    st = lib().rra_tree_keep(_i32(draft_tokens, ids, "draft_tokens"), _i32(parents, ids, "parents"), choices.data_ptr(), step,
-                             _i32(tree_lens, row, "tree_lens") if tree_lens is not None else None,
-                             _i32(positions, row, "positions"), pointers[0], pointers[1], layers, _ptr(block_table), mbps,
-                             bs, nblk, max_len, tokens_ptr, kept_ptr, nodes_ptr, next_ptr, B, N, Hkv, shape[3], code,
-                             _ptr(err_flag), _stream(stream, draft_tokens))
-    _check("rra_tree_keep", st)
+    tokens, pos = _i32(draft_tokens, ids, "draft_tokens"), _i32(positions, row, "positions")
+    if tokens_out is None:
+        tokens_out = torch.empty_like(draft_tokens)
+    if nodes_out is None:
+        nodes_out = torch.empty_like(draft_tokens)
+    if n_kept is None:
+        n_kept = torch.empty_like(positions)
+    if positions_out is None:
+        positions_out = torch.empty_like(positions)
+    st = lib().rra_tree_keep(tokens, _i32(parents, ids, "parents"), choices.data_ptr(), step,
+                             _i32(tree_lens, row, "tree_lens") if tree_lens is not None else None, pos, k_ptrs, v_ptrs,
+                             layers, _ptr(block_table), mbps, bs, nblk, max_len, _i32(tokens_out, ids, "tokens_out"),
+                             _i32(n_kept, row, "n_kept"), _i32(nodes_out, ids, "nodes_out"),
+                             _i32(positions_out, row, "positions_out"), B, N, Hkv, cache[3], code, _ptr(err_flag),
+                             _stream(stream, draft_tokens))
+    if st != 0:
+        raise RraError("rra_tree_keep", st)
     return tokens_out, n_kept, nodes_out, positions_out
 
 
 # --------------------------------------------------------------------------- log probabilities of tokens
+def _given(t, shape, dtype, what: str) -> int:
+    """The pointer of an output that the caller brings."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what}: a {dtype} tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
 def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entropy=None, top_logprobs=None,
                        top_tokens=None, err_flag=None, stream=None) -> tuple:
     """(log probabilities of ``tokens``, entropies, log probabilities of the top_k most likely tokens, these tokens)
@@ -769,39 +785,52 @@ def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entro
     int32 tensors of the shapes [...] or [..., T], [...], [..., top_k] and [..., top_k], made where they are not given; without
     ``tokens`` the first is None, without ``top_k`` the last two are.
     """
-    rows, V = logits.shape[:-1], logits.shape[-1]
-    if len(rows) == 1:
-        (B,), N, sb, st_ = rows, 1, logits.stride(0), 0
-    elif len(rows) == 2:
-        (B, N), sb, st_ = rows, logits.stride(0), logits.stride(1)
+    shape, strides, dt = logits.shape, logits.stride(), logits.dtype
+    rows = shape[:-1]
+    if len(shape) == 2:
+        (B, V), N, sb, st_ = shape, 1, strides[0], 0
+    elif len(shape) == 3:
+        (B, N, V), sb, st_ = shape, strides[0], strides[1]
     else:
         raise ValueError("logits: [rows, V] or [B, N, V]")
-    code = _dtype_code(logits)
-    if not logits.is_cuda or (logits.stride(-1) != 1 and V > 1):
+    code = RRA_F32 if dt == _F32 else _dtype_code(logits)
+    if not logits.is_cuda or (strides[-1] != 1 and V > 1):
         raise ValueError("logits: a CUDA tensor with a unit last stride")
-    T, device = 0, logits.device
+    # (outputs made here are not checked: the call takes longer on the host than on the GPU)
+    T, tokens_ptr, lp_ptr, top_lp_ptr, top_ptr = 0, None, None, None, None
     if tokens is not None:
-        if tokens.shape[:len(rows)] != rows or tokens.dim() > len(rows) + 1:
+        given = tokens.shape
+        if given == rows:
+            T = 1
+        elif given[:-1] == rows:
+            T = given[-1]
+        else:
             raise ValueError("tokens: [...] or [..., T] for logits [..., V]")
-        T = tokens.shape[-1] if tokens.dim() > len(rows) else 1
-
-    def output(t, shape, dtype, what):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=device)
-            return t, t.data_ptr()
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError(f"{what}: a {dtype} tensor of shape {tuple(shape)}")
-        return t, _ptr(t)
-
-    lp_ptr = top_lp_ptr = top_ptr = None
-    if tokens is not None:
-        logprobs, lp_ptr = output(logprobs, tokens.shape, _F32, "logprobs")
-    entropy, h_ptr = output(entropy, rows, _F32, "entropy")
+        tokens_ptr = _i32(tokens, given, "tokens")
+        if logprobs is None:
+            logprobs = logits.new_empty(given, dtype=_F32)
+            lp_ptr = logprobs.data_ptr()
+        else:
+            lp_ptr = _given(logprobs, given, _F32, "logprobs")
+    if entropy is None:
+        entropy = logits.new_empty(rows, dtype=_F32)
+        h_ptr = entropy.data_ptr()
+    else:
+        h_ptr = _given(entropy, rows, _F32, "entropy")
     if top_k > 0:
-        top_logprobs, top_lp_ptr = output(top_logprobs, rows + (top_k,), _F32, "top_logprobs")
-        top_tokens, top_ptr = output(top_tokens, rows + (top_k,), _I32, "top_tokens")
-    st = lib().rra_token_logprobs(logits.data_ptr(), sb, st_,
-                                  _i32(tokens, tokens.shape, "tokens") if tokens is not None else None, T, lp_ptr, h_ptr,
-                                  top_k, top_lp_ptr, top_ptr, B, N, V, code, _ptr(err_flag), _stream(stream, logits))
-    _check("rra_token_logprobs", st)
+        top = rows + (top_k,)
+        if top_logprobs is None:
+            top_logprobs = logits.new_empty(top, dtype=_F32)
+            top_lp_ptr = top_logprobs.data_ptr()
+        else:
+            top_lp_ptr = _given(top_logprobs, top, _F32, "top_logprobs")
+        if top_tokens is None:
+            top_tokens = logits.new_empty(top, dtype=_I32)
+            top_ptr = top_tokens.data_ptr()
+        else:
+            top_ptr = _given(top_tokens, top, _I32, "top_tokens")
+    st = lib().rra_token_logprobs(logits.data_ptr(), sb, st_, tokens_ptr, T, lp_ptr, h_ptr, top_k, top_lp_ptr, top_ptr, B, N,
+                                  V, code, _ptr(err_flag), _stream(stream, logits))
+    if st != 0:
+        raise RraError("rra_token_logprobs", st)
     return logprobs, entropy, top_logprobs, top_tokens
