@@ -111,13 +111,16 @@ __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool
   return s;
 }
 
-// The key tiles of all units in one line, cut into `ranges` runs whose lengths differ by one at most.
+// The key tiles of all units in one line, cut into `ranges` runs whose lengths differ by one at most. Where the units are
+// equally long and `ranges` is a multiple of their number, every unit starts with a run of its own.
 struct Cut {
-  int each, more;  // the first `more` runs have each + 1 tiles
-  __device__ __forceinline__ int border(int r) const { return each * r + min(r, more); }
-  __device__ __forceinline__ int range_of(int t) const {
-    const int split = more * (each + 1);
-    return t < split ? t / (each + 1) : more + (t - split) / max(each, 1);
+  int total, ranges;
+  __device__ __forceinline__ int border(int r) const {
+    if (total < 1 << 21) return static_cast<int>(static_cast<uint32_t>(total) * r / static_cast<uint32_t>(ranges));  // (at most 1024 of them)
+    return static_cast<int>(static_cast<int64_t>(total) * r / ranges);
+  }
+  __device__ __forceinline__ int range_of(int t) const {  // the last r with border(r) <= t
+    return static_cast<int>((static_cast<int64_t>(t + 1) * ranges - 1) / total);
   }
 };
 
@@ -130,7 +133,9 @@ struct Start {
 };
 
 // Adds up the sequences' tiles and finds the start of range r (all threads of the CTA; r past the ranges in use: t0 = t1).
-// Ranges of at least min_tiles tiles, unless there are more units than such ranges: so some of a.ranges may stay unused.
+// Ranges of at least min_tiles tiles, unless there are more units than such ranges; and a whole number of them per unit where
+// that leaves no more than every ninth out (a CTA that goes from one unit to the next takes some 3 us longer: one user's
+// 4000 tokens). So some of a.ranges may stay unused.
 template <int THREADS>
 __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) {
   const int per = (a.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
@@ -162,9 +167,16 @@ __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) 
     total += s->sums[0][w];
     units += s->sums[1][w] * a.Hkv;
   }
-  const int ranges = min(a.ranges, max((total + a.min_tiles - 1) / a.min_tiles, max(units, 1)));
-  if (r < ranges) {
-    const Cut cut{total / ranges, total % ranges};
+  int ranges = min(a.ranges, max((total + a.min_tiles - 1) / a.min_tiles, max(units, 1)));
+  if (units > 0 && units <= ranges) {
+    const int up = (ranges + units - 1) / units * units, down = ranges / units;
+    if (up <= min(a.ranges, total))  // (no range without tiles)
+      ranges = up;
+    else if (down >= 8)
+      ranges = down * units;
+  }
+  if (r < ranges && total > 0) {
+    const Cut cut{total, ranges};
     const int t0 = cut.border(r), t1 = cut.border(r + 1);
     if (t0 < t1 && before <= t0 && t0 < before + mine) {  // one thread
       int b = b0;
@@ -459,20 +471,35 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       const int j = row / a.n_rep;
       return (static_cast<size_t>(b) * a.N + j) * a.Hq + g * a.n_rep + (row - j * a.n_rep);
     };
-    auto load_q = [&]() {  // the unit's query row
-      const bool real = row < u.seq.n * a.n_rep;
-      const size_t q_row = out_row_of(u.b, u.g);
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + q_row * D);
+    auto load_q = [&]() {  // the unit's query rows
+      const int live = u.seq.n * a.n_rep;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q));
       uint4 qv[D / 8];
+      if constexpr (NQ == 2) {
+        // Into the Q tile (K-major, 128-byte swizzle): this warp's rows, 16 lanes a row (8 at head dim 64), so that loads are
+        // whole lines. (A row per thread: one user's 131072 tokens 1.3 us longer.)
+        constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;  // lanes per row, rows per load
+        const int x = lane % kLanes, row0 = first_row + k * kRows + (r & ~31) + lane / kLanes;
+        int j = row0 / a.n_rep, i = row0 - j * a.n_rep;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) qv[c] = real ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (NQ == 2) {  // into the Q tile (K-major, 128-byte swizzle)
-        uint8_t* dst = smem + k * C::kHalves * C::kQHalfBytes + r * 128;
+        for (int c = 0; c < D / 8; ++c) {
+          qv[c] = row0 + c * kRowsPer < live ? __ldcg(q + ((static_cast<size_t>(u.b) * a.N + j) * a.Hq + u.g * a.n_rep + i) * kLanes + x)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+          for (i += kRowsPer; i >= a.n_rep; i -= a.n_rep) ++j;
+        }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kQHalfBytes + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
+        for (int c = 0; c < D / 8; ++c) {
+          const int rr = (r & ~31) + c * kRowsPer + lane / kLanes;
+          *reinterpret_cast<uint4*>(smem + (k * C::kHalves + (x >> 3)) * C::kQHalfBytes + rr * 128 + (((x & 7) ^ (rr & 7)) << 4)) = qv[c];
+        }
         tc::fence_smem_to_async();
-      } else {  // into Tensor Memory: dims (2c, 2c + 1) in column kColQ + c
+      } else {
+        // Into Tensor Memory, a row per lane: dims (2c, 2c + 1) in column kColQ + c. (By lines and through shared
+        // memory: 2 us longer.)
+        const bool real = row < live;
+        const uint4* src = q + out_row_of(u.b, u.g) * (D / 8);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) qv[c] = real ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
         uint32_t qw[D / 2];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
