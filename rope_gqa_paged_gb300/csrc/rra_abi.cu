@@ -421,7 +421,7 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
   const int tile = rra::tree_tile(D, p->nq);
   const int64_t tiles = int64_t(B) * Hkv * ((max_tokens + tile - 1) / tile);
-  if (tiles > INT32_MAX) return RRA_ERANGE;
+  if (tiles + int64_t(B) * Hkv * 4 > INT32_MAX) return RRA_ERANGE;
   if (requested > 0) {
     p->ranges = std::min(requested, rra::kMaxSplits);
   } else {
@@ -1676,6 +1676,7 @@ static int tree_attn_launch(const void* q_rot, const void* k_cache, const void* 
   a.row_ctas = p.row_ctas;
   a.ranges = p.ranges;
   a.min_tiles = p.min_tiles;
+  a.unit_tiles = p.nq == 2 ? 4 : 3;
   if (p.ranges > 1) {
     uint8_t* base = static_cast<uint8_t*>(workspace);
     a.ws_o = reinterpret_cast<float*>(base);

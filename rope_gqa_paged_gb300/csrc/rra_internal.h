@@ -230,6 +230,7 @@ struct TreeArgs {
   int rows;                     // N * n_rep
   int nq, row_ctas;             // row tiles per CTA, CTAs for the rows of a KV head
   int ranges, min_tiles;        // runs of key tiles, the least tiles of one
+  int unit_tiles;               // what a CTA takes for one more unit, in key tiles
   float* ws_o;                  // [ranges, 2, rows, D] unnormalised partial outputs (ranges > 1)
   float* ws_ml;                 // [ranges, 2, rows, 2] (running max in log2 units, running sum)
   int4* headers;                // what tree_merge_kernel joins: (partials, first range, unit, live rows), 0 partials: nothing

@@ -78,7 +78,7 @@ struct Cfg {
   // q_ready, ring_full[kRing], ring_empty[kRing], s_full[NQ], p_full[NQ][kParts], o_done
   static constexpr int kNumBars = 1 + 2 * kRing + NQ + NQ * kParts + 1;
   static constexpr int kOffStart = kOffBar + kNumBars * 8;   // Start
-  static constexpr int kOffUnits = kOffStart + 144;          // Units, one per softmax warp
+  static constexpr int kOffUnits = kOffStart + 160;          // Units, one per softmax warp
   static constexpr int kOffTmemSlot = kOffUnits + kWarps * 48;
   static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
   // + producer warp + MMA warp; NQ 2: and two idle ones, so that a whole warpgroup gives registers to the softmax
@@ -97,10 +97,14 @@ struct Seq {
   int p, n, tiles;
   bool refused;
 };
-__device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool flag = false) {
-  Seq s;
-  s.p = __ldcg(a.positions + b);
-  s.n = a.lens != nullptr ? __ldcg(a.lens + b) : a.N;
+struct Raw {
+  int p, n;
+};
+__device__ __forceinline__ Raw raw_sequence(const TreeArgs& a, int b) {
+  return {__ldcg(a.positions + b), a.lens != nullptr ? __ldcg(a.lens + b) : a.N};
+}
+__device__ __forceinline__ Seq sequence(const TreeArgs& a, const Raw& raw, int tile, bool flag = false) {
+  Seq s{raw.p, raw.n, 0, false};
   if (s.n < 0 || s.n > a.N) {
     if (flag) flag_error(a.err, RRA_ERR_SEQ_LEN);
     s.n = min(max(s.n, 0), a.N);
@@ -110,11 +114,15 @@ __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool
   s.tiles = s.refused || s.n == 0 ? 0 : (s.p + s.n - 1) / tile + 1;
   return s;
 }
+__device__ __forceinline__ Seq sequence(const TreeArgs& a, int b, int tile, bool flag = false) {
+  return sequence(a, raw_sequence(a, b), tile, flag);
+}
 
-// The key tiles of all units in one line, cut into `ranges` runs whose lengths differ by one at most. Where the units are
-// equally long and `ranges` is a multiple of their number, every unit starts with a run of its own.
+// The units in one line, each `extra` places (what a CTA takes for one more unit, in key tiles) and its key tiles, cut into
+// `ranges` runs whose lengths differ by one at most. A border among the extra places is the start of the unit.
+// Where the units are equally long and `ranges` is a multiple of their number, every unit starts with a run of its own.
 struct Cut {
-  int total, ranges;
+  int total, ranges, extra;
   __device__ __forceinline__ int border(int r) const {
     if (total < 1 << 21) return static_cast<int>(static_cast<uint32_t>(total) * r / static_cast<uint32_t>(ranges));  // (at most 1024 of them)
     return static_cast<int>(static_cast<int64_t>(total) * r / ranges);
@@ -124,7 +132,7 @@ struct Cut {
   }
 };
 
-// Where a range starts: tiles [t0, t1) of all, from tile `off` of sequence b's Hkv x tiles on.
+// Where a range starts: places [t0, t1) of the line, from place `off` of sequence b's on.
 struct Start {
   int t0, t1, b, off;
   Cut cut;
@@ -140,51 +148,59 @@ template <int THREADS>
 __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) {
   const int per = (a.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
   Seq seq{0, 0, 0, false};
-  int mine = 0, seqs = 0;
+  int tiles = 0, seqs = 0;
   for (int b = b0; b < b1; ++b) {
     seq = sequence(a, b, tile, flag);
-    mine += seq.tiles * a.Hkv;
+    tiles += seq.tiles;
     seqs += seq.tiles > 0;
   }
-  int incl = mine;
+  int tiles_to = tiles, seqs_to = seqs;  // inclusive sums
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
+    const int x = __shfl_up_sync(0xffffffffu, tiles_to, d), y = __shfl_up_sync(0xffffffffu, seqs_to, d);
+    if (lane >= d) {
+      tiles_to += x;
+      seqs_to += y;
+    }
   }
-  seqs = __reduce_add_sync(0xffffffffu, seqs);
   if (lane == 31) {
-    s->sums[0][warp] = incl;
-    s->sums[1][warp] = seqs;
+    s->sums[0][warp] = tiles_to;
+    s->sums[1][warp] = seqs_to;
   }
   if (threadIdx.x == 0) s->t0 = s->t1 = 0;
   __syncthreads();
-  int before = incl - mine, total = 0, units = 0;
+  int tiles_before = tiles_to - tiles, seqs_before = seqs_to - seqs, total = 0, units = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += s->sums[0][w];
-    total += s->sums[0][w];
+    if (w < warp) {
+      tiles_before += s->sums[0][w];
+      seqs_before += s->sums[1][w];
+    }
+    total += s->sums[0][w] * a.Hkv;
     units += s->sums[1][w] * a.Hkv;
   }
-  int ranges = min(a.ranges, max((total + a.min_tiles - 1) / a.min_tiles, max(units, 1)));
+  int ranges = min(a.ranges, max((total + a.min_tiles - 1) / a.min_tiles, max(units, 1))), extra = a.unit_tiles;
   if (units > 0 && units <= ranges) {
     const int up = (ranges + units - 1) / units * units, down = ranges / units;
     if (up <= min(a.ranges, total))  // (no range without tiles)
       ranges = up;
     else if (down >= 8)
       ranges = down * units;
+    if (ranges % units == 0) extra = 0;
   }
   if (r < ranges && total > 0) {
-    const Cut cut{total, ranges};
-    const int t0 = cut.border(r), t1 = cut.border(r + 1);
+    const Cut cut{total + units * extra, ranges, extra};
+    int before = (tiles_before + seqs_before * extra) * a.Hkv;
+    const int mine = (tiles + seqs * extra) * a.Hkv, t0 = cut.border(r), t1 = cut.border(r + 1);
     if (t0 < t1 && before <= t0 && t0 < before + mine) {  // one thread
       int b = b0;
       if (per > 1) {
         for (;; ++b) {
           seq = sequence(a, b, tile);
-          if (t0 < before + seq.tiles * a.Hkv) break;
-          before += seq.tiles * a.Hkv;
+          const int span = seq.tiles > 0 ? (seq.tiles + extra) * a.Hkv : 0;
+          if (t0 < before + span) break;
+          before += span;
         }
       }
       s->t0 = t0;
@@ -198,23 +214,31 @@ __device__ void locate(const TreeArgs& a, int tile, int r, bool flag, Start* s) 
   __syncthreads();
 }
 
-// A range's units one after the other: key tiles [j0, j1) of KV head g of sequence b.
+// A range's units one after the other: key tiles [j0, j1) of KV head g of sequence b; `rest` of its places are left
+// for later ranges.
 struct Units {
-  int b, g, j0, j1, off, left;
+  int b, g, j0, j1, rest, off, left, extra;
   Seq seq;
-  __device__ __forceinline__ Units(const Start& s) : b(s.b), g(0), j0(0), j1(0), off(s.off), left(s.t1 - s.t0), seq(s.seq) {}
-  __device__ __forceinline__ bool next(const TreeArgs& a, int tile, int first_row) {
+  __device__ __forceinline__ Units(const Start& s)
+      : b(s.b), g(0), j0(0), j1(0), rest(0), off(s.off), left(s.t1 - s.t0), extra(s.cut.extra), seq(s.seq) {}
+  // `ahead`: what is known of sequence b + 1, loaded when b began.
+  __device__ __forceinline__ bool next(const TreeArgs& a, int tile, int first_row, Raw& ahead) {
     while (left > 0) {
-      while (off >= seq.tiles * a.Hkv) {
+      while (seq.tiles == 0 || off >= (seq.tiles + extra) * a.Hkv) {
         off = 0;
-        seq = sequence(a, ++b, tile);
+        ++b;
+        seq = sequence(a, ahead, tile);
+        ahead = raw_sequence(a, min(b + 1, a.B - 1));
       }
-      g = off / seq.tiles;
-      j0 = off - g * seq.tiles;
-      j1 = min(seq.tiles, j0 + left);
-      off += j1 - j0;
-      left -= j1 - j0;
-      if (seq.n * a.n_rep > first_row) return true;  // (a smaller tree leaves this CTA's rows empty)
+      const int span = seq.tiles + extra;
+      g = off / span;
+      const int from = off - g * span, take = min(span - from, left);
+      j0 = max(from - extra, 0);
+      j1 = max(from + take - extra, 0);
+      rest = span - from - take;
+      off += take;
+      left -= take;
+      if (j1 > j0 && seq.n * a.n_rep > first_row) return true;  // (a smaller tree leaves this CTA's rows empty)
     }
     return false;
   }
@@ -255,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   uint64_t* p_full = s_full + NQ;
   uint64_t* o_done = p_full + NQ * kParts;
   Start* start = reinterpret_cast<Start*>(smem + C::kOffStart);
-  static_assert(sizeof(Start) <= 144 && sizeof(Units) <= 48 && sizeof(Units) % 4 == 0 && C::kOffSees % 16 == 0 && kTreeMaxNodes == 128, "layout");
+  static_assert(sizeof(Start) <= 160 && sizeof(Units) <= 48 && sizeof(Units) % 4 == 0 && C::kOffSees % 16 == 0 && kTreeMaxNodes == 128, "layout");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffTmemSlot);
 
   if (threadIdx.x == 0) {
@@ -297,6 +321,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
   if (warp >= C::kWarps) {
    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
    Units u(*start);
+   Raw ahead = raw_sequence(a, min(u.b + 1, a.B - 1));
    if (warp == kProducerWarp) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
@@ -307,20 +332,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     const int box = PAGED ? min(bs, kTile) : kTile;  // rows per TMA box, as the tensor maps were encoded
     bool ok = true, waited = !a.after_append;
     uint32_t issued = 0;
-    while (ok && u.next(a, kTile, first_row)) {
+    int4 h = make_int4(0, 0, 0, 0);
+    while (ok && u.next(a, kTile, first_row, ahead)) {
       const int L = u.seq.p + u.seq.n;
       if (first_row == 0 && lane == 0 && a.headers != nullptr) {
-        // a unit that starts here and goes on in later ranges is merged for this range's header
-        int4 h = make_int4(0, 0, 0, 0);
+        // a unit that starts here and goes on in later ranges (it is this one's last) is merged for this header
+        h = make_int4(0, 0, 0, 0);
         if (u.j0 == 0 && !u.whole()) {
-          const int end = start->t1 + (u.seq.tiles - u.j1);  // the unit's end among all tiles
+          const int end = start->t1 + u.rest;  // the unit's end in the line
           h = make_int4(start->cut.range_of(end - 1) - range + 1, range, u.b * a.Hkv + u.g, u.seq.n * a.n_rep);
         }
-        if (a.headers_by_unit) {
-          if (u.j0 == 0) a.headers[u.b * a.Hkv + u.g] = h;
-        } else if (u.left == 0) {
-          a.headers[range] = h;
-        }
+        if (a.headers_by_unit && u.j0 == 0) a.headers[u.b * a.Hkv + u.g] = h;
       }
       const int32_t* row = a.block_table + static_cast<size_t>(u.b) * a.max_blocks_per_seq;
       // block where this lane's box of tile j starts (the id loads a tile ahead of its use)
@@ -367,6 +389,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
         }
       }
     }
+    if (first_row == 0 && lane == 0 && a.headers != nullptr && !a.headers_by_unit) a.headers[range] = h;
     pad_rows(a, D, lane, 32);
     if (lane == 0) {
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
@@ -386,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       const uint64_t q_desc = tc::sw128_desc(base, 1024, 1024);
       bool ok = true;
       uint32_t c = 0, units = 0;  // the CTA's tiles and units so far
-      while (ok && u.next(a, kTile, first_row)) {
+      while (ok && u.next(a, kTile, first_row, ahead)) {
         const bool short_seq = u.seq.p < kShortRow;
         ok = mbar_wait(q_ready, units & 1u);
         tc::fence_after_sync();
@@ -458,9 +481,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     uint4* sees = reinterpret_cast<uint4*>(smem + C::kOffSees);
     // The warp's place in the list of units, in shared memory: S takes the registers.
     Units& u = *reinterpret_cast<Units*>(smem + C::kOffUnits + 48 * warp);
+    Raw ahead = raw_sequence(a, min(start->b + 1, a.B - 1));  // (lane 0's counts)
     auto advance = [&]() -> bool {
       __syncwarp();
-      const int more = __shfl_sync(0xffffffffu, lane == 0 && u.next(a, kTile, first_row) ? 1 : 0, 0);
+      const int more = __shfl_sync(0xffffffffu, lane == 0 && u.next(a, kTile, first_row, ahead) ? 1 : 0, 0);
       __syncwarp();
       return more != 0;
     };
@@ -523,19 +547,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       const int p = u.seq.p, j0 = u.j0, j1 = u.j1;
       const bool short_seq = p < kShortRow;
       const bool warp_real = first_row + k * kRows + (r & ~31) < u.seq.n * a.n_rep;  // any row of this warp
-      // the row's node and its ancestors, one bit each (kept in shared memory: every register counts below)
-      if (warp_real && j1 * kTile > p) {
-        uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
-        int up[kTreeMaxNodes / 32];  // parents of nodes lane, lane + 32, ...
+      // The row's node and its ancestors, one bit each: parents now, the bits when the first tile with nodes comes.
+      int up[kTreeMaxNodes / 32];  // parents of nodes lane, lane + 32, ...
+      const bool has_nodes = warp_real && j1 * kTile > p;
+      if (has_nodes) {
 #pragma unroll
         for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
           const int n = 32 * w + lane;
           up[w] = n < u.seq.n ? __ldcg(a.parents + static_cast<size_t>(u.b) * a.N + n) : -1;
-          if (up[w] < -1 || up[w] >= n) {
+        }
+      }
+      auto find_ancestors = [&]() {  // (kept in shared memory: every register counts below)
+#pragma unroll
+        for (int w = 0; w < kTreeMaxNodes / 32; ++w)
+          if (up[w] < -1 || up[w] >= 32 * w + lane) {
             flag_error(a.err, RRA_ERR_TREE);
             up[w] = -1;
           }
-        }
+        uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0;
         int n = row < u.seq.n * a.n_rep ? row / a.n_rep : -1;
         while (__any_sync(0xffffffffu, n >= 0)) {  // (parents come before their children)
           const uint32_t bit = n >= 0 ? 1u << (n & 31) : 0u;
@@ -549,9 +578,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
           n = w < 0 ? -1 : w == 0 ? x0 : w == 1 ? x1 : w == 2 ? x2 : x3;
         }
         sees[threadIdx.x] = make_uint4(s0, s1, s2, s3);
-      }
+      };
+      const int first_nodes = max(j0, p / kTile);  // the first tile of this part that may have nodes
       float m_use = -INFINITY, l = 0.f;  // running max (log2 units) and sum
       for (int j = j0; j < j1; ++j, ++c) {
+        if (has_nodes && j == first_nodes) find_ancestors();
         if (!warp_wait(&s_full[k], c & 1u)) {  // S_k is there, and every MMA issued before it is complete
           ok = false;
           break;
