@@ -104,7 +104,9 @@ struct Vec<float> {
                    __uint_as_float(w.w));
   }
   static constexpr int kPairs = 2;
-  static __device__ __forceinline__ void clamped(const uint4& w, float bound, uint64_t (&x)[2]) {
+  using Bound = float;
+  static __device__ __forceinline__ Bound make_bound(float b) { return b; }
+  static __device__ __forceinline__ void clamped(const uint4& w, Bound bound, uint64_t (&x)[2]) {
     x[0] = pack2(max_nan(__uint_as_float(w.x), bound), max_nan(__uint_as_float(w.y), bound));
     x[1] = pack2(max_nan(__uint_as_float(w.z), bound), max_nan(__uint_as_float(w.w), bound));
   }
@@ -119,9 +121,11 @@ struct Vec<__nv_bfloat16> {
     return max_nan(m, max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)));
   }
   static constexpr int kPairs = 4;
-  static __device__ __forceinline__ void clamped(const uint4& w, float bound, uint64_t (&x)[4]) {
-    const __nv_bfloat16 b = __float2bfloat16_rd(bound);
-    const uint32_t bb = static_cast<uint32_t>(__bfloat16_as_ushort(b)) * 0x10001u;
+  using Bound = uint32_t;  // twice
+  static __device__ __forceinline__ Bound make_bound(float b) {
+    return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rd(b))) * 0x10001u;
+  }
+  static __device__ __forceinline__ void clamped(const uint4& w, Bound bb, uint64_t (&x)[4]) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -454,6 +458,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
   // ---- (m, S, U), one pass
   Stats st{-INFINITY, 0.f, 0.f};
   int entry = t, in_entry = 0;
+  bool plain = true;
+  uint64_t minus_m = 0;
+  typename Vec<T>::Bound bound{};
   auto batch = [&](const uint4 (&w)[kBatch]) {
     float mx = -INFINITY;
 #pragma unroll
@@ -465,12 +472,17 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
         entry += kThreads;
       }
     }
-    if (!(mx <= st.m)) st.move_to(mx);  // (a NaN too: it makes m and the sums NaN)
-    // A logit far below m adds 0 to both sums, wherever it is: held at a bound, so that -inf is no infinity to
-    // multiply 0 with. (e^-150 is 0 in float32; |m| / 16 so that the bound is another number than m.)
-    const float m0 = st.m == -INFINITY ? 0.f : st.m, bound = m0 - fmaf(fabsf(m0), 0x1p-4f, 150.f);
-    if (bound > -1e38f) {
-      const uint64_t minus_m = pack2(-m0, -m0), log2e = pack2(kLog2e, kLog2e);
+    if (!(mx <= st.m)) {  // (a NaN too: it makes m and the sums NaN)
+      st.move_to(mx);
+      // A logit far below m adds 0 to both sums, wherever it is: held at a bound, so that -inf is no infinity to
+      // multiply 0 with. (e^-150 is 0 in float32; |m| / 16 so that the bound is another number than m.)
+      const float low = mx - fmaf(fabsf(mx), 0x1p-4f, 150.f);
+      plain = !(low > -1e38f);
+      bound = Vec<T>::make_bound(low);
+      minus_m = pack2(-mx, -mx);
+    }
+    if (!plain) {
+      const uint64_t log2e = pack2(kLog2e, kLog2e);
       uint64_t s2[2] = {0, 0}, u2[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -486,7 +498,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
       const uint64_t s = add2(s2[0], s2[1]), u = add2(u2[0], u2[1]);
       st.s += lo2(s) + hi2(s);
       st.u += lo2(u) + hi2(u);
-    } else {  // (nothing but values near the type's lowest so far)
+    } else {  // (nothing but -inf, or values near the type's lowest, so far; or a NaN)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         float x[E];
@@ -504,8 +516,13 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
       if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[s], (n / kRing) & 1))) break;
       const uint4* in = reinterpret_cast<const uint4*>(smem + s * kStageBytes) + t;
       uint4 w[kBatch];
+      if (n + 1 < batches) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) w[i] = v + i * kThreads < part.v1 ? in[i * kThreads] : Vec<T>::none();
+        for (int i = 0; i < kBatch; ++i) w[i] = in[i * kThreads];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) w[i] = v + i * kThreads < part.v1 ? in[i * kThreads] : Vec<T>::none();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[s]);
       batch(w);
@@ -610,28 +627,33 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
     }
     return;
   }
-  Key* kept = reinterpret_cast<Key*>(smem);  // (the ring is done)
-  static_assert(kRing * kStageBytes >= kMaxFound * 8, "they fit");
-  // the k largest of all keys: those that reach a bound made in the same way, sorted by counting
-  Key mine_of[kMaxFound / kThreads];
-  uint32_t best = 0;
+  // the k largest of all keys, sorted by counting; of several CTAs' those that reach a bound made in the same way
+  const Key* kept = all;
+  int n = sh.counts[0];
+  if (C > 1) {
+    Key* list = reinterpret_cast<Key*>(smem);  // (the ring is done)
+    static_assert(kRing * kStageBytes >= kMaxFound * 8, "they fit");
+    Key mine_of[kMaxFound / kThreads];
+    uint32_t best = 0;
 #pragma unroll
-  for (int i = 0; i < kMaxFound / kThreads; ++i) {
-    const int at = t + i * kThreads, c = at / places;
-    mine_of[i] = c < C && at - c * places < sh.counts[c] ? all[at] : 0;
-    best = max(best, static_cast<uint32_t>(mine_of[i] >> 32));
+    for (int i = 0; i < kMaxFound / kThreads; ++i) {
+      const int at = t + i * kThreads, c = at / places;
+      mine_of[i] = c < C && at - c * places < sh.counts[c] ? all[at] : 0;
+      best = max(best, static_cast<uint32_t>(mine_of[i] >> 32));
+    }
+    const uint32_t bound32 = common_bound(best, k, sh);
+#pragma unroll
+    for (int i = 0; i < kMaxFound / kThreads; ++i)
+      if (mine_of[i] != 0 && static_cast<uint32_t>(mine_of[i] >> 32) >= bound32) list[atomicAdd(&sh.kept, 1)] = mine_of[i];
+    sync_readers();
+    kept = list;
+    n = sh.kept;
   }
-  const uint32_t bound = C > 1 ? common_bound(best, k, sh) : 0;
-#pragma unroll
-  for (int i = 0; i < kMaxFound / kThreads; ++i)
-    if (mine_of[i] != 0 && static_cast<uint32_t>(mine_of[i] >> 32) >= bound) kept[atomicAdd(&sh.kept, 1)] = mine_of[i];
-  sync_readers();
-  const int n = sh.kept;
   for (int i = t; i < n; i += kThreads) {
     const Key key = kept[i];
     int larger = 0;
     for (int j = 0; j < n; ++j) larger += kept[j] > key;
-    if (larger < k) {
+    if (key != 0 && larger < k) {
       a.top_tokens[r * k + larger] = key_index(key);
       a.top_logprobs[r * k + larger] = (key_value(key) - s.m) - log_s;
     }
