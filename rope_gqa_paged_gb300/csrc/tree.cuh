@@ -547,17 +547,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       const int p = u.seq.p, j0 = u.j0, j1 = u.j1;
       const bool short_seq = p < kShortRow;
       const bool warp_real = first_row + k * kRows + (r & ~31) < u.seq.n * a.n_rep;  // any row of this warp
-      // The row's node and its ancestors, one bit each: parents now, the bits when the first tile with nodes comes.
+      // The row's node and its ancestors, one bit each: parents now, the bits when the first tile with nodes comes (the
+      // parents then too where S takes 128 of 168 registers).
+      constexpr bool kParentsAhead = NQ == 2 || kTile == 64;
       int up[kTreeMaxNodes / 32];  // parents of nodes lane, lane + 32, ...
       const bool has_nodes = warp_real && j1 * kTile > p;
-      if (has_nodes) {
+      auto load_parents = [&]() {
 #pragma unroll
         for (int w = 0; w < kTreeMaxNodes / 32; ++w) {
           const int n = 32 * w + lane;
           up[w] = n < u.seq.n ? __ldcg(a.parents + static_cast<size_t>(u.b) * a.N + n) : -1;
         }
-      }
+      };
+      if (kParentsAhead && has_nodes) load_parents();
       auto find_ancestors = [&]() {  // (kept in shared memory: every register counts below)
+        if (!kParentsAhead) load_parents();
 #pragma unroll
         for (int w = 0; w < kTreeMaxNodes / 32; ++w)
           if (up[w] < -1 || up[w] >= 32 * w + lane) {

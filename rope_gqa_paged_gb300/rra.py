@@ -796,7 +796,7 @@ def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entro
     code = RRA_F32 if dt == _F32 else _dtype_code(logits)
     if not logits.is_cuda or (strides[-1] != 1 and V > 1):
         raise ValueError("logits: a CUDA tensor with a unit last stride")
-    # (outputs made here are not checked: the call takes longer on the host than on the GPU)
+    # (outputs made here are not checked, and made by the cheapest calls: this one takes longer on the host than on the GPU)
     T, tokens_ptr, lp_ptr, top_lp_ptr, top_ptr = 0, None, None, None, None
     if tokens is not None:
         given = tokens.shape
@@ -808,24 +808,24 @@ def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entro
             raise ValueError("tokens: [...] or [..., T] for logits [..., V]")
         tokens_ptr = _i32(tokens, given, "tokens")
         if logprobs is None:
-            logprobs = logits.new_empty(given, dtype=_F32)
+            logprobs = torch.empty_like(tokens, dtype=_F32)
             lp_ptr = logprobs.data_ptr()
         else:
             lp_ptr = _given(logprobs, given, _F32, "logprobs")
     if entropy is None:
-        entropy = logits.new_empty(rows, dtype=_F32)
+        entropy = torch.empty_strided(rows, (N, 1) if len(rows) == 2 else (1,), dtype=_F32, device=logits.device)
         h_ptr = entropy.data_ptr()
     else:
         h_ptr = _given(entropy, rows, _F32, "entropy")
     if top_k > 0:
-        top = rows + (top_k,)
+        top, steps = rows + (top_k,), (N * top_k, top_k, 1) if len(rows) == 2 else (top_k, 1)
         if top_logprobs is None:
-            top_logprobs = logits.new_empty(top, dtype=_F32)
+            top_logprobs = torch.empty_strided(top, steps, dtype=_F32, device=logits.device)
             top_lp_ptr = top_logprobs.data_ptr()
         else:
             top_lp_ptr = _given(top_logprobs, top, _F32, "top_logprobs")
         if top_tokens is None:
-            top_tokens = logits.new_empty(top, dtype=_I32)
+            top_tokens = torch.empty_strided(top, steps, dtype=_I32, device=logits.device)
             top_ptr = top_tokens.data_ptr()
         else:
             top_ptr = _given(top_tokens, top, _I32, "top_tokens")
