@@ -25,6 +25,17 @@
 // tile, which comes after that reading.
 // P is rounded to bf16 (half a step, 2^-8 of each weight); in sequences of fewer than kShortRow cached tokens, where
 // such errors do not average out, its remainders go through a second P.V (2^-16). Maxima, sums and O are float32.
+//
+// Two shapes of CTA, by the rows of a KV head:
+// * NQ = 1 (up to 128): two CTAs per SM, whose copies together keep up with HBM, which bounds it: 64 sequences of 500 to 8000
+//   tokens with 16 nodes of 32 / 8 heads (1.15 GB) 197 us the step, 5.8 TB/s; under a profiler 16 of them read 1.00 times their
+//   bytes, tensor pipe 31 % busy.
+// * NQ = 2 (more): one CTA per SM, K and V serve 256 rows, key tiles of 128. Bound by what one CTA's copies bring in boxes of
+//   one block (16 tokens: 4.7 TB/s, 32 tokens: 5.6) and by its softmax chain: 1.76 us per key tile at best, of which the MMAs
+//   are 1.07. One user's 131072 tokens with 64 nodes 118 us, 1.16 PFLOP/s over the whole step (142 with NQ = 1); 32
+//   sequences with up to 60 nodes 156 us.
+// Few keys are latency: one user's 4000 tokens 16 us, of which the queries are there after 5.7, a CTA's four
+// tiles take 3.3, its partial rows 1.6 and the merge of 16 partials 4.
 #pragma once
 
 #include "shared_prefix.cuh"
@@ -81,7 +92,8 @@ struct Cfg {
   static constexpr int kOffUnits = kOffStart + 160;          // Units, one per softmax warp
   static constexpr int kOffTmemSlot = kOffUnits + kWarps * 48;
   static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
-  // + producer warp + MMA warp; NQ 2: and two idle ones, so that a whole warpgroup gives registers to the softmax
+  // + producer warp + MMA warp; NQ 2: and two idle ones, so that a whole warpgroup gives registers to the softmax (which spilled
+  // some without: 5 % of the step)
   static constexpr int kThreads = 32 * kWarps + (NQ == 2 ? 128 : 64);
   static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's
   static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
