@@ -475,7 +475,7 @@ RRA_API int rra_tree_append(const void* q, const void* k_new, const void* v_new,
 
 /* The attention of the nodes over a cache that holds them already. The keys of the whole batch are cut into `num_splits`
  * runs of equal length (0: chosen by the library, fewer where there are too few keys); the workspace of rra_tree_plan's bytes (may be NULL when
- * that is 0) needs no filling and holds nothing between calls. Softmax weights enter P.V as bf16, those of sequences of fewer
+ * that is 0) needs no filling and holds nothing between calls; calls that share one must not overlap on the GPU. Softmax weights enter P.V as bf16, those of sequences of fewer
  * than 256 cached tokens as two bf16 parts (2^-16); maxima, sums and partial outputs are float32. `out` must not lie over
  * q_rot. scale as in rra_decode_attn_contig. */
 RRA_API int rra_tree_attn(const void* q_rot, const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -539,7 +539,7 @@ RRA_API int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents, c
  *   entropy       float32 [B, N], may be NULL
  *   top_logprobs, top_tokens  float32 and int32 [B, N, top_k], top_k 0..32 and at most V (NULL for 0)
  * Sums are float32 over parts of a row of a few hundred to a few thousand values, joined in a fixed order. V is at most 2^30. No
- * output may lie over another one or over the tokens (RRA_EINVAL), nor over the logits. */
+ * output may lie over another one, over the tokens or over the span of the logits (RRA_EINVAL). */
 RRA_API int rra_token_logprobs(const void* logits, int64_t stride_b, int64_t stride_t, const int32_t* tokens, int T,
                                float* logprobs, float* entropy, int top_k, float* top_logprobs, int32_t* top_tokens,
                                int B, int N, int V, rra_dtype dt, int32_t* err_flag, void* stream);

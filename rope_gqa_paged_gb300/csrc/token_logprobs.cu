@@ -709,15 +709,17 @@ extern "C" int rra_token_logprobs(const void* logits, int64_t stride_b, int64_t 
   if (!logits || (T > 0 && (!tokens || !logprobs)) || (top_k > 0 && (!top_logprobs || !top_tokens))) return RRA_EINVAL;
   if (reinterpret_cast<uintptr_t>(logits) & (dt == RRA_BF16 ? 1 : 3)) return RRA_EINVAL;
   if (stride_b < 0 || stride_t < 0) return RRA_EINVAL;
-  {  // an output over another one or over the tokens: some row would read what another row wrote
+  {  // an output over another one, over the tokens or over the logits: some row would read what another row wrote
     struct Range {
       const void* p;
       size_t n;
     };
     const size_t rows = size_t(B) * N * 4;
-    const Range all[] = {{logprobs, rows * T}, {entropy, rows}, {top_logprobs, rows * top_k}, {top_tokens, rows * top_k}, {tokens, rows * T}};
+    const size_t es = dt == RRA_BF16 ? 2 : 4, span = (size_t(B - 1) * stride_b + size_t(N - 1) * stride_t + V) * es;
+    const Range all[] = {{logprobs, rows * T}, {entropy, rows}, {top_logprobs, rows * top_k}, {top_tokens, rows * top_k}, {tokens, rows * T},
+                         {logits, span}};
     for (int i = 0; i < 4; ++i)
-      for (int j = i + 1; j < 5; ++j) {
+      for (int j = i + 1; j < 6; ++j) {
         const uintptr_t x = reinterpret_cast<uintptr_t>(all[i].p), y = reinterpret_cast<uintptr_t>(all[j].p);
         if (x != 0 && y != 0 && all[i].n > 0 && all[j].n > 0 && x < y + all[j].n && y < x + all[i].n) return RRA_EINVAL;
       }

@@ -104,6 +104,21 @@ struct Cfg {
   static_assert(kThreads <= 32 * 32, "the scan's warps");
 };
 
+// 32 bytes from L2. A load instruction takes a clock per line that its lanes touch, so rows of 256 bytes, one per lane, come in
+// half the time of 16-byte loads (which tensors that start at an odd multiple of 16 bytes need).
+__device__ __forceinline__ void ld_32_bytes(const uint4* p, uint32_t* r, bool aligned32) {
+  if (!aligned32) {
+    const uint4 x = __ldcg(p), y = __ldcg(p + 1);
+    r[0] = x.x, r[1] = x.y, r[2] = x.z, r[3] = x.w;
+    r[4] = y.x, r[5] = y.y, r[6] = y.z, r[7] = y.w;
+    return;
+  }
+  asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+
 // Sequence b: cached tokens, nodes, key tiles. Refused: no tiles, and nothing of it is written.
 struct Seq {
   int p, n, tiles;
@@ -510,8 +525,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     auto load_q = [&]() {  // the unit's query rows
       const int live = u.seq.n * a.n_rep;
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q));
-      uint4 qv[D / 8];
       if constexpr (NQ == 2) {
+        uint4 qv[D / 8];
         // Into the Q tile (K-major, 128-byte swizzle): this warp's rows, 16 lanes a row (8 at head dim 64), so that loads are
         // whole lines. (A row per thread: one user's 131072 tokens 1.3 us longer.)
         constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;  // lanes per row, rows per load
@@ -532,17 +547,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       } else {
         // Into Tensor Memory, a row per lane: dims (2c, 2c + 1) in column kColQ + c. (By lines and through shared
         // memory: 2 us longer.)
-        const bool real = row < live;
         const uint4* src = q + out_row_of(u.b, u.g) * (D / 8);
+        const bool aligned32 = (reinterpret_cast<uintptr_t>(a.q) & 31) == 0;
+        uint32_t qw[D / 2] = {};
+        if (row < live) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) qv[c] = real ? __ldcg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t qw[D / 2];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          qw[4 * c] = qv[c].x;
-          qw[4 * c + 1] = qv[c].y;
-          qw[4 * c + 2] = qv[c].z;
-          qw[4 * c + 3] = qv[c].w;
+          for (int c = 0; c < D / 16; ++c) ld_32_bytes(src + 2 * c, qw + 8 * c, aligned32);
         }
         st_cols<D / 2>(tmem + lane_base + C::kColQ, qw);
         tc::tmem_wait_st();

@@ -189,7 +189,8 @@ def test_logprobs_refusals(rra):
                    (dict(logprobs=None), RRA_EINVAL), (dict(top=None), RRA_EINVAL), (dict(top_lp=None), RRA_EINVAL),
                    (dict(logits=LP_AT["logits"] + 1), RRA_EINVAL), (dict(logits=LP_AT["logits"] + 2, dt=0), RRA_EINVAL),
                    (dict(sb=-1), RRA_EINVAL), (dict(st=-5), RRA_EINVAL), (dict(entropy=LP_AT["tokens"] + 4), RRA_EINVAL),
-                   (dict(top=LP_AT["top_lp"] + 5 * rows - 4), RRA_EINVAL), (dict(logprobs=LP_AT["entropy"]), RRA_EINVAL)):
+                   (dict(top=LP_AT["top_lp"] + 5 * rows - 4), RRA_EINVAL), (dict(logprobs=LP_AT["entropy"]), RRA_EINVAL),
+                   (dict(entropy=LP_AT["logits"] + 2 * (3 * 16000 + 16 * 1000) - 4), RRA_EINVAL)):
         assert _logprobs(rra, **kw) == st, kw
     assert _logprobs(rra, B=0) == RRA_OK
 

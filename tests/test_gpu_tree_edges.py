@@ -146,3 +146,21 @@ def test_steps_among_other_kernels(R):
         assert torch.equal(step.out, want) and step.error_bits() == 0
     for x, y in zip(got[1:], lp[1:]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("N", [20, 50])
+def test_tensors_at_odd_multiples_of_16_bytes(R, N):
+    c = Case([300, 77], N, 8, 2, 128, 16, seed=7)
+
+    def moved(x):
+        y = torch.empty(x.numel() + 8, dtype=x.dtype, device=DEV)[8:].reshape(x.shape)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        return y
+
+    c.q, c.k, c.v, c.k_new, c.v_new = (moved(x) for x in (c.q, c.k, c.v, c.k_new, c.v_new))
+    out = moved(torch.full_like(c.q, NAN))
+    check(c, c.attend(R, out=out)[0], *c.expect())
+    q_rot = moved(torch.zeros_like(c.q))
+    R.rra_tree_step(c.q, c.k_new, c.v_new, c.positions, c.parents, q_rot, c.k, c.v, out, c.table, workspace=c.workspace(R))
+    check(c, out, *c.expect(q_rot))
