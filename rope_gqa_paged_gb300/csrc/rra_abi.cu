@@ -417,6 +417,8 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   if (max_tokens > (int64_t(1) << 30) || Hkv > 65535 || rows > 65535 || int64_t(B) * Hkv > INT32_MAX) return RRA_ERANGE;
   p->rows = static_cast<int>(rows);
   p->capacity = max_tokens;
+  // Two row tiles per CTA as soon as one does not hold the rows (32 trees of up to 240 rows 157 us, 174 with one each, whose CTAs
+  // read the keys twice; 256 rows over 131072 tokens 118 and 142), not before (64 rows: 200 us with one, 291 with two).
   p->nq = rows > rra::kTreeRows ? 2 : 1;
   p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
   const int tile = rra::tree_tile(D, p->nq);
@@ -427,7 +429,7 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   } else {
     const int sms = sm_count() > 0 ? sm_count() : 152;  // (without a device: a GB300's)
     p->ranges = std::max(1, (p->nq == 2 ? 1 : 2) * sms / p->row_ctas);
-    p->min_tiles = 256 / tile;
+    p->min_tiles = 256 / tile;  // (one user's 4000 tokens 15.7 us; runs of 192 or 384 tokens 17.3, of 512 18.4)
   }
   p->ranges = static_cast<int>(std::min<int64_t>(p->ranges, std::max<int64_t>({1, (tiles + p->min_tiles - 1) / p->min_tiles, int64_t(B) * Hkv})));
   return RRA_OK;
@@ -1676,6 +1678,8 @@ static int tree_attn_launch(const void* q_rot, const void* k_cache, const void* 
   a.row_ctas = p.row_ctas;
   a.ranges = p.ranges;
   a.min_tiles = p.min_tiles;
+  // 64 ragged sequences of 16 nodes / 32 trees of up to 60: 213 / 176 us with 0 and 0, 207 / 160 with 1 and 2, 204 / 157 with 2
+  // and 3, 200 / 156 with 3 and 4, 200 / 158 with 4 and 5, 200 / 159 with 8 and 8
   a.unit_tiles = p.nq == 2 ? 4 : 3;
   if (p.ranges > 1) {
     uint8_t* base = static_cast<uint8_t*>(workspace);

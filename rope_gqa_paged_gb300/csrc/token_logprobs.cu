@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
   part.per_entry = (batches + kEntries - 1) / kEntries;
   part.single = -1;
   part.in = batches <= kRing ? reinterpret_cast<const uint4*>(smem) : vec + part.v0;
-  const bool ringed = batches > 1;  // (one batch is loaded as it is: the ring's barriers would only delay it)
+  const bool ringed = batches > 1;  // (one batch is loaded as it is: 4000 x 1000 bf16 37 us, 42 through the ring)
   __syncthreads();
   if (warp == kWarps) {  // the warp that feeds the ring: one copy per batch
     if (ringed && lane == 0) {
@@ -739,9 +739,15 @@ extern "C" int rra_token_logprobs(const void* logits, int64_t stride_b, int64_t 
   a.T = T;
   a.top_k = top_k;
   a.err = err_flag;
-  const int64_t sms = std::max(1, rra::current_sm_count());
-  int clusters = a.rows * rra::kMaxCluster <= sms ? rra::kMaxCluster : 8;
-  while (clusters > 1 && int64_t(clusters) * a.rows > rra::kCtasPerSm * sms) clusters /= 2;
+  // CTAs per row: the most (a power of two up to 16) that leave no SM more than two (64 x 128000 float32 14.7 us with 4,
+  // 16.9 with 8, 17.3 with 2; 256 x 128256 bf16 21.2 with 1, 22.2 with 2; 1024 x 128000 bf16 51.5 with 1, 66 with 2, 79 with 4: clusters
+  // wait for places side by side, and every CTA looks twice), and no more than one where their parts are short (32 x
+  // 32000 bf16 6.5 us with 4, 8.7 with 8; 16 x 128000 bf16 7.7 with 16, 9.6 with 8; 1 x 128000 6.1 with 16, 8.3 with 8).
+  const int64_t sms = std::max(1, rra::current_sm_count()), vecs = V / (dt == RRA_BF16 ? 8 : 4);
+  int clusters = rra::kMaxCluster;
+  while (clusters > 1 && (a.rows * clusters > 2 * sms ||
+                          (a.rows * clusters > sms && vecs / clusters < 3 * rra::kThreads)))
+    clusters /= 2;
   const cudaError_t e = dt == RRA_BF16 ? rra::launch_logprobs<__nv_bfloat16>(a, clusters, static_cast<cudaStream_t>(stream))
                                        : rra::launch_logprobs<float>(a, clusters, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) return RRA_OK;

@@ -38,6 +38,8 @@
 // tiles take 3.3, its partial rows 1.6 and the merge of 16 partials 4.
 #pragma once
 
+#include <atomic>
+
 #include "shared_prefix.cuh"
 
 namespace rra {
@@ -914,6 +916,16 @@ cudaError_t launch_attn(const TreeArgs& a, const CUtensorMap& km, const CUtensor
   auto kern = tree_attn_kernel<D, NQ, PAGED>;
   cudaError_t e = ensure_smem(kern, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
+  if constexpr (NQ == 2) {  // a block that asks for more registers than it was launched with would wait for them without end
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes attr{};
+      e = cudaFuncGetAttributes(&attr, kern);
+      if (e != cudaSuccess) return e;
+      regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) * C::kThreads < 256 * C::kSoftmaxRegs + 128 * C::kOtherRegs) return cudaErrorInvalidKernelImage;
+  }
   e = launch_pdl(kern, dim3(static_cast<unsigned>(a.ranges) * a.row_ctas), dim3(C::kThreads), C::kSmemBytes, st, km, vm, a);
   if (e != cudaSuccess || a.ranges == 1) return e;
   // partials of a cut unit: about ranges / units, two or three where there are more units
