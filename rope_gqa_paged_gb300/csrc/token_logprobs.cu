@@ -297,7 +297,7 @@ __device__ __noinline__ void top_slowly(const Part<T> part, int k, Shared& sh) {
   }
 }
 
-// A bound that at least k of the values that the threads hold (0: none) reach, 0 if there are not k: the k-th largest
+// A bound that at least k of the values that the threads hold (0: none) reach, sh.bound as it was if there are not k: the k-th largest
 // of the maxima of groups of four threads. (The k-th largest of all is no smaller; of values in no order about
 // 64 (1/64 + 1/63 + ... , k terms) reach it: 24 for k = 20.) Every thread ranks one maximum against a quarter of the
 // others.
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) token_logprobs_kern
       mine_of[i] = c < C && at - c * places < sh.counts[c] ? all[at] : 0;
       best = max(best, static_cast<uint32_t>(mine_of[i] >> 32));
     }
-    const uint32_t bound32 = common_bound(best, k, sh);
+    const uint32_t bound32 = common_bound(best, k, sh);  // (where too few threads have keys, this CTA's own stands: a lower one)
 #pragma unroll
     for (int i = 0; i < kMaxFound / kThreads; ++i)
       if (mine_of[i] != 0 && static_cast<uint32_t>(mine_of[i] >> 32) >= bound32) list[atomicAdd(&sh.kept, 1)] = mine_of[i];

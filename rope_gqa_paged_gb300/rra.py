@@ -710,31 +710,40 @@ def _cache_pointers(caches, shape, dtype, device: int):
     return (_vp * len(caches))(*[c.data_ptr() for c in caches])
 
 
+def _stacked_pointers(caches, shape, dtype, device: int):
+    """The device pointers of the layers of one tensor [layers, ...]."""
+    if caches.shape != shape or caches.dtype != dtype or caches.get_device() != device or not caches.is_contiguous():
+        raise ValueError("the layers' caches: contiguous tensors alike, on the tokens' device")
+    base, step = caches.data_ptr(), caches.stride(0) * caches.element_size()
+    return (_vp * shape[0])(*range(base, base + step * shape[0], step))
+
+
 def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches, block_table=None, tree_lens=None,
                   tokens_out=None, n_kept=None, nodes_out=None, positions_out=None, err_flag=None, stream=None) -> tuple:
     """(tokens [B, N], kept [B], nodes [B, N], next positions [B]): the path of drafted nodes that the target's
     ``choices`` [B, N] follow from node 0, then -1; its keys and values move together in the caches.
 
-    k_caches / v_caches: the caches of every layer (lists of tensors alike, or one tensor each), bf16 or fp32,
-    contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
+    k_caches / v_caches: the caches of every layer (lists of tensors alike, one tensor each, or one that holds the layers'
+    [layers, ...]: the cheapest call), bf16 or fp32, contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
     Outputs are made where they are not given.
     """
     ids = draft_tokens.shape
     if len(ids) != 2:
         raise ValueError("draft_tokens: [B, N]")
     B, N = ids
-    if isinstance(k_caches, torch.Tensor):
+    if isinstance(k_caches, torch.Tensor) and k_caches.dim() == 4:
         k_caches = (k_caches,)
-    if isinstance(v_caches, torch.Tensor):
+    if isinstance(v_caches, torch.Tensor) and v_caches.dim() == 4:
         v_caches = (v_caches,)
-    layers = len(k_caches)
+    layers, device = len(k_caches), draft_tokens.get_device()
     if layers == 0 or len(v_caches) != layers:
         raise ValueError("k_caches, v_caches: the caches of each layer")
     k0 = k_caches[0]
-    cache = k0.shape
-    code, device = _dtype_code(k0), draft_tokens.get_device()
-    k_ptrs = _cache_pointers(k_caches, cache, k0.dtype, device)
-    v_ptrs = _cache_pointers(v_caches, cache, k0.dtype, device)
+    cache, dtype = k0.shape, k0.dtype
+    code = _dtype_code(k0)
+    k_ptrs, v_ptrs = (
+        _stacked_pointers(c, (layers, *cache), dtype, device) if isinstance(c, torch.Tensor) else
+        _cache_pointers(c, cache, dtype, device) for c in (k_caches, v_caches))
     if len(cache) != 4 or (block_table is None and cache[0] != B):
         raise ValueError("caches: [B, Hkv, max_len, D], or [num_blocks, block_size, Hkv, D] with a block table")
     if block_table is not None and (block_table.dtype != _I32 or block_table.dim() != 2 or block_table.shape[0] != B):

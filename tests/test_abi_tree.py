@@ -202,7 +202,8 @@ def test_binding_refusals_of_the_others(rra):
             rra.rra_token_logprobs(**{"tokens": tok, **kw})
     ids, pos, k = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 8, 64)
     for kw in (dict(k_caches=[]), dict(v_caches=[k, k]), dict(k_caches=[k[:1]]), dict(choices=ids.long()),
-               dict(v_caches=[k.bfloat16()]), dict(block_table=ids.long()), dict()):
+               dict(v_caches=[k.bfloat16()]), dict(block_table=ids.long()), dict(k_caches=k[None, None]),
+               dict(k_caches=k[None].expand(2, *k.shape), v_caches=[k, k]), dict(k_caches=k[None], v_caches=k[None, :1]), dict()):
         a = dict(draft_tokens=ids, parents=ids, choices=ids, positions=pos, k_caches=[k], v_caches=[k])
         a.update(kw)
         with pytest.raises(ValueError):

@@ -130,6 +130,20 @@ def test_many_layers_and_a_column_of_choices(R):
     check(R, one, choices=one.choices.to(DEV).expand(2, 1))
 
 
+def test_layers_in_one_tensor(R):
+    c = Keep([40, 3, 9], 20, 2, 64, 16, 5, seed=6, vocab=3)
+    a = c.args()
+    stacked = [torch.stack(a["k_caches"]), torch.stack(a["v_caches"])]
+    a["k_caches"], a["v_caches"] = stacked
+    R.rra_tree_keep(**a)
+    for got, want in zip(list(stacked[0]) + list(stacked[1]), c.expect()[1]):
+        assert torch.equal(got.cpu(), want)
+    mixed = c.args()
+    mixed["k_caches"] = torch.stack(mixed["k_caches"])
+    R.rra_tree_keep(**mixed)
+    assert torch.equal(mixed["k_caches"], stacked[0]) and all(torch.equal(x, y) for x, y in zip(mixed["v_caches"], stacked[1]))
+
+
 def test_choices_that_are_no_token(R):
     c = Keep([5], 4, 1, 64, 0, 1)
     c.tokens[:] = -1
