@@ -417,13 +417,13 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   if (max_tokens > (int64_t(1) << 30) || Hkv > 65535 || rows > 65535 || int64_t(B) * Hkv > INT32_MAX) return RRA_ERANGE;
   p->rows = static_cast<int>(rows);
   p->capacity = max_tokens;
-  // Two row tiles per CTA as soon as one does not hold the rows (32 trees of up to 240 rows 157 us, 174 with one each, whose CTAs
-  // read the keys twice; 256 rows over 131072 tokens 118 and 142), not before (64 rows: 200 us with one, 291 with two).
+  // Two row tiles per CTA as soon as one does not hold the rows (32 trees of up to 240 rows 145 us, 174 with one each, whose CTAs
+  // read the keys twice; 256 rows over 131072 tokens 113 and 142), not before (64 rows: 200 us with one, 291 with two).
   p->nq = rows > rra::kTreeRows ? 2 : 1;
   p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
   const int tile = rra::tree_tile(D, p->nq);
   const int64_t tiles = int64_t(B) * Hkv * ((max_tokens + tile - 1) / tile);
-  if (tiles + int64_t(B) * Hkv * 4 > INT32_MAX) return RRA_ERANGE;
+  if (tiles + int64_t(B) * Hkv * 5 > INT32_MAX) return RRA_ERANGE;  // (with a unit's own places)
   if (requested > 0) {
     p->ranges = std::min(requested, rra::kMaxSplits);
   } else {
@@ -1678,9 +1678,10 @@ static int tree_attn_launch(const void* q_rot, const void* k_cache, const void* 
   a.row_ctas = p.row_ctas;
   a.ranges = p.ranges;
   a.min_tiles = p.min_tiles;
-  // 64 ragged sequences of 16 nodes / 32 trees of up to 60: 213 / 176 us with 0 and 0, 207 / 160 with 1 and 2, 204 / 157 with 2
-  // and 3, 200 / 156 with 3 and 4, 200 / 158 with 4 and 5, 200 / 159 with 8 and 8
-  a.unit_tiles = p.nq == 2 ? 4 : 3;
+  // One row tile, 64 ragged sequences of 16 nodes: 213 us with 0, 207 with 1, 204 with 2, 200 with 3, 4 and 8. Two, 16 trees of 64
+  // nodes over 2000 to 8000 tokens of 64 heads: 168 us with 3, 165.5 with 4, 163.5 with 5, 163 with 6 (32 trees of up to
+  // 60: 149, 145, 145, 146).
+  a.unit_tiles = p.nq == 2 ? 5 : 3;
   if (p.ranges > 1) {
     uint8_t* base = static_cast<uint8_t*>(workspace);
     a.ws_o = reinterpret_cast<float*>(base);

@@ -15,8 +15,8 @@
 // lengths for itself. A unit that lies wholly in one range is written to the output; the parts of a cut one leave
 // (o, m, l) for tree_merge_kernel. Those are the first and the last unit of a range at most.
 //
-// In a CTA the roles run through the same list of units: a producer warp (K and V tiles by TMA into a ring that goes
-// on over unit borders), an MMA lane and a softmax warpgroup for each row tile. For row tile k and key tile j
+// In a CTA the roles run through the same list of units: one or two producer warps (K and V tiles by TMA into a ring that
+// goes on over unit borders), an MMA lane and a softmax warpgroup for each row tile. For row tile k and key tile j
 //   S_k = Q_k K_j^T   D / 16 MMAs (M 128, N kTile, K 16) into Tensor Memory
 //   softmax           one row per thread; running max, moved only when it grows by more than 2^8
 //   O_k += P V_j      kTile / 16 MMAs, P (bf16) the A operand from Tensor Memory over the S columns
@@ -31,9 +31,10 @@
 //   tokens with 16 nodes of 32 / 8 heads (1.15 GB) 197 us the step, 5.8 TB/s; under a profiler 16 of them read 1.00 times their
 //   bytes, tensor pipe 31 % busy.
 // * NQ = 2 (more): one CTA per SM, K and V serve 256 rows, key tiles of 128. Bound by what one CTA's copies bring in boxes of
-//   one block (16 tokens: 4.7 TB/s, 32 tokens: 5.6) and by its softmax chain: 1.76 us per key tile at best, of which the MMAs
-//   are 1.07. One user's 131072 tokens with 64 nodes 118 us, 1.16 PFLOP/s over the whole step (142 with NQ = 1); 32
-//   sequences with up to 60 nodes 156 us.
+//   one block and by its softmax chain: some 1.7 us per key tile, of which the MMAs are 1.07. K and V have a producer warp each: one
+//   warp's copies bring 4.7 TB/s in blocks of 16 tokens. One user's 131072 tokens with 64 nodes 113 us (118 with one
+//   producer), 1.2 PFLOP/s over the whole step; 32 sequences with up to 60 nodes 145 us (157). (V through cp.async by two warps
+//   of its own: 135 and 170.)
 // Few keys are latency: one user's 4000 tokens 16 us, of which the queries are there after 5.7, a CTA's four
 // tiles take 3.3, its partial rows 1.6 and the merge of 16 partials 4.
 #pragma once
@@ -94,8 +95,8 @@ struct Cfg {
   static constexpr int kOffUnits = kOffStart + 160;          // Units, one per softmax warp
   static constexpr int kOffTmemSlot = kOffUnits + kWarps * 48;
   static constexpr int kSmemBytes = 1024 + kOffTmemSlot + 16;
-  // + producer warp + MMA warp; NQ 2: and two idle ones, so that a whole warpgroup gives registers to the softmax (which spilled
-  // some without: 5 % of the step)
+  // + producer warp + MMA warp; NQ 2: and the producer of V and an idle one, a whole warpgroup, which gives registers to the
+  // softmax (which spilled some without: 5 % of the step)
   static constexpr int kThreads = 32 * kWarps + (NQ == 2 ? 128 : 64);
   static constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;  // 256 x 216 + 128 x 72 = 384 x 168, the launch's
   static constexpr int kCtasPerSm = NQ == 2 ? 1 : 2;
@@ -351,8 +352,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
    Units u(*start);
    Raw ahead = raw_sequence(a, min(u.b + 1, a.B - 1));
-   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------------ producer
+   if (warp == kProducerWarp || (NQ == 2 && warp == kMmaWarp + 1)) {
+    // ------------------------------------------------------------------ producer (NQ 2: one for K, one for V)
+    constexpr int kCopied = NQ == 2 ? 1 : 2;
+    const int kv0 = warp == kProducerWarp ? 0 : 1;
+    const bool first_producer = warp == kProducerWarp;
     if (lane == 0) {
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
@@ -360,11 +364,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
     const int log2_bs = a.log2_bs, bs = 1 << log2_bs;
     const int box = PAGED ? min(bs, kTile) : kTile;  // rows per TMA box, as the tensor maps were encoded
     bool ok = true, waited = !a.after_append;
-    uint32_t issued = 0;
+    uint32_t tiles = 0;  // of the CTA so far
     int4 h = make_int4(0, 0, 0, 0);
     while (ok && u.next(a, kTile, first_row, ahead)) {
       const int L = u.seq.p + u.seq.n;
-      if (first_row == 0 && lane == 0 && a.headers != nullptr) {
+      if (first_producer && first_row == 0 && lane == 0 && a.headers != nullptr) {
         // a unit that starts here and goes on in later ranges (it is this one's last) is merged for this header
         h = make_int4(0, 0, 0, 0);
         if (u.j0 == 0 && !u.whole()) {
@@ -393,19 +397,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
           waited = true;
         }
         const int rows8 = PAGED ? (id << (log2_bs - 3)) + (((tile0 + lane * box) & (bs - 1)) >> 3) : 0;
-        for (int kv = 0; kv < 2; ++kv, ++issued) {
-          const uint32_t s = slot_of(issued);
+        for (int kv = kv0; ok && kv < kv0 + kCopied; ++kv) {
+          const uint32_t r = 2 * tiles + kv, s = slot_of(r);
           int good = 1;
           if (lane == 0) {
-            if (issued >= kRing && !mbar_wait(&ring_empty[s], phase_of(issued) ^ 1u))
+            if (r >= kRing && !mbar_wait(&ring_empty[s], phase_of(r) ^ 1u))
               good = 0;
             else
               mbar_arrive_expect_tx(&ring_full[s], static_cast<uint32_t>(nbox * box * 128 * C::kHalves));
           }
-          if (!__shfl_sync(0xffffffffu, good, 0)) {
-            ok = false;
-            break;
-          }
+          ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+          if (!ok) break;
           uint8_t* dst = smem + C::kOffRing + s * C::kTileBytes;
           const CUtensorMap* map = kv ? &v_map : &k_map;
           if constexpr (PAGED) {
@@ -416,14 +418,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
           }
           __syncwarp();
         }
+        if (ok) ++tiles;
       }
     }
-    if (first_row == 0 && lane == 0 && a.headers != nullptr && !a.headers_by_unit) a.headers[range] = h;
-    pad_rows(a, D, lane, 32);
+    if (first_producer) {
+      if (first_row == 0 && lane == 0 && a.headers != nullptr && !a.headers_by_unit) a.headers[range] = h;
+      pad_rows(a, D, lane, 32);
+    }
     if (lane == 0) {
       if (!ok) flag_error(a.err, RRA_ERR_TIMEOUT);
       // no copy may still be landing when the CTA exits
-      for (uint32_t r = issued > kRing ? issued - kRing : 0; r < issued; ++r) mbar_wait(&ring_full[slot_of(r)], phase_of(r));
+      const uint32_t issued = 2 * tiles;
+      for (uint32_t r = issued > kRing ? issued - kRing : 0; r < issued; ++r)
+        if (kCopied == 2 || (r & 1u) == static_cast<uint32_t>(kv0)) mbar_wait(&ring_full[slot_of(r)], phase_of(r));
+      if (!ok && kCopied == 2) mbar_wait(&ring_full[slot_of(issued)], phase_of(issued));  // (K of the tile whose V found no place)
     }
    } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue (one lane)
