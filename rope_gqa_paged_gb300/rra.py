@@ -164,6 +164,17 @@ def _stream(stream, t: torch.Tensor) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _current(stream, t: torch.Tensor):
+    """A context in which ``stream`` is the current one of tensor ``t``'s device: what a call makes or copies by itself
+    has to be of the stream that its kernel runs on, which alone orders memory that torch hands out again."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, t.device) if handle > 1 else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError("stream: of another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
 def _check(name: str, status: int) -> None:
     if status != 0:
         raise RraError(name, status)
@@ -215,6 +226,9 @@ def rra_status_str(status: int) -> str:
 def rra_rope_cos_sin(positions: torch.Tensor, head_dim: int, rope_base: float = 10000.0, out=None,
                      stream=None) -> torch.Tensor:
     """cos hi, cos lo, sin hi, sin lo of positions[p] * theta_i on the device: float32 [n, 4, head_dim/2]."""
+    if stream is not None and positions.is_cuda:
+        with _current(stream, positions):
+            return rra_rope_cos_sin(positions, head_dim, rope_base, out)
     if positions.dtype != torch.int32 or not positions.is_cuda or not positions.is_contiguous():
         raise ValueError("positions: a contiguous int32 CUDA tensor")
     n = positions.numel()
@@ -548,9 +562,13 @@ def rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs
 
     target_probs [B, gamma + 1, V] and draft_probs [B, gamma, V] (or None: a drafter without
     probabilities) are bf16 or fp32 with a unit last stride; u_accept [B, gamma] and u_sample [B] are
-    uniform random numbers in [0, 1). Outputs are made where they are not given; positions_out may be
-    positions.
+    uniform random numbers in [0, 1). Outputs are made where they are not given (from the memory of the
+    call's stream); positions_out may be positions.
     """
+    if stream is not None and target_probs.is_cuda:
+        with _current(stream, target_probs):
+            return rra_accept_draft(target_probs, draft_tokens, u_accept, u_sample, draft_probs, draft_lens, positions,
+                                    tokens_out, n_accepted, positions_out, err_flag)
     ids = draft_tokens.shape
     B, gamma = ids
     V, dt = target_probs.shape[-1], target_probs.dtype
@@ -725,8 +743,13 @@ def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches,
 
     k_caches / v_caches: the caches of every layer (lists of tensors alike, one tensor each, or one that holds the layers'
     [layers, ...]: the cheapest call), bf16 or fp32, contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
-    Outputs are made where they are not given.
+    Outputs are made where they are not given, and ``choices`` whose rows are not N of its steps apart are copied: both on
+    the call's stream and from its memory.
     """
+    if stream is not None and draft_tokens.is_cuda:
+        with _current(stream, draft_tokens):
+            return rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches, block_table, tree_lens,
+                                 tokens_out, n_kept, nodes_out, positions_out, err_flag)
     ids = draft_tokens.shape
     if len(ids) != 2:
         raise ValueError("draft_tokens: [B, N]")
@@ -792,8 +815,11 @@ def rra_token_logprobs(logits, tokens=None, top_k: int = 0, logprobs=None, entro
 
     ``tokens``: int32, one per row ([...]) or several ([..., T]); -1: no token, 0. The results are float32 and
     int32 tensors of the shapes [...] or [..., T], [...], [..., top_k] and [..., top_k], made where they are not given; without
-    ``tokens`` the first is None, without ``top_k`` the last two are.
+    ``tokens`` the first is None, without ``top_k`` the last two are. What is made comes from the memory of the call's stream.
     """
+    if stream is not None and logits.is_cuda:
+        with _current(stream, logits):
+            return rra_token_logprobs(logits, tokens, top_k, logprobs, entropy, top_logprobs, top_tokens, err_flag)
     shape, strides, dt = logits.shape, logits.stride(), logits.dtype
     rows = shape[:-1]
     if len(shape) == 2:
