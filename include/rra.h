@@ -513,7 +513,9 @@ RRA_API int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_toke
  *   draft_tokens, parents  int32 [B, N]; choices int32 [B, N], consecutive ones choice_stride elements apart (so that one column of
  *                 rra_token_logprobs' top_tokens will do). A choice below 0 matches no child.
  *   k_caches, v_caches  HOST arrays of n_layers (0..128) device pointers: caches of element type dt (bf16 or fp32), all laid
- *                 out alike (paged pools of any power of two, or contiguous) under one block table
+ *                 out alike (paged pools of any power of two, or contiguous) under one block table. A pointer that stands there
+ *                 more than once (layers that share keys or values) is one cache, whose rows move once; caches that overlap
+ *                 otherwise are refused (RRA_EINVAL)
  * tree_lens, positions, parents and their error bits as in rra_tree_append; a sequence with RRA_ERR_POSITION has its path
  * written, positions_out = positions and nothing moved; a row whose slot has a block id outside the pool does not
  * move (RRA_ERR_BLOCK_ID). No output may lie over another one or over an input (RRA_EINVAL). N is 1..128. */

@@ -7,10 +7,12 @@
 //
 // Bound: latency (the walk: loads, then one step of a warp per kept node; the move: loads, then stores) for a few
 // sequences; HBM for many, with each kept row that is not in place read and written once per layer. One CTA per
-// (sequence, layer): it walks for itself, then its threads take 16-byte columns of the kept rows, K's and V's.
+// sequence and pair of caches (a layer's K and V, as a rule): it walks for itself, then its threads take 16-byte columns of the
+// kept rows. Every cache is in one pair, once: two CTAs that move the same rows would read what the other has written.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <functional>
 
 #include "rra_device.cuh"
 #include "rra_internal.h"
@@ -32,19 +34,19 @@ struct KeepArgs {
   const int32_t* block_table;    // nullptr: contiguous caches
   int max_blocks_per_seq, log2_bs, num_blocks, capacity;
   int32_t *tokens_out, *n_kept, *nodes_out, *positions_out;
-  int B, N, layers, Hkv, row_vecs;  // 16-byte vectors of a head's row
+  int B, N, pairs, Hkv, row_vecs;  // pairs of caches; 16-byte vectors of a head's row
   int32_t* err;
-  void* caches[2 * kMaxLayers];  // K and V of every layer
+  void* caches[2 * kMaxLayers];  // different ones; the last one nullptr where their number is odd
 };
 
 __global__ void __launch_bounds__(kThreads) tree_keep_kernel(const __grid_constant__ KeepArgs a) {
   __shared__ int parent[kTreeMaxNodes], token[kTreeMaxNodes], choice[kTreeMaxNodes], path[kTreeMaxNodes];
   __shared__ long long src_row[kTreeMaxNodes], dst_row[kTreeMaxNodes];
   __shared__ int kept_sh, moves_sh;
-  const int b = blockIdx.y, layer = blockIdx.x, t = threadIdx.x, lane = t & 31;
+  const int b = blockIdx.y, pair = blockIdx.x, t = threadIdx.x, lane = t & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const bool scribe = layer == 0;
+  const bool scribe = pair == 0;
   int n = a.lens != nullptr ? a.lens[b] : a.N;
   if (n < 0 || n > a.N) {
     if (scribe && t == 0) flag_error(a.err, RRA_ERR_SEQ_LEN);
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) tree_keep_kernel(const __grid_consta
       a.positions_out[b] = refused ? p : p + kept;
     }
   }
-  if (refused || a.layers == 0) return;
+  if (refused || a.pairs == 0) return;
   // ---- the rows to move (path[i] = i from the start: in place)
   if (t == 0) {
     int first = 0;
@@ -123,11 +125,11 @@ __global__ void __launch_bounds__(kThreads) tree_keep_kernel(const __grid_consta
   }
   __syncthreads();
   const long long head_stride = a.block_table != nullptr ? 1 : a.capacity;
-  const int columns = a.Hkv * a.row_vecs;
-  for (int c = t; c < 2 * columns; c += kThreads) {  // a column of K, then of V: moved by one thread, in order
-    const bool is_v = c >= columns;
-    const int g = (is_v ? c - columns : c) / a.row_vecs, x = (is_v ? c - columns : c) - g * a.row_vecs;
-    uint4* cache = static_cast<uint4*>(a.caches[2 * layer + (is_v ? 1 : 0)]) + x;
+  const int columns = a.Hkv * a.row_vecs, caches = a.caches[2 * pair + 1] != nullptr ? 2 : 1;
+  for (int c = t; c < caches * columns; c += kThreads) {  // a column of one cache, then of the other: moved by one thread, in order
+    const bool second = c >= columns;
+    const int g = (second ? c - columns : c) / a.row_vecs, x = (second ? c - columns : c) - g * a.row_vecs;
+    uint4* cache = static_cast<uint4*>(a.caches[2 * pair + (second ? 1 : 0)]) + x;
     for (int i = first; i < kept; i += kBatch) {
       uint4 v[kBatch];
 #pragma unroll
@@ -182,7 +184,17 @@ extern "C" int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents
     for (const void* c : {k_caches[l], v_caches[l]})
       if (c == nullptr || (reinterpret_cast<uintptr_t>(c) & 15) != 0) return RRA_EINVAL;
   }
-  // every layer's CTA reads the inputs, one of them writes the outputs
+  // Each cache once (layers may share one); others must not meet.
+  std::sort(a.caches, a.caches + 2 * n_layers, std::less<void*>());
+  const int n_caches = static_cast<int>(std::unique(a.caches, a.caches + 2 * n_layers) - a.caches);
+  std::fill(a.caches + n_caches, a.caches + 2 * n_layers, nullptr);
+  const unsigned __int128 all_rows = block_table != nullptr ? static_cast<unsigned __int128>(num_blocks) << log2_bs
+                                                            : static_cast<unsigned __int128>(B) * max_len;
+  const size_t cache_bytes = static_cast<size_t>(
+      std::min<unsigned __int128>(all_rows * Hkv * D * (dt == RRA_BF16 ? 2 : 4), size_t(1) << 62));
+  for (int i = 0; i + 1 < n_caches; ++i)
+    if (meet(a.caches[i], cache_bytes, a.caches[i + 1], cache_bytes)) return RRA_EINVAL;
+  // every pair's CTA reads the inputs, one of them writes the outputs
   const size_t s = size_t(B) * 4, sn = s * N, choice_bytes = ((size_t(B) * N - 1) * choice_stride + 1) * 4;
   const struct {
     const void* p;
@@ -212,11 +224,11 @@ extern "C" int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents
   a.positions_out = positions_out;
   a.B = B;
   a.N = N;
-  a.layers = n_layers;
+  a.pairs = (n_caches + 1) / 2;
   a.Hkv = Hkv;
   a.row_vecs = D * (dt == RRA_BF16 ? 2 : 4) / 16;
   a.err = err_flag;
-  const cudaError_t e = launch_pdl(tree_keep_kernel, dim3(std::max(1, n_layers), B), dim3(kThreads), 0,
+  const cudaError_t e = launch_pdl(tree_keep_kernel, dim3(std::max(1, a.pairs), B), dim3(kThreads), 0,
                                    static_cast<cudaStream_t>(stream), a);
   if (e == cudaSuccess) return RRA_OK;
   record_cuda_error(e, "tree_keep launch");

@@ -742,7 +742,7 @@ def rra_tree_keep(draft_tokens, parents, choices, positions, k_caches, v_caches,
     ``choices`` [B, N] follow from node 0, then -1; its keys and values move together in the caches.
 
     k_caches / v_caches: the caches of every layer (lists of tensors alike, one tensor each, or one that holds the layers'
-    [layers, ...]: the cheapest call), bf16 or fp32, contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
+    [layers, ...]: the cheapest call; a cache that several layers share moves once), bf16 or fp32, contiguous or paged as for the steps. ``choices`` may be a column of ``rra_token_logprobs``' top tokens.
     Outputs are made where they are not given, and ``choices`` whose rows are not N of its steps apart are copied: both on
     the call's stream and from its memory.
     """
