@@ -518,7 +518,8 @@ RRA_API int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_toke
  *                 otherwise are refused (RRA_EINVAL)
  * tree_lens, positions, parents and their error bits as in rra_tree_append; a sequence with RRA_ERR_POSITION has its path
  * written, positions_out = positions and nothing moved; a row whose slot has a block id outside the pool does not
- * move (RRA_ERR_BLOCK_ID). No output may lie over another one or over an input (RRA_EINVAL). N is 1..128. */
+ * move (RRA_ERR_BLOCK_ID). No output may lie over another one or over an input, the block table
+ * among them, and no cache over either (RRA_EINVAL). N is 1..128. */
 RRA_API int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents, const int32_t* choices,
                           int64_t choice_stride, const int32_t* tree_lens, const int32_t* positions,
                           void* const* k_caches, void* const* v_caches, int n_layers, const int32_t* block_table,

@@ -194,18 +194,25 @@ extern "C" int rra_tree_keep(const int32_t* draft_tokens, const int32_t* parents
       std::min<unsigned __int128>(all_rows * Hkv * D * (dt == RRA_BF16 ? 2 : 4), size_t(1) << 62));
   for (int i = 0; i + 1 < n_caches; ++i)
     if (meet(a.caches[i], cache_bytes, a.caches[i + 1], cache_bytes)) return RRA_EINVAL;
-  // every pair's CTA reads the inputs, one of them writes the outputs
+  // Every pair's CTA reads the inputs, one of them writes the outputs, and all write to the caches meanwhile.
   const size_t s = size_t(B) * 4, sn = s * N, choice_bytes = ((size_t(B) * N - 1) * choice_stride + 1) * 4;
   const struct {
     const void* p;
     size_t n;
   } outs[] = {{tokens_out, sn}, {n_kept, s}, {nodes_out, sn}, {positions_out, s}},
-    ins[] = {{draft_tokens, sn}, {parents, sn}, {choices, choice_bytes}, {tree_lens, s}, {positions, s}};
+    ins[] = {{draft_tokens, sn}, {parents, sn}, {choices, choice_bytes}, {tree_lens, s}, {positions, s},
+           {block_table, s * max_blocks_per_seq}};
   for (int i = 0; i < 4; ++i) {
     for (int j = 0; j < i; ++j)
       if (meet(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return RRA_EINVAL;
     for (const auto& in : ins)
       if (meet(outs[i].p, outs[i].n, in.p, in.n)) return RRA_EINVAL;
+  }
+  for (int i = 0; i < n_caches; ++i) {
+    for (const auto& out : outs)
+      if (meet(a.caches[i], cache_bytes, out.p, out.n)) return RRA_EINVAL;
+    for (const auto& in : ins)
+      if (meet(a.caches[i], cache_bytes, in.p, in.n)) return RRA_EINVAL;
   }
   a.tokens = draft_tokens;
   a.parents = parents;

@@ -1,4 +1,4 @@
-"""Which caches rra_tree_keep refuses, on the host (no GPU needed)."""
+"""What rra_tree_keep refuses of caches and of outputs that lie over what it reads, on the host (no GPU needed)."""
 
 import ctypes
 
@@ -51,3 +51,24 @@ def test_caches_of_absurd_sizes(rra):
     kw = dict(nblk=2 ** 31 - 1, bs=1 << 29, mbps=1, B=65535)
     assert keep(rra, [K], [1 << 50], **kw) == RRA_EINVAL
     assert keep(rra, [K], [K], **kw) == RRA_ECUDA
+
+
+OUTPUTS = [("tokens_out", 4 * 16 * 4), ("kept", 4 * 4), ("nodes_out", 4 * 16 * 4), ("next", 4 * 4)]
+
+
+@pytest.mark.parametrize("name,size", OUTPUTS)
+def test_outputs_over_the_table_or_a_cache(rra, name, size):
+    """The first and the last byte of either count; beside them an output may lie."""
+    caches = ([K], [K + POOL])
+    for start, length in ((AT["table"], 4 * 64 * 4), (K, 2 * POOL)):
+        for at in (start, start + length - 4, start - size + 4):
+            assert keep(rra, *caches, **{name: at}) == RRA_EINVAL, at - start
+        for at in (start - size, start + length):
+            assert keep(rra, *caches, **{name: at}) == RRA_ECUDA, at - start
+
+
+@pytest.mark.parametrize("name", ["tokens", "parents", "choices", "lens", "positions", "table"])
+def test_inputs_over_a_cache(rra, name):
+    for cache in (K, K + POOL):
+        assert keep(rra, [K], [K + POOL], **{name: cache + POOL - 4}) == RRA_EINVAL
+    assert keep(rra, [K], [K + POOL], **{name: K + 2 * POOL}) == RRA_ECUDA
