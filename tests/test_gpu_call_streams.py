@@ -4,7 +4,8 @@ nothing of it waits for the current stream. In every test the current stream is 
 import pytest
 import torch
 
-from tests.test_gpu_tree import DEV
+from tests.test_gpu_tree import DEV, Case
+from tests.test_gpu_tree import check as check_tree
 from tests.test_gpu_tree_keep import Keep
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +139,26 @@ def test_captured_on_a_given_stream(R, name):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+def test_tree_attention_and_step(R):
+    c = Case([700, 350], 20, 32, 8, 128, 16, seed=12)
+    want, mag = c.expect()
+    ws, err, out = c.workspace(R), torch.zeros(1, dtype=torch.int32, device=DEV), torch.full_like(c.q, float("nan"))
+    step = R.TreeStep(c.B, c.N, 32, 8, 128, c.k.clone(), c.v.clone(), c.table)
+    first = step(c.q, c.k_new, c.v_new, c.positions, c.parents).clone()
+    step.out.fill_(float("nan"))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    c.attend(R, ws=ws, out=out, err=err, stream=s)
+    torch.cuda.synchronize()
+    out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    busy = Busy()
+    c.attend(R, ws=ws, out=out, err=err, stream=s)
+    step(c.q, c.k_new, c.v_new, c.positions, c.parents, stream=s)
+    s.synchronize()
+    assert busy.still()
+    torch.cuda.synchronize()
+    check_tree(c, out, want, mag)
+    assert torch.equal(step.out, first)
+    assert int(err) == step.error_bits() == 0
