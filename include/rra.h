@@ -512,7 +512,8 @@ RRA_API int rra_tree_plan(int B, int N, int Hq, int Hkv, int D, int64_t max_toke
  *
  *   draft_tokens, parents  int32 [B, N]; choices int32 [B, N], consecutive ones choice_stride elements apart (so that one column of
  *                 rra_token_logprobs' top_tokens will do). A choice below 0 matches no child.
- *   k_caches, v_caches  HOST arrays of n_layers (0..128) device pointers: caches of element type dt (bf16 or fp32), all laid
+ *   k_caches, v_caches  HOST arrays of n_layers (0..128) device pointers: caches of element type dt (bf16, which the tree calls
+ *                 fill; or fp32, of a program that puts its nodes into the fp32 decode calls' caches itself), all laid
  *                 out alike (paged pools of any power of two, or contiguous) under one block table. A pointer that stands there
  *                 more than once (layers that share keys or values) is one cache, whose rows move once; caches that overlap
  *                 otherwise are refused (RRA_EINVAL)

@@ -418,7 +418,7 @@ int make_plan_tree(int B, int N, int Hq, int Hkv, int D, int64_t max_tokens, int
   p->rows = static_cast<int>(rows);
   p->capacity = max_tokens;
   // Two row tiles per CTA as soon as one does not hold the rows (32 trees of up to 240 rows 145 us, 174 with one each, whose CTAs
-  // read the keys twice; 256 rows over 131072 tokens 113 and 142), not before (64 rows: 200 us with one, 291 with two).
+  // read the keys twice; 256 rows over 131000 tokens 113 and 142), not before (64 rows: 200 us with one, 291 with two).
   p->nq = rows > rra::kTreeRows ? 2 : 1;
   p->row_ctas = static_cast<int>((rows + p->nq * rra::kTreeRows - 1) / (p->nq * rra::kTreeRows));
   const int tile = rra::tree_tile(D, p->nq);
@@ -1680,7 +1680,8 @@ static int tree_attn_launch(const void* q_rot, const void* k_cache, const void* 
   a.min_tiles = p.min_tiles;
   // One row tile, 64 ragged sequences of 16 nodes: 213 us with 0, 207 with 1, 204 with 2, 200 with 3, 4 and 8. Two, 16 trees of 64
   // nodes over 2000 to 8000 tokens of 64 heads: 168 us with 3, 165.5 with 4, 163.5 with 5, 163 with 6 (32 trees of up to
-  // 60: 149, 145, 145, 146).
+  // 60: 149, 145, 145, 146). Head dim 64, whose one row tile has key tiles of 128: 21 short sequences of 42 heads 37.7 us with 0, 29.5 with 1,
+  // 28.2 with 2, 27.9 with 3, 29.1 with 5; 32 trees of 32 nodes over 3000 to 6000 tokens 89.7, 89.1, 88.7, 88.3, 89.2.
   a.unit_tiles = p.nq == 2 ? 5 : 3;
   if (p.ranges > 1) {
     uint8_t* base = static_cast<uint8_t*>(workspace);

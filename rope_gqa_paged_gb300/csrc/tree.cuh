@@ -24,17 +24,21 @@
 // Q goes in before O is read, so that its first S runs meanwhile; its first P.V waits for the softmax of its first
 // tile, which comes after that reading.
 // P is rounded to bf16 (half a step, 2^-8 of each weight); in sequences of fewer than kShortRow cached tokens, where
-// such errors do not average out, its remainders go through a second P.V (2^-16). Maxima, sums and O are float32.
+// such errors do not average out, its remainders go through a second P.V (2^-16). Longer ones are within 0.0023 of 64 bits (root
+// mean square, relative), 0.0017 of which is the output's own rounding. A second P.V for them too leaves those 0.0017, and
+// takes 1 % more for 64 ragged sequences of 16 nodes (201 us from 199), 7 % for one user's 4000 tokens (16.8 from 15.8) and at head dim 64 (94
+// from 88), 13 % for 16 x 16 nodes of 32 heads with one KV head (55 from 49), 16 to 21 % with two row tiles (168 from 144, 136 from 113).
+// Maxima, sums and O are float32.
 //
 // Two shapes of CTA, by the rows of a KV head:
 // * NQ = 1 (up to 128): two CTAs per SM, whose copies together keep up with HBM, which bounds it: 64 sequences of 500 to 8000
-//   tokens with 16 nodes of 32 / 8 heads (1.15 GB) 197 us the step, 5.8 TB/s; under a profiler 16 of them read 1.00 times their
-//   bytes, tensor pipe 31 % busy.
-// * NQ = 2 (more): one CTA per SM, K and V serve 256 rows, key tiles of 128. Bound by what one CTA's copies bring in boxes of
-//   one block and by its softmax chain: some 1.7 us per key tile, of which the MMAs are 1.07. K and V have a producer warp each: one
-//   warp's copies bring 4.7 TB/s in blocks of 16 tokens. One user's 131072 tokens with 64 nodes 113 us (118 with one
-//   producer), 1.2 PFLOP/s over the whole step; 32 sequences with up to 60 nodes 145 us (157). (V through cp.async by two warps
-//   of its own: 135 and 170.)
+//   tokens with 16 nodes of 32 / 8 heads (1.15 GB) 199 us the step, 5.8 TB/s; under a profiler 16 of them read 1.00 times their
+//   bytes, tensor pipe 32 % busy.
+// * NQ = 2 (more): one CTA per SM, K and V serve 256 rows, key tiles of 128. No one part bounds it: a CTA's copies (boxes of one
+//   block), its MMAs and its softmax follow one another in part, some 1.7 us per key tile, of which the MMAs are 1.07. One user's 131000
+//   tokens with 64 nodes 113 us, 101 where no tile is copied, 105 without the softmax's arithmetic; 32 sequences with up to 60 nodes 144, 134
+//   and 135; 16 of 64 nodes of 64 heads 163, 155 and 138. K and V have a producer warp each (with one 118 us for the first and 157 for the
+//   second; V through cp.async by two warps of its own: 135 and 170). The first does 1.2 PFLOP/s over its three kernels.
 // Few keys are latency: one user's 4000 tokens 16 us, of which the queries are there after 5.7, a CTA's four
 // tiles take 3.3, its partial rows 1.6 and the merge of 16 partials 4.
 #pragma once
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, PAGED>::kThreads, Cfg<D, NQ, PAGED>
       if constexpr (NQ == 2) {
         uint4 qv[D / 8];
         // Into the Q tile (K-major, 128-byte swizzle): this warp's rows, 16 lanes a row (8 at head dim 64), so that loads are
-        // whole lines. (A row per thread: one user's 131072 tokens 1.3 us longer.)
+        // whole lines. (A row per thread: one user's 131000 tokens 1.3 us longer.)
         constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;  // lanes per row, rows per load
         const int x = lane % kLanes, row0 = first_row + k * kRows + (r & ~31) + lane / kLanes;
         int j = row0 / a.n_rep, i = row0 - j * a.n_rep;
