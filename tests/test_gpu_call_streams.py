@@ -110,16 +110,18 @@ def test_outputs_come_from_the_calls_stream(R, name):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("handle", [0, 1, 2])
 @pytest.mark.parametrize("name", ["keep", "logprobs", "accept", "angles"])
-def test_the_default_stream_by_its_handle(R, name):
-    """Handle 0 is the default stream, whatever the current one is."""
+def test_the_default_streams_by_their_handles(R, name, handle):
+    """Handles 0 and 1 are the default stream, 2 the host thread's, whatever the current one is."""
     call = calls(R)[name]
     want = [x.clone() for x in call(None)]
+    call(handle)   # (memory of that stream is taken at a first call)
     torch.cuda.synchronize()
     with torch.cuda.stream(torch.cuda.Stream()):
         busy = Busy()
-        got = call(0)
-        torch.cuda.default_stream().synchronize()
+        got = call(handle)
+        (torch.cuda.ExternalStream(2) if handle == 2 else torch.cuda.default_stream()).synchronize()
         assert busy.still()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
